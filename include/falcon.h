@@ -372,6 +372,88 @@ int falcon_bwd_chunk_noalloc(int variant, int window, int flags, float beta, con
                              float* dv_out, float* dbeta_t, float* dk_prev, float* dS0,
                              void* stream);
 
+/*
+ * Norms before and after a block.  The sequence entry points take q and k
+ * normalized and head-major [batch, heads, L, d]; a projection gives token-major
+ * rows [batch, L, heads, d], often views of one fused projection.  A token-major
+ * argument has a stride ld (elements) from one token's row of heads * d
+ * consecutive elements to the next, batch after batch: token (b, t) starts at
+ * (b * L + t) * ld.  ld >= heads * d and a multiple of 16 bytes.
+ *
+ * falcon_norm_in - per token and head
+ *   q = q_in / sqrt(|q_in|^2 + eps),  k = k_in / sqrt(|k_in|^2 + eps),  v = v_in
+ *   q_in, k_in, v_in   token-major, dtype; v_in and v may both be NULL
+ *   q, k, v            head-major, dtype, contiguous
+ *   eps                finite, >= 0 (eps = 0 with a zero row gives NaN)
+ * Sums are float32; each output is rounded once.
+ *
+ * falcon_norm_in_bwd - its gradient: with r = 1 / sqrt(|x|^2 + eps), y = r x
+ *   dx = r (dy - y (y . dy)) for q and k,  dv_in = dv
+ *   dq, dk, dv         head-major float32 (as the backward entry points give them)
+ *   dq_in, dk_in, dv_in  token-major, dtype; dv and dv_in may both be NULL
+ *
+ * falcon_norm_out - per token and head, from a sequence entry point's o
+ *   y = residual + scale * act(gate) * weight * o / sqrt(mean(o^2) + eps)
+ *   o                  [batch, heads, L, dv] float32
+ *   weight             [dv] float32
+ *   gate               token-major, dtype, or NULL (act = 1)
+ *   gate_kind          FALCON_GATE_SILU (g / (1 + e^-g)) or FALCON_GATE_SIGMOID
+ *   residual           token-major, dtype, or NULL; may equal y exactly (in place)
+ *   scale              finite
+ *   y                  token-major, dtype
+ *
+ * falcon_norm_out_bwd - its gradients for o, gate and weight (the residual's is
+ * dy itself)
+ *   dy                 token-major, dtype
+ *   dO                 [batch, heads, L, dv] float32
+ *   dgate              token-major, dtype; NULL exactly when gate is
+ *   dweight            [dv] float32, summed in a fixed order
+ *   workspace          falcon_norm_out_bwd_workspace_bytes(...) bytes of device
+ *                      memory, 16-byte aligned
+ *
+ * dk, dv in {16, 32, 64, 128}, bf16 or fp32; batch * L < 2^31.  Outputs overlap no
+ * other argument, except that token-major outputs may interleave (views of one
+ * fused buffer with one ld) and y as above.  Errors as elsewhere.
+ */
+#define FALCON_GATE_SILU 0
+#define FALCON_GATE_SIGMOID 1
+int falcon_norm_in(int batch, int heads, int seqlen, int dk, int dv, int dtype, const void* q_in,
+                   long long ld_q, const void* k_in, long long ld_k, const void* v_in,
+                   long long ld_v, float eps, void* q, void* k, void* v, void* stream);
+int falcon_norm_in_bwd(int batch, int heads, int seqlen, int dk, int dv, int dtype,
+                       const void* q_in, long long ld_q, const void* k_in, long long ld_k,
+                       float eps, const float* dq, const float* dk_, const float* dv_, void* dq_in,
+                       long long ld_dq, void* dk_in, long long ld_dk, void* dv_in,
+                       long long ld_dv, void* stream);
+int falcon_norm_out(int batch, int heads, int seqlen, int dv, int dtype, const float* o,
+                    const float* weight, const void* gate, long long ld_gate, int gate_kind,
+                    const void* residual, long long ld_res, float scale, float eps, void* y,
+                    long long ld_y, void* stream);
+unsigned long long falcon_norm_out_bwd_workspace_bytes(int batch, int seqlen, int dv);
+int falcon_norm_out_bwd(int batch, int heads, int seqlen, int dv, int dtype, const float* o,
+                        const float* weight, const void* gate, long long ld_gate, int gate_kind,
+                        float scale, float eps, const void* dy, long long ld_dy, float* dO,
+                        void* dgate, long long ld_dgate, float* dweight, void* workspace,
+                        unsigned long long workspace_bytes, void* stream);
+
+/*
+ * The gated linear recurrence: the inner-product update with a gate of its own
+ * per (batch, head, token) in place of the decay 1 - eta lambda, and the same
+ * step's key:
+ *   S_t = a_t S_{t-1} + v_t k_t^T,   a_t = exp(log_a_t),   o_t = S_t q_t
+ *   log_a    [batch, heads, L] float32, or NULL (a = 1).  A log decay below
+ *            -1000 counts as -1000 (e^-1000 is 0 in float32), so -inf resets the
+ *            state: a new sequence starts at that token.
+ *
+ * falcon_gated_decode_step - one token for serving: S [nseq, heads, dv, dk]
+ * float32 updated in place, q, k [nseq, heads, dk], v [nseq, heads, dv], log_a
+ * [nseq, heads] or NULL, o [nseq, heads, dv] float32.  No argument may overlap
+ * another.  nseq * heads * dk * dv < 2^34 (FALCON_ERR_UNSUPPORTED from there on).
+ */
+int falcon_gated_decode_step(int nseq, int heads, int dk, int dv, int dtype, float* S,
+                             const void* q, const void* k, const void* v, const float* log_a,
+                             float* o, void* stream);
+
 #ifdef __cplusplus
 }
 #endif

@@ -1,0 +1,137 @@
+"""Refusals of the norms' and the gated recurrence's entry points, before any HIP call
+(fake, never-dereferenced pointers) and in the binding."""
+import os
+
+import pytest
+
+import weight_recurrent_memory_amd as fw
+from weight_recurrent_memory_amd import binding
+
+pytestmark = pytest.mark.cpu
+
+INVALID, UNSUPPORTED = 1, 2
+P = [0x100000000 + 0x10000000 * i for i in range(16)]
+NAN, INF = float("nan"), float("inf")
+
+
+@pytest.fixture(scope="module")
+def lib():
+    if not os.path.exists(binding.library_path()):
+        from weight_recurrent_memory_amd import build_lib
+        build_lib.build()
+    return fw.load_library()
+
+
+def _call(fn, defaults, over):
+    a = dict(defaults)
+    assert set(over) <= set(a), over
+    a.update(over)
+    return fn(*a.values(), None)
+
+
+NORM_IN = dict(batch=2, heads=3, seqlen=8, dk=64, dv=64, dtype=0, q_in=P[0], ld_q=576,
+               k_in=P[0] + 384, ld_k=576, v_in=P[0] + 768, ld_v=576, eps=1e-6, q=P[1], k=P[2],
+               v=P[3])
+NORM_IN_BWD = dict(batch=2, heads=3, seqlen=8, dk=64, dv=64, dtype=0, q_in=P[0], ld_q=576,
+                   k_in=P[0] + 384, ld_k=576, eps=1e-6, dq=P[1], dk_=P[2], dv_=P[3], dq_in=P[4],
+                   ld_dq=576, dk_in=P[4] + 384, ld_dk=576, dv_in=P[4] + 768, ld_dv=576)
+NORM_OUT = dict(batch=2, heads=3, seqlen=8, dv=64, dtype=0, o=P[0], weight=P[1], gate=P[2],
+                ld_gate=192, gate_kind=0, residual=P[3], ld_res=192, scale=1.0, eps=1e-6, y=P[4],
+                ld_y=192)
+NORM_OUT_BWD = dict(batch=2, heads=3, seqlen=8, dv=64, dtype=0, o=P[0], weight=P[1], gate=P[2],
+                    ld_gate=192, gate_kind=0, scale=1.0, eps=1e-6, dy=P[3], ld_dy=192, dO=P[4],
+                    dgate=P[5], ld_dgate=192, dweight=P[6], ws=P[7], wsb=1 << 20)
+DECODE = dict(nseq=2, heads=3, dk=64, dv=64, dtype=0, S=P[0], q=P[1], k=P[2], v=P[3], log_a=P[4],
+              o=P[5])
+
+SIZES = [(dict(heads=0), INVALID), (dict(dtype=2), INVALID), (dict(dv=48), UNSUPPORTED)]
+SEQ = SIZES + [(dict(batch=0), INVALID), (dict(seqlen=0), INVALID),
+               (dict(batch=1 << 16, seqlen=1 << 15), INVALID), (dict(eps=-1.0), INVALID),
+               (dict(eps=NAN), INVALID)]
+
+
+@pytest.mark.parametrize("over,status", SEQ + [
+    (dict(dk=256, ld_q=3 * 256, ld_k=3 * 256), UNSUPPORTED),
+    (dict(q_in=None), INVALID), (dict(k=None), INVALID),
+    (dict(v=None), INVALID), (dict(v_in=None), INVALID),       # one without the other
+    (dict(q_in=P[0] + 8), INVALID), (dict(k=P[2] + 4), INVALID),   # alignment
+    (dict(ld_q=191), INVALID), (dict(ld_k=580), INVALID), (dict(ld_q=-576), INVALID),
+    (dict(ld_v=1 << 41), INVALID),
+    (dict(q=P[0] + 1024), INVALID), (dict(q=P[2]), INVALID),   # overlaps
+])
+def test_norm_in(lib, over, status):
+    assert _call(lib.falcon_norm_in, NORM_IN, over) == status
+
+
+@pytest.mark.parametrize("over,status", SEQ + [
+    (dict(dq=None), INVALID), (dict(dk_in=None), INVALID), (dict(dv_=None), INVALID),
+    (dict(dv_in=None), INVALID), (dict(dq=P[1] + 4), INVALID), (dict(dq_in=P[4] + 8), INVALID),
+    (dict(ld_dq=100), INVALID),
+    (dict(dk_in=P[4] + 368), INVALID),               # rows that reach into dq_in's
+    (dict(dv_in=P[4] + 784), INVALID),               # rows that reach the next token's dq_in
+    (dict(dk_in=P[4] + 384, ld_dk=584), INVALID),    # interleaved with another distance
+    (dict(dq_in=P[0]), INVALID), (dict(dq_in=P[1]), INVALID),
+])
+def test_norm_in_bwd(lib, over, status):
+    assert _call(lib.falcon_norm_in_bwd, NORM_IN_BWD, over) == status
+
+
+@pytest.mark.parametrize("over,status", SEQ + [
+    (dict(o=None), INVALID), (dict(weight=None), INVALID), (dict(y=None), INVALID),
+    (dict(gate_kind=2), INVALID), (dict(gate_kind=-1), INVALID), (dict(scale=INF), INVALID),
+    (dict(weight=P[1] + 4), INVALID), (dict(y=P[4] + 8), INVALID), (dict(ld_gate=64), INVALID),
+    (dict(y=P[0]), INVALID), (dict(y=P[1]), INVALID), (dict(y=P[2]), INVALID),
+    (dict(y=P[3] + 16), INVALID), (dict(y=P[3], ld_y=200), INVALID),   # not exactly in place
+])
+def test_norm_out(lib, over, status):
+    assert _call(lib.falcon_norm_out, NORM_OUT, over) == status
+
+
+@pytest.mark.parametrize("over,status", SEQ + [
+    (dict(dy=None), INVALID), (dict(dO=None), INVALID), (dict(dweight=None), INVALID),
+    (dict(ws=None), INVALID), (dict(wsb=0), INVALID), (dict(ws=P[7] + 8), INVALID),
+    (dict(gate=None), INVALID), (dict(dgate=None), INVALID), (dict(gate_kind=2), INVALID),
+    (dict(scale=NAN), INVALID), (dict(dgate=P[2]), INVALID), (dict(dO=P[0]), INVALID),
+    (dict(ws=P[4] + 64), INVALID), (dict(dweight=P[3]), INVALID), (dict(ld_dy=190), INVALID),
+])
+def test_norm_out_bwd(lib, over, status):
+    assert _call(lib.falcon_norm_out_bwd, NORM_OUT_BWD, over) == status
+
+
+def test_norm_out_bwd_workspace(lib):
+    f = lib.falcon_norm_out_bwd_workspace_bytes
+    assert f(1, 1, 64) == 64 * 4                     # one workgroup's part of dweight
+    assert f(8, 2048, 64) <= 1024 * 64 * 4
+    assert f(0, 1, 64) == f(1, 1, 48) == f(1 << 16, 1 << 15, 64) == 0
+
+
+@pytest.mark.parametrize("over,status", SIZES + [
+    (dict(nseq=0), INVALID), (dict(dk=24), UNSUPPORTED), (dict(S=None), INVALID),
+    (dict(o=None), INVALID), (dict(q=P[1] + 2), INVALID), (dict(log_a=P[4] + 4), INVALID),
+    (dict(o=P[0] + 64), INVALID), (dict(o=P[4]), INVALID), (dict(S=P[2]), INVALID),
+    (dict(nseq=1 << 18, heads=16, S=1 << 44, q=1 << 40, k=2 << 40, v=3 << 40, log_a=4 << 40,
+          o=5 << 40), UNSUPPORTED),
+])
+def test_gated_decode_step(lib, over, status):
+    assert _call(lib.falcon_gated_decode_step, DECODE, over) == status
+
+
+def test_binding_refuses_host_tensors_and_odd_layouts():
+    torch = pytest.importorskip("torch")
+    x = torch.zeros(1, 2, 3, 16)
+    with pytest.raises(ValueError):
+        fw.norm_in(x, x, x)
+    with pytest.raises(ValueError):
+        fw.norm_out(x, x[0, 0, 0])
+    with pytest.raises(ValueError):
+        fw.gated_decode_step(x, x[0], x[0], x[0])
+    rows = fw.norms._rows
+    ok = torch.zeros(2, 5, 96)[..., 48:].view(2, 5, 3, 16)
+    assert rows(torch, "x", ok, (2, 5, 3, 16), torch.float32, ok.device)[1] == 96
+    assert rows(torch, "x", ok[:, :1], (2, 1, 3, 16), torch.float32, ok.device)[1] == 480
+    for bad in (ok.transpose(1, 2).contiguous().transpose(1, 2), ok[:, ::2], ok[..., ::2],
+                ok[:, :, :1].expand(2, 5, 3, 16), ok[:1].expand(2, 5, 3, 16)):
+        with pytest.raises(ValueError):
+            rows(torch, "x", bad, tuple(bad.shape), torch.float32, bad.device)
+    with pytest.raises(ValueError):
+        fw.norms._gate_kind("relu")

@@ -77,6 +77,21 @@ def load_library():
     lib.falcon_bwd_chunk_noalloc.restype = i
     lib.falcon_bwd_chunk_noalloc.argtypes = [i, i, i, f, vp, i, f, f, i, i, i, i, i, i, vp, vp, vp,
                                              vp, vp, vp, vp, vp, vp, vp, vp, vp, vp, vp, vp]
+    ll, ull = ctypes.c_longlong, ctypes.c_ulonglong
+    lib.falcon_norm_in.restype = i
+    lib.falcon_norm_in.argtypes = [i] * 6 + [vp, ll, vp, ll, vp, ll, f, vp, vp, vp, vp]
+    lib.falcon_norm_in_bwd.restype = i
+    lib.falcon_norm_in_bwd.argtypes = [i] * 6 + [vp, ll, vp, ll, f, vp, vp, vp, vp, ll, vp, ll, vp,
+                                                 ll, vp]
+    lib.falcon_norm_out.restype = i
+    lib.falcon_norm_out.argtypes = [i] * 5 + [vp, vp, vp, ll, i, vp, ll, f, f, vp, ll, vp]
+    lib.falcon_norm_out_bwd_workspace_bytes.restype = ull
+    lib.falcon_norm_out_bwd_workspace_bytes.argtypes = [i, i, i]
+    lib.falcon_norm_out_bwd.restype = i
+    lib.falcon_norm_out_bwd.argtypes = [i] * 5 + [vp, vp, vp, ll, i, f, f, vp, ll, vp, vp, ll, vp,
+                                                  vp, ull, vp]
+    lib.falcon_gated_decode_step.restype = i
+    lib.falcon_gated_decode_step.argtypes = [i] * 5 + [vp] * 7
     _LIB = lib
     return lib
 
@@ -123,6 +138,32 @@ def _stream(torch, device, stream):
     if stream is not None:
         return ctypes.c_void_p(stream.cuda_stream if hasattr(stream, "cuda_stream") else stream)
     return ctypes.c_void_p(torch.cuda.current_stream(device).cuda_stream)
+
+
+class _NoGuard:
+    def __enter__(self):
+        return None
+
+    def __exit__(self, *exc):
+        return False
+
+
+_NO_GUARD = _NoGuard()
+
+
+def _guard(torch, device, stream):
+    """Context of one call: `device` current, and with an explicit stream that stream,
+    so that what the call allocates belongs to the stream it runs on."""
+    if stream is None:
+        if torch.cuda.current_device() == device.index:
+            return _NO_GUARD
+        return torch.cuda.device(device)
+    if not isinstance(stream, torch.cuda.Stream):
+        handle = stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)
+        stream = torch.cuda.ExternalStream(handle, device=device)
+    if stream.device != device:
+        raise ValueError("stream belongs to %s, the tensors to %s" % (stream.device, device))
+    return torch.cuda.stream(stream)
 
 
 def _raise(lib, fn, status):

@@ -553,3 +553,219 @@ FALCON_EXPORT int falcon_bwd_chunk_noalloc(int variant, int window, int flags, f
   b.workspace = static_cast<float*>(ws);
   return finish_launch(falcon::launch_backward(b, (hipStream_t)stream));
 }
+
+// ---------------------------------------------------------------------------
+// Norms before and after a block, and the gated linear recurrence.
+
+namespace {
+
+// A token-major argument: N rows of `width` bytes, `pitch` bytes apart.
+struct Rows {
+  const void* p;
+  size_t n, width, pitch;
+};
+
+Range hull(const Rows& r) { return Range{r.p, r.p ? (r.n - 1) * r.pitch + r.width : 0}; }
+
+// Whether two token-major arguments share a byte.  Rows of one pitch may
+// interleave (views of one fused buffer); other hulls that meet count as shared.
+bool overlap(const Rows& a, const Rows& b) {
+  if (!overlap(hull(a), hull(b))) return false;
+  if (a.pitch != b.pitch) return true;
+  const uintptr_t pa = reinterpret_cast<uintptr_t>(a.p), pb = reinterpret_cast<uintptr_t>(b.p);
+  const size_t d = pb >= pa ? (pb - pa) % a.pitch : (a.pitch - (pa - pb) % a.pitch) % a.pitch;
+  return d < a.width || a.pitch - d < b.width;
+}
+
+// Sizes common to the calls below; fills N (tokens) and es (element size).
+int check_sizes(int batch, int heads, int seqlen, int d0, int d1, int dtype, size_t* N, size_t* es) {
+  if (batch < 1 || heads < 1 || seqlen < 1 || d0 < 1 || d1 < 1) return FALCON_ERR_INVALID_ARG;
+  if (dtype != FALCON_BF16 && dtype != FALCON_F32) return FALCON_ERR_INVALID_ARG;
+  if ((double)batch * heads * seqlen * (d0 > d1 ? d0 : d1) > 1099511627776.0)
+    return FALCON_ERR_INVALID_ARG;  // 2^40 elements
+  if ((double)batch * seqlen >= 2147483648.0) return FALCON_ERR_INVALID_ARG;
+  *N = (size_t)batch * seqlen;
+  *es = dtype == FALCON_BF16 ? 2 : 4;
+  return FALCON_OK;
+}
+
+// One token-major argument's pointer and stride.
+int check_rows(const void* p, long long ld, int heads, int d, size_t N, size_t es, Rows* out) {
+  *out = Rows{nullptr, 1, 0, 1};
+  if (!p) return FALCON_OK;
+  if (!aligned16(p) || ld < (long long)heads * d || ld > (1ll << 40) || (ld * (long long)es) % 16 != 0)
+    return FALCON_ERR_INVALID_ARG;
+  if ((double)N * (double)ld > 4398046511104.0) return FALCON_ERR_INVALID_ARG;  // 2^42 elements
+  *out = Rows{p, N, (size_t)heads * d * es, (size_t)ld * es};
+  return FALCON_OK;
+}
+
+// Outputs against each other and against the inputs (null ones take no part).
+template <int NO, int NI>
+bool any_overlap(const Range (&outs)[NO], const Range (&ins)[NI]) {
+  for (int i = 0; i < NO; ++i) {
+    for (int j = i + 1; j < NO; ++j)
+      if (overlap(outs[i], outs[j])) return true;
+    for (int j = 0; j < NI; ++j)
+      if (overlap(outs[i], ins[j])) return true;
+  }
+  return false;
+}
+
+template <int N>
+bool all_aligned16(const void* const (&ptrs)[N]) {
+  for (const void* p : ptrs)
+    if (p && !aligned16(p)) return false;
+  return true;
+}
+
+}  // namespace
+
+FALCON_EXPORT int falcon_norm_in(int batch, int heads, int seqlen, int dk, int dv, int dtype,
+                                 const void* q_in, long long ld_q, const void* k_in,
+                                 long long ld_k, const void* v_in, long long ld_v, float eps,
+                                 void* q, void* k, void* v, void* stream) {
+  size_t N, es;
+  int st = check_sizes(batch, heads, seqlen, dk, dv, dtype, &N, &es);
+  if (st != FALCON_OK) return st;
+  if (!finite_nonneg(eps)) return FALCON_ERR_INVALID_ARG;
+  if (!q_in || !k_in || !q || !k || (v_in == nullptr) != (v == nullptr))
+    return FALCON_ERR_INVALID_ARG;
+  const void* ptrs[] = {q, k, v};
+  if (!all_aligned16(ptrs)) return FALCON_ERR_INVALID_ARG;
+  Rows rq, rk, rv;
+  if (check_rows(q_in, ld_q, heads, dk, N, es, &rq) || check_rows(k_in, ld_k, heads, dk, N, es, &rk) ||
+      check_rows(v_in, ld_v, heads, dv, N, es, &rv))
+    return FALCON_ERR_INVALID_ARG;
+  const Range outs[] = {{q, N * heads * dk * es}, {k, N * heads * dk * es}, {v, N * heads * dv * es}};
+  const Range ins[] = {hull(rq), hull(rk), hull(rv)};
+  if (any_overlap(outs, ins)) return FALCON_ERR_INVALID_ARG;
+  if (!supported_dim(dk) || !supported_dim(dv)) return FALCON_ERR_UNSUPPORTED;
+  const falcon::NormInArgs a{batch, heads, seqlen, dk, dv, dtype, q_in, (long)ld_q, k_in, (long)ld_k,
+                             v_in, (long)ld_v, eps, q, k, v};
+  return finish_launch(falcon::launch_norm_in(a, (hipStream_t)stream));
+}
+
+FALCON_EXPORT int falcon_norm_in_bwd(int batch, int heads, int seqlen, int dk, int dv, int dtype,
+                                     const void* q_in, long long ld_q, const void* k_in,
+                                     long long ld_k, float eps, const float* dq, const float* dk_,
+                                     const float* dv_, void* dq_in, long long ld_dq, void* dk_in,
+                                     long long ld_dk, void* dv_in, long long ld_dv, void* stream) {
+  size_t N, es;
+  int st = check_sizes(batch, heads, seqlen, dk, dv, dtype, &N, &es);
+  if (st != FALCON_OK) return st;
+  if (!finite_nonneg(eps)) return FALCON_ERR_INVALID_ARG;
+  if (!q_in || !k_in || !dq || !dk_ || !dq_in || !dk_in || (dv_ == nullptr) != (dv_in == nullptr))
+    return FALCON_ERR_INVALID_ARG;
+  const void* ptrs[] = {dq, dk_, dv_};
+  if (!all_aligned16(ptrs)) return FALCON_ERR_INVALID_ARG;
+  Rows rq, rk, oq, ok, ov;
+  if (check_rows(q_in, ld_q, heads, dk, N, es, &rq) || check_rows(k_in, ld_k, heads, dk, N, es, &rk) ||
+      check_rows(dq_in, ld_dq, heads, dk, N, es, &oq) || check_rows(dk_in, ld_dk, heads, dk, N, es, &ok) ||
+      check_rows(dv_in, ld_dv, heads, dv, N, es, &ov))
+    return FALCON_ERR_INVALID_ARG;
+  const Rows outs[] = {oq, ok, ov};
+  const Range ins[] = {hull(rq), hull(rk), {dq, N * heads * dk * 4}, {dk_, N * heads * dk * 4},
+                       {dv_, N * heads * dv * 4}};
+  for (int i = 0; i < 3; ++i) {
+    for (int j = i + 1; j < 3; ++j)
+      if (overlap(outs[i], outs[j])) return FALCON_ERR_INVALID_ARG;
+    for (const Range& r : ins)
+      if (overlap(hull(outs[i]), r)) return FALCON_ERR_INVALID_ARG;
+  }
+  if (!supported_dim(dk) || !supported_dim(dv)) return FALCON_ERR_UNSUPPORTED;
+  const falcon::NormInBwdArgs a{batch, heads, seqlen, dk, dv, dtype, q_in, (long)ld_q, k_in,
+                                (long)ld_k, eps, dq, dk_, dv_, dq_in, (long)ld_dq, dk_in,
+                                (long)ld_dk, dv_in, (long)ld_dv};
+  return finish_launch(falcon::launch_norm_in_bwd(a, (hipStream_t)stream));
+}
+
+FALCON_EXPORT int falcon_norm_out(int batch, int heads, int seqlen, int dv, int dtype,
+                                  const float* o, const float* weight, const void* gate,
+                                  long long ld_gate, int gate_kind, const void* residual,
+                                  long long ld_res, float scale, float eps, void* y,
+                                  long long ld_y, void* stream) {
+  size_t N, es;
+  int st = check_sizes(batch, heads, seqlen, dv, dv, dtype, &N, &es);
+  if (st != FALCON_OK) return st;
+  if (!finite_nonneg(eps) || !isfinite(scale)) return FALCON_ERR_INVALID_ARG;
+  if (gate_kind != FALCON_GATE_SILU && gate_kind != FALCON_GATE_SIGMOID)
+    return FALCON_ERR_INVALID_ARG;
+  if (!o || !weight || !y) return FALCON_ERR_INVALID_ARG;
+  const void* ptrs[] = {o, weight};
+  if (!all_aligned16(ptrs)) return FALCON_ERR_INVALID_ARG;
+  Rows rg, rr, ry;
+  if (check_rows(gate, ld_gate, heads, dv, N, es, &rg) || check_rows(residual, ld_res, heads, dv, N, es, &rr) ||
+      check_rows(y, ld_y, heads, dv, N, es, &ry))
+    return FALCON_ERR_INVALID_ARG;
+  const Range out = hull(ry);
+  if (overlap(out, Range{o, N * heads * dv * 4}) || overlap(out, Range{weight, (size_t)dv * 4}) ||
+      overlap(ry, rg))
+    return FALCON_ERR_INVALID_ARG;
+  // in place: each element of the residual is read before y's is written there
+  if (!(residual == y && ld_res == ld_y) && overlap(ry, rr)) return FALCON_ERR_INVALID_ARG;
+  if (!supported_dim(dv)) return FALCON_ERR_UNSUPPORTED;
+  const falcon::NormOutArgs a{batch, heads, seqlen, dv, dtype, o, weight, gate, (long)ld_gate,
+                              gate_kind, residual, (long)ld_res, scale, eps, y, (long)ld_y};
+  return finish_launch(falcon::launch_norm_out(a, (hipStream_t)stream));
+}
+
+FALCON_EXPORT unsigned long long falcon_norm_out_bwd_workspace_bytes(int batch, int seqlen, int dv) {
+  if (batch < 1 || seqlen < 1 || !supported_dim(dv) || (double)batch * seqlen >= 2147483648.0)
+    return 0;
+  return (unsigned long long)falcon::norm_out_bwd_workspace_bytes(batch, seqlen, dv);
+}
+
+FALCON_EXPORT int falcon_norm_out_bwd(int batch, int heads, int seqlen, int dv, int dtype,
+                                      const float* o, const float* weight, const void* gate,
+                                      long long ld_gate, int gate_kind, float scale, float eps,
+                                      const void* dy, long long ld_dy, float* dO, void* dgate,
+                                      long long ld_dgate, float* dweight, void* workspace,
+                                      unsigned long long workspace_bytes, void* stream) {
+  size_t N, es;
+  int st = check_sizes(batch, heads, seqlen, dv, dv, dtype, &N, &es);
+  if (st != FALCON_OK) return st;
+  if (!finite_nonneg(eps) || !isfinite(scale)) return FALCON_ERR_INVALID_ARG;
+  if (gate_kind != FALCON_GATE_SILU && gate_kind != FALCON_GATE_SIGMOID)
+    return FALCON_ERR_INVALID_ARG;
+  if (!o || !weight || !dy || !dO || !dweight || !workspace || (gate == nullptr) != (dgate == nullptr))
+    return FALCON_ERR_INVALID_ARG;
+  const void* ptrs[] = {o, weight, dO, dweight, workspace};
+  if (!all_aligned16(ptrs)) return FALCON_ERR_INVALID_ARG;
+  Rows rg, rd, og;
+  if (check_rows(gate, ld_gate, heads, dv, N, es, &rg) || check_rows(dy, ld_dy, heads, dv, N, es, &rd) ||
+      check_rows(dgate, ld_dgate, heads, dv, N, es, &og))
+    return FALCON_ERR_INVALID_ARG;
+  if (!supported_dim(dv)) return FALCON_ERR_UNSUPPORTED;
+  const size_t need = falcon::norm_out_bwd_workspace_bytes(batch, seqlen, dv);
+  if (workspace_bytes < need) return FALCON_ERR_INVALID_ARG;
+  const Range outs[] = {{dO, N * heads * dv * 4}, {dweight, (size_t)dv * 4}, {workspace, need}};
+  const Range ins[] = {{o, N * heads * dv * 4}, {weight, (size_t)dv * 4}, hull(rg), hull(rd), hull(og)};
+  if (any_overlap(outs, ins)) return FALCON_ERR_INVALID_ARG;
+  if (overlap(hull(og), ins[0]) || overlap(hull(og), ins[1]) || overlap(og, rg) || overlap(og, rd))
+    return FALCON_ERR_INVALID_ARG;
+  const falcon::NormOutBwdArgs a{batch, heads, seqlen, dv, dtype, o, weight, gate, (long)ld_gate,
+                                 gate_kind, scale, eps, dy, (long)ld_dy, dO, dgate, (long)ld_dgate,
+                                 dweight, static_cast<float*>(workspace)};
+  return finish_launch(falcon::launch_norm_out_bwd(a, (hipStream_t)stream));
+}
+
+FALCON_EXPORT int falcon_gated_decode_step(int nseq, int heads, int dk, int dv, int dtype, float* S,
+                                           const void* q, const void* k, const void* v,
+                                           const float* log_a, float* o, void* stream) {
+  size_t N, es;
+  int st = check_sizes(nseq, heads, 1, dk, dv, dtype, &N, &es);
+  if (st != FALCON_OK) return st;
+  if (!S || !q || !k || !v || !o) return FALCON_ERR_INVALID_ARG;
+  const void* ptrs[] = {S, q, k, v, log_a, o};
+  if (!all_aligned16(ptrs)) return FALCON_ERR_INVALID_ARG;
+  const size_t NH = N * heads;
+  const Range outs[] = {{S, NH * dv * dk * 4}, {o, NH * dv * 4}};
+  const Range ins[] = {{q, NH * dk * es}, {k, NH * dk * es}, {v, NH * dv * es}, {log_a, NH * 4}};
+  if (any_overlap(outs, ins)) return FALCON_ERR_INVALID_ARG;
+  if (!supported_dim(dk) || !supported_dim(dv)) return FALCON_ERR_UNSUPPORTED;
+  // one thread per four state elements in one launch
+  if ((double)NH * dv * dk >= 17179869184.0) return FALCON_ERR_UNSUPPORTED;
+  const falcon::GatedDecodeArgs a{nseq, heads, dk, dv, dtype, S, q, k, v, log_a, o};
+  return finish_launch(falcon::launch_gated_decode(a, (hipStream_t)stream));
+}

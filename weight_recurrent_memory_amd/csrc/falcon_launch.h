@@ -121,4 +121,102 @@ hipError_t launch_decode(const DecodeArgs& a, hipStream_t stream);
 // (which may equal a.x_hist / a.y_hist); enqueue after the call's kernel
 hipError_t launch_history_out(const SeqArgs& a, void* x_out, void* y_out, hipStream_t stream);
 
+// ---- gated linear recurrence (falcon_gated.hip, falcon_gated_bwd.hip)
+
+// Forward over a sequence: S_t = a_t S_{t-1} + v_t k_t^T, o_t = S_t q_t, a = exp(log_a).
+struct GatedArgs {
+  int batch, heads, seqlen, dk, dv;
+  int dtype;             // 0 bf16, 1 fp32
+  const void* q;
+  const void* k;
+  const void* v;
+  const float* log_a;    // may be null (no decay)
+  const float* S0;       // may be null
+  float* o;
+  float* S_out;          // may be null
+};
+struct GatedDecodeArgs {
+  int nseq, heads, dk, dv;
+  int dtype;
+  float* S;
+  const void* q;
+  const void* k;
+  const void* v;
+  const float* log_a;    // may be null
+  float* o;
+};
+hipError_t launch_gated_decode(const GatedDecodeArgs& a, hipStream_t stream);
+
+// ---- norms before and after a block (falcon_norm.hip); ld_*: elements from one
+// token's row of heads to the next
+
+struct NormInArgs {
+  int batch, heads, seqlen, dk, dv;
+  int dtype;
+  const void* q_in;
+  long ld_q;
+  const void* k_in;
+  long ld_k;
+  const void* v_in;      // null with v
+  long ld_v;
+  float eps;
+  void* q;
+  void* k;
+  void* v;
+};
+struct NormInBwdArgs {
+  int batch, heads, seqlen, ndk, ndv;
+  int dtype;
+  const void* q_in;
+  long ld_q;
+  const void* k_in;
+  long ld_k;
+  float eps;
+  const float* dq;
+  const float* dk;
+  const float* dv;       // null with dv_in
+  void* dq_in;
+  long ld_dq;
+  void* dk_in;
+  long ld_dk;
+  void* dv_in;
+  long ld_dv;
+};
+struct NormOutArgs {
+  int batch, heads, seqlen, dv;
+  int dtype;
+  const float* o;
+  const float* weight;
+  const void* gate;      // may be null
+  long ld_gate;
+  int gate_kind;         // 0 silu, 1 sigmoid
+  const void* residual;  // may be null; may equal y
+  long ld_res;
+  float scale, eps;
+  void* y;
+  long ld_y;
+};
+struct NormOutBwdArgs {
+  int batch, heads, seqlen, dv;
+  int dtype;
+  const float* o;
+  const float* weight;
+  const void* gate;      // null with dgate
+  long ld_gate;
+  int gate_kind;
+  float scale, eps;
+  const void* dy;
+  long ld_dy;
+  float* dO;
+  void* dgate;
+  long ld_dgate;
+  float* dweight;
+  float* workspace;      // norm_out_bwd_workspace_bytes(...)
+};
+hipError_t launch_norm_in(const NormInArgs& a, hipStream_t stream);
+hipError_t launch_norm_in_bwd(const NormInBwdArgs& a, hipStream_t stream);
+hipError_t launch_norm_out(const NormOutArgs& a, hipStream_t stream);
+size_t norm_out_bwd_workspace_bytes(int batch, int seqlen, int dv);
+hipError_t launch_norm_out_bwd(const NormOutBwdArgs& a, hipStream_t stream);
+
 }  // namespace falcon
