@@ -445,11 +445,30 @@ int falcon_norm_out_bwd(int batch, int heads, int seqlen, int dv, int dtype, con
  *            -1000 counts as -1000 (e^-1000 is 0 in float32), so -inf resets the
  *            state: a new sequence starts at that token.
  *
+ * falcon_gated_fwd_chunk - a sequence, in chunks of 64 tokens
+ *   q, k, v, S0, o, S_out   as falcon_fwd_chunk (S0, S_out may be NULL; S_out may
+ *             equal S0); bf16 or fp32 inputs, dk, dv in {16, 32, 64, 128}, any L >= 1
+ *   workspace device memory, 16-byte aligned, overlapping no other argument, or
+ *             NULL.  With workspace_bytes >= falcon_gated_fwd_workspace_bytes(...)
+ *             a long sequence of few chains is cut into segments that run side by
+ *             side; otherwise each chain is walked in order.  Results agree up to
+ *             rounding.
+ * Finite inputs (log_a: also -inf) give the recurrence to float32 rounding: products
+ * run on bf16 matrix cores with float32 operands in three bf16 parts, decays as
+ * differences of float64 sums.  log_a > 0 (growth) is taken as given.
+ * batch * heads * dv < 2^27 (FALCON_ERR_UNSUPPORTED from there on).
+ *
  * falcon_gated_decode_step - one token for serving: S [nseq, heads, dv, dk]
  * float32 updated in place, q, k [nseq, heads, dk], v [nseq, heads, dv], log_a
  * [nseq, heads] or NULL, o [nseq, heads, dv] float32.  No argument may overlap
  * another.  nseq * heads * dk * dv < 2^34 (FALCON_ERR_UNSUPPORTED from there on).
  */
+unsigned long long falcon_gated_fwd_workspace_bytes(int batch, int heads, int seqlen, int dk,
+                                                    int dv, int dtype);
+int falcon_gated_fwd_chunk(int batch, int heads, int seqlen, int dk, int dv, int dtype,
+                           const void* q, const void* k, const void* v, const float* log_a,
+                           const float* S0, float* o, float* S_out, void* workspace,
+                           unsigned long long workspace_bytes, void* stream);
 int falcon_gated_decode_step(int nseq, int heads, int dk, int dv, int dtype, float* S,
                              const void* q, const void* k, const void* v, const float* log_a,
                              float* o, void* stream);

@@ -1,0 +1,152 @@
+"""The gated recurrence's chunk forward and backward against the fp64 recurrence.
+
+Tolerances, u = 2^-24 (float32).  The oracle is also run on absolute values, which
+gives for each output the sum A of the absolute values of its terms.  The kernels form
+each term with at most: the planes' dropped parts 3u a product of two products, decays
+to 4u (a float32 exponent, v_exp_f32), and float32 sums, at most 64 + dk terms inside a
+chunk in matrix-core order and one rounding of the state a chunk while a term lives.  A
+worst case of every rounding the same way: (dk + dv + 80 + 8 chunks) u A for the forward;
+roundings do not all point one way, so errors stay well below it.  The comparison is per
+element with the tensor's rounding floor (A itself is at least a millionth of its mean).
+"""
+import numpy as np
+import pytest
+
+from oracle import block_oracle as bo
+
+pytestmark = pytest.mark.gpu
+
+torch = pytest.importorskip("torch")
+import weight_recurrent_memory_amd as fw  # noqa: E402
+
+U = 2.0 ** -24
+TYPES = [torch.bfloat16, torch.float32]
+
+
+@pytest.fixture(scope="module", autouse=True)
+def _gpu():
+    if not torch.cuda.is_available():
+        pytest.skip("no GPU")
+    fw.load_library()
+
+
+def _np(t):
+    return None if t is None else t.detach().double().cpu().numpy()
+
+
+def _up(x, dtype=torch.float32):
+    return torch.from_numpy(np.ascontiguousarray(x, dtype=np.float32)).cuda().to(dtype)
+
+
+def _inputs(seed, B, H, L, dk, dv, dtype, *, gate="mixed", start=True):
+    r = np.random.default_rng(seed)
+    n = lambda *s: r.standard_normal(s)  # noqa: E731
+    unit = lambda x: x / np.linalg.norm(x, axis=-1, keepdims=True)  # noqa: E731
+    x = dict(q=_up(unit(n(B, H, L, dk)), dtype), k=_up(unit(n(B, H, L, dk)), dtype),
+             v=_up(n(B, H, L, dv), dtype))
+    g = -np.log1p(np.exp(-(2.0 * n(B, H, L) + 3.0)))
+    if gate == "strong":                 # decays down to e^-60 beside weak ones
+        g = np.where(r.random((B, H, L)) < 0.3, -60 * r.random((B, H, L)), g)
+    if gate == "resets":
+        g = np.where(r.random((B, H, L)) < 0.05, -np.inf, g)
+    x["log_a"] = None if gate == "none" else _up(g)
+    x["S0"] = _up(0.3 * n(B, H, dv, dk)) if start else None
+    return x
+
+
+def _forward_ref(x):
+    a = [_np(x[n]) for n in ("q", "k", "v", "log_a", "S0")]
+    o, S = bo.gated_recurrence(*a)
+    ab = [None if y is None else np.abs(y) for y in a]
+    ab[3] = a[3]
+    ao, aS = bo.gated_recurrence(*ab)
+    return o, S, ao, aS
+
+
+def _meets(name, got, ref, size, factor):
+    got = _np(got)
+    assert got.shape == ref.shape, name
+    tol = factor * U * np.maximum(size, 1e-6 * np.mean(size))
+    bad = ~(np.abs(got - ref) <= tol)
+    assert not bad.any(), "%s: %d off, worst %g times the tolerance" % (
+        name, bad.sum(), np.nanmax(np.abs(got - ref)[bad] / np.maximum(tol[bad], 1e-300)))
+
+
+def _factor(L, dk, dv):
+    return dk + dv + 80 + 8 * (-(-L // 64))
+
+
+DIMS = [(16, 16), (16, 128), (32, 32), (64, 64), (128, 16), (64, 32), (32, 64), (128, 64), (128, 128)]
+LENGTHS = [1, 2, 15, 16, 17, 63, 64, 65, 127, 130, 321]
+
+
+def _check_forward(x, **kw):
+    B, H, L, dk = x["q"].shape
+    o, S = fw.gated_fwd_chunk(x["q"], x["k"], x["v"], x["log_a"], S0=x["S0"], return_state=True, **kw)
+    ro, rS, ao, aS = _forward_ref(x)
+    f = _factor(L, dk, x["v"].shape[-1])
+    _meets("o", o, ro, ao, f)
+    _meets("S", S, rS, aS, f)
+    return o, S
+
+
+@pytest.mark.parametrize("dtype", TYPES)
+@pytest.mark.parametrize("dk,dv", DIMS)
+@pytest.mark.parametrize("L", LENGTHS)
+def test_forward(dtype, dk, dv, L):
+    gate = ["mixed", "strong", "resets", "none"][(L + dk + dv) % 4]
+    _check_forward(_inputs(L, 2, 3, L, dk, dv, dtype, gate=gate, start=L % 2 == 1))
+
+
+@pytest.mark.parametrize("dtype", TYPES)
+@pytest.mark.parametrize("gate", ["mixed", "strong", "resets", "none"])
+@pytest.mark.parametrize("start", [False, True])
+def test_forward_gates(dtype, gate, start):
+    _check_forward(_inputs(7, 1, 2, 200, 64, 64, dtype, gate=gate, start=start))
+
+
+@pytest.mark.parametrize("dtype", TYPES)
+@pytest.mark.parametrize("dk,dv,L", [(64, 64, 2049), (128, 128, 1100), (16, 32, 4000), (32, 128, 777)])
+def test_forward_in_segments(dtype, dk, dv, L):
+    """Long sequences of few heads: the call cut into segments and the one in order
+    both meet the recurrence; each is the same bits every time."""
+    x = _inputs(8, 1, 2, L, dk, dv, dtype, gate="resets")
+    need = fw.load_library().falcon_gated_fwd_workspace_bytes(1, 2, L, dk, dv, int(dtype == torch.float32))
+    assert need > 0
+    o, S = _check_forward(x)
+    o2, S2 = _check_forward(x, workspace=torch.empty(need + 100, device="cuda", dtype=torch.uint8))
+    assert torch.equal(o, o2) and torch.equal(S, S2)
+    o3, S3 = _check_forward(x, workspace=None)
+    o4, S4 = _check_forward(x, workspace=torch.empty(max(need - 16, 0), device="cuda", dtype=torch.uint8))
+    assert torch.equal(o3, o4) and torch.equal(S3, S4)
+    # the state written over the one that the call starts from
+    S5 = x["S0"].clone()
+    o5 = fw.gated_fwd_chunk(x["q"], x["k"], x["v"], x["log_a"], S0=S5, S_out=S5)
+    assert torch.equal(o5, o) and torch.equal(S5, S)
+
+
+def test_resumed_sequence_and_single_tokens():
+    """A sequence in pieces, the last ones single tokens, against one call's oracle."""
+    L, cuts = 150, [0, 1, 65, 100, 147, 148, 149, 150]
+    x = _inputs(9, 2, 2, L, 64, 64, torch.bfloat16)
+    S, parts = x["S0"].clone(), []
+    for a, b in zip(cuts, cuts[1:]):
+        q, k, v = (x[n][:, :, a:b].contiguous() for n in ("q", "k", "v"))
+        la = x["log_a"][:, :, a:b].contiguous()
+        if b - a == 1:
+            parts.append(fw.gated_decode_step(S, q[:, :, 0].contiguous(), k[:, :, 0].contiguous(),
+                                              v[:, :, 0].contiguous(), la[:, :, 0].contiguous())[:, :, None])
+        else:
+            parts.append(fw.gated_fwd_chunk(q, k, v, la, S0=S, S_out=S))
+    ro, rS, ao, aS = _forward_ref(x)
+    _meets("o", torch.cat(parts, 2), ro, ao, _factor(L, 64, 64) + 8 * len(cuts))
+    _meets("S", S, rS, aS, _factor(L, 64, 64) + 8 * len(cuts))
+
+
+def test_many_chains_and_rows_behind():
+    """More chains than segments are cut for; memory behind and before o untouched."""
+    x = _inputs(10, 70, 12, 70, 16, 16, torch.bfloat16)
+    buf = torch.full((70 * 12 * 70 * 16 + 512,), 7.0, device="cuda")
+    out = buf[256:-256].view(70, 12, 70, 16)
+    o, _ = _check_forward(x, out=out)
+    assert bool((buf[:256] == 7).all()) and bool((buf[-256:] == 7).all())

@@ -90,6 +90,10 @@ def load_library():
     lib.falcon_norm_out_bwd.restype = i
     lib.falcon_norm_out_bwd.argtypes = [i] * 5 + [vp, vp, vp, ll, i, f, f, vp, ll, vp, vp, ll, vp,
                                                   vp, ull, vp]
+    lib.falcon_gated_fwd_workspace_bytes.restype = ull
+    lib.falcon_gated_fwd_workspace_bytes.argtypes = [i] * 6
+    lib.falcon_gated_fwd_chunk.restype = i
+    lib.falcon_gated_fwd_chunk.argtypes = [i] * 6 + [vp] * 8 + [ull, vp]
     lib.falcon_gated_decode_step.restype = i
     lib.falcon_gated_decode_step.argtypes = [i] * 5 + [vp] * 7
     _LIB = lib

@@ -769,3 +769,49 @@ FALCON_EXPORT int falcon_gated_decode_step(int nseq, int heads, int dk, int dv, 
   const falcon::GatedDecodeArgs a{nseq, heads, dk, dv, dtype, S, q, k, v, log_a, o};
   return finish_launch(falcon::launch_gated_decode(a, (hipStream_t)stream));
 }
+
+namespace {
+
+// Chains a launch of the chunk kernels may hold (256 threads per 16 value rows or more).
+bool gated_chains(int batch, int heads, int dv) {
+  return (double)batch * heads * dv < 134217728.0;  // 2^27
+}
+
+}  // namespace
+
+FALCON_EXPORT unsigned long long falcon_gated_fwd_workspace_bytes(int batch, int heads, int seqlen,
+                                                                  int dk, int dv, int dtype) {
+  size_t N, es;
+  if (check_sizes(batch, heads, seqlen, dk, dv, dtype, &N, &es) != FALCON_OK || !supported_dim(dk) ||
+      !supported_dim(dv) || !gated_chains(batch, heads, dv))
+    return 0;
+  falcon::GatedArgs a{batch, heads, seqlen, dk, dv, dtype};
+  return (unsigned long long)falcon::gated_workspace_bytes(a);
+}
+
+FALCON_EXPORT int falcon_gated_fwd_chunk(int batch, int heads, int seqlen, int dk, int dv, int dtype,
+                                         const void* q, const void* k, const void* v,
+                                         const float* log_a, const float* S0, float* o, float* S_out,
+                                         void* workspace, unsigned long long workspace_bytes,
+                                         void* stream) {
+  size_t N, es;
+  int st = check_sizes(batch, heads, seqlen, dk, dv, dtype, &N, &es);
+  if (st != FALCON_OK) return st;
+  if (!q || !k || !v || !o) return FALCON_ERR_INVALID_ARG;
+  const void* ptrs[] = {q, k, v, log_a, S0, o, S_out, workspace};
+  if (!all_aligned16(ptrs)) return FALCON_ERR_INVALID_ARG;
+  if (!supported_dim(dk) || !supported_dim(dv)) return FALCON_ERR_UNSUPPORTED;
+  if (!gated_chains(batch, heads, dv)) return FALCON_ERR_UNSUPPORTED;
+  const size_t NH = N * heads, state = (size_t)batch * heads * dv * dk * 4;
+  const falcon::GatedArgs a{batch, heads, seqlen, dk, dv, dtype, q, k, v, log_a, S0, o, S_out};
+  const size_t need = falcon::gated_workspace_bytes(a);
+  const bool cut = need > 0 && workspace && workspace_bytes >= need;
+  const Range outs[] = {{o, NH * dv * 4}, {S_out, state}, {workspace, cut ? need : 0}};
+  const Range ins[] = {{q, NH * dk * es}, {k, NH * dk * es}, {v, NH * dv * es}, {log_a, NH * 4}};
+  if (any_overlap(outs, ins)) return FALCON_ERR_INVALID_ARG;
+  const Range s0{S0, state};
+  if (overlap(outs[0], s0) || overlap(outs[2], s0)) return FALCON_ERR_INVALID_ARG;
+  if (S_out != S0 && overlap(outs[1], s0)) return FALCON_ERR_INVALID_ARG;
+  return finish_launch(falcon::launch_gated(a, cut ? workspace : nullptr, cut ? need : 0,
+                                            (hipStream_t)stream));
+}

@@ -135,6 +135,10 @@ struct GatedArgs {
   float* o;
   float* S_out;          // may be null
 };
+// Bytes of device workspace with which launch_gated cuts the sequence into segments
+// (0: one segment in any case); without it every chain is one segment.
+size_t gated_workspace_bytes(const GatedArgs& a);
+hipError_t launch_gated(const GatedArgs& a, void* ws, size_t ws_bytes, hipStream_t stream);
 struct GatedDecodeArgs {
   int nseq, heads, dk, dv;
   int dtype;
