@@ -458,6 +458,18 @@ int falcon_norm_out_bwd(int batch, int heads, int seqlen, int dv, int dtype, con
  * differences of float64 sums.  log_a > 0 (growth) is taken as given.
  * batch * heads * dv < 2^27 (FALCON_ERR_UNSUPPORTED from there on).
  *
+ * falcon_gated_bwd_chunk - gradients of sum <dO, o> + <dS_L, S_L>
+ *   q, k, v, log_a, S0, dtype   as the forward's
+ *   dO        [batch, heads, L, dv] float32
+ *   dS_L      [batch, heads, dv, dk] float32, or NULL
+ *   dq, dk_out, dv_out   [batch, heads, L, dk / dk / dv] float32
+ *   dlog_a    [batch, heads, L] float32, or NULL; needs log_a.  0 at a reset.
+ *   dS0       [batch, heads, dv, dk] float32, or NULL (with S0 NULL: the gradient of
+ *             the zero state)
+ *   workspace falcon_gated_bwd_workspace_bytes(...) bytes, 16-byte aligned
+ * Outputs and workspace overlap no other argument.  FALCON_ERR_UNSUPPORTED as the
+ * forward, and from batch * heads * max(dk, dv) * ceil(L / 1024) = 2^27 on.
+ *
  * falcon_gated_decode_step - one token for serving: S [nseq, heads, dv, dk]
  * float32 updated in place, q, k [nseq, heads, dk], v [nseq, heads, dv], log_a
  * [nseq, heads] or NULL, o [nseq, heads, dv] float32.  No argument may overlap
@@ -469,6 +481,13 @@ int falcon_gated_fwd_chunk(int batch, int heads, int seqlen, int dk, int dv, int
                            const void* q, const void* k, const void* v, const float* log_a,
                            const float* S0, float* o, float* S_out, void* workspace,
                            unsigned long long workspace_bytes, void* stream);
+unsigned long long falcon_gated_bwd_workspace_bytes(int batch, int heads, int seqlen, int dk,
+                                                    int dv, int dtype);
+int falcon_gated_bwd_chunk(int batch, int heads, int seqlen, int dk, int dv, int dtype,
+                           const void* q, const void* k, const void* v, const float* log_a,
+                           const float* S0, const float* dO, const float* dS_L, float* dq,
+                           float* dk_out, float* dv_out, float* dlog_a, float* dS0,
+                           void* workspace, unsigned long long workspace_bytes, void* stream);
 int falcon_gated_decode_step(int nseq, int heads, int dk, int dv, int dtype, float* S,
                              const void* q, const void* k, const void* v, const float* log_a,
                              float* o, void* stream);

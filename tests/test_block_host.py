@@ -135,3 +135,49 @@ def test_binding_refuses_host_tensors_and_odd_layouts():
             rows(torch, "x", bad, tuple(bad.shape), torch.float32, bad.device)
     with pytest.raises(ValueError):
         fw.norms._gate_kind("relu")
+
+
+FWD = dict(batch=2, heads=3, seqlen=8, dk=64, dv=64, dtype=0, q=P[0], k=P[1], v=P[2], log_a=P[3],
+           S0=P[4], o=P[5], S_out=P[6], ws=P[7], wsb=0)
+BWD = dict(batch=2, heads=3, seqlen=8, dk=64, dv=64, dtype=0, q=P[0], k=P[1], v=P[2], log_a=P[3],
+           S0=P[4], dO=P[5], dS_L=P[6], dq=P[7], dk_=P[8], dv_=P[9], dlog_a=P[10], dS0=P[11],
+           ws=P[12], wsb=1 << 20)
+
+
+@pytest.mark.parametrize("over,status", SIZES + [
+    (dict(batch=0), INVALID), (dict(seqlen=0), INVALID), (dict(batch=1 << 16, seqlen=1 << 15), INVALID),
+    (dict(dk=24), UNSUPPORTED), (dict(q=None), INVALID), (dict(o=None), INVALID),
+    (dict(k=P[1] + 8), INVALID), (dict(log_a=P[3] + 4), INVALID), (dict(ws=P[7] + 8), INVALID),
+    (dict(o=P[0]), INVALID), (dict(o=P[3]), INVALID), (dict(S_out=P[2]), INVALID),
+    (dict(S_out=P[4] + 64), INVALID),                # the start's state only exactly in place
+    (dict(o=P[4]), INVALID), (dict(S_out=P[5]), INVALID),
+    (dict(seqlen=2048, ws=P[5] + 4096, wsb=1 << 26), INVALID),   # workspace inside o
+    (dict(batch=1 << 17, heads=16, seqlen=1, q=1 << 44, k=2 << 40, v=3 << 40, log_a=4 << 40,
+          S0=5 << 40, o=6 << 40, S_out=7 << 40), UNSUPPORTED),
+])
+def test_gated_fwd_chunk(lib, over, status):
+    assert _call(lib.falcon_gated_fwd_chunk, FWD, over) == status
+
+
+@pytest.mark.parametrize("over,status", SIZES + [
+    (dict(batch=0), INVALID), (dict(seqlen=-1), INVALID), (dict(dk=256), UNSUPPORTED),
+    (dict(dO=None), INVALID), (dict(dq=None), INVALID), (dict(ws=None), INVALID),
+    (dict(wsb=100), INVALID), (dict(ws=P[12] + 8), INVALID), (dict(log_a=None), INVALID),
+    (dict(dO=P[5] + 4), INVALID), (dict(dq=P[0]), INVALID), (dict(dk_=P[7]), INVALID),
+    (dict(dS0=P[4]), INVALID), (dict(dS0=P[6]), INVALID), (dict(dlog_a=P[3]), INVALID),
+    (dict(ws=P[9] + 64), INVALID),
+    (dict(heads=512, batch=64, seqlen=1 << 17, q=1 << 45, k=2 << 45, v=3 << 45, log_a=4 << 45,
+          S0=5 << 45, dO=6 << 45, dS_L=7 << 45, dq=8 << 45, dk_=9 << 45, dv_=10 << 45,
+          dlog_a=11 << 45, dS0=12 << 45, ws=13 << 45), UNSUPPORTED),
+])
+def test_gated_bwd_chunk(lib, over, status):
+    assert _call(lib.falcon_gated_bwd_chunk, BWD, over) == status
+
+
+def test_gated_workspaces(lib):
+    f, b = lib.falcon_gated_fwd_workspace_bytes, lib.falcon_gated_bwd_workspace_bytes
+    assert f(1, 1, 64, 64, 64, 0) == 0               # one chunk
+    assert f(64, 16, 8192, 64, 64, 0) == 0           # chains enough to fill the GPU
+    assert f(1, 4, 32768, 128, 128, 0) > 0
+    assert f(1, 1, 0, 64, 64, 0) == b(1, 1, 64, 48, 64, 0) == b(1, 1, 64, 64, 64, 3) == 0
+    assert b(1, 1, 1, 16, 16, 0) > 0

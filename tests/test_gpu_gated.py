@@ -150,3 +150,92 @@ def test_many_chains_and_rows_behind():
     out = buf[256:-256].view(70, 12, 70, 16)
     o, _ = _check_forward(x, out=out)
     assert bool((buf[:256] == 7).all()) and bool((buf[-256:] == 7).all())
+
+
+def _backward(x, seed, *, end=True, **kw):
+    r = np.random.default_rng(seed)
+    B, H, L, dk = x["q"].shape
+    dv = x["v"].shape[-1]
+    dO = _up(r.standard_normal((B, H, L, dv)))
+    dS = _up(0.3 * r.standard_normal((B, H, dv, dk))) if end else None
+    return dO, dS, fw.gated_bwd_chunk(x["q"], x["k"], x["v"], x["log_a"], dO, S0=x["S0"], dS_L=dS, **kw)
+
+
+def _check_backward(x, seed, **kw):
+    """dlog_a's terms: r and c are dot products of an output with an input (d more terms),
+    and a segment's sums add up to 1024 of each: an error of every r and c before it,
+    f u of each one's own size, beside X's.  All bounds on absolute sums."""
+    dO, dS, got = _backward(x, seed, **kw)
+    B, H, L, dk = x["q"].shape
+    dv = x["v"].shape[-1]
+    a = [_np(x[n]) for n in ("q", "k", "v", "log_a")]
+    ref = bo.gated_backward(*a, _np(dO), _np(x["S0"]), _np(dS))
+    ab = [None if y is None else np.abs(y) for y in a]
+    ab[3] = a[3]
+    size = bo.gated_backward(*ab, np.abs(_np(dO)), None if x["S0"] is None else np.abs(_np(x["S0"])),
+                             None if dS is None else np.abs(_np(dS)))
+    f = _factor(L, dk, dv) + max(dk, dv)
+    for n in ("dq", "dk", "dv"):
+        _meets(n, got[n], ref[n], size[n], f)
+    assert ("dS0" in got) == (x["S0"] is not None) and ("dlog_a" in got) == (x["log_a"] is not None)
+    if "dS0" in got:
+        _meets("dS0", got["dS0"], ref["dS0"], size["dS0"], f)
+    if "dlog_a" in got:
+        # sizes of r and c over the segment (1024 tokens at most), the borders' own beside
+        rc = np.sum(np.abs(a[0]) * size["dq"], -1) + np.sum(np.abs(a[1]) * size["dk"], -1)
+        behind = np.cumsum(rc[..., ::-1], -1)[..., ::-1]
+        behind[..., :-1024] -= behind[..., 1024:]
+        top = np.max(size["dlog_a"], axis=-1, keepdims=True)
+        _meets("dlog_a", got["dlog_a"], ref["dlog_a"], behind + top, f)
+        # and as a whole: the errors of a sum's terms do not all point one way
+        err = np.linalg.norm(_np(got["dlog_a"]) - ref["dlog_a"])
+        assert err <= 2e-5 * np.linalg.norm(ref["dlog_a"]) + 1e-6
+    return got
+
+
+@pytest.mark.parametrize("dtype", TYPES)
+@pytest.mark.parametrize("dk,dv", DIMS)
+@pytest.mark.parametrize("L", LENGTHS)
+def test_backward(dtype, dk, dv, L):
+    gate = ["mixed", "strong", "resets", "none"][(L + dk + dv) % 4]
+    _check_backward(_inputs(L, 2, 3, L, dk, dv, dtype, gate=gate, start=L % 2 == 1), 20, end=L % 3 != 0)
+
+
+@pytest.mark.parametrize("dtype", TYPES)
+@pytest.mark.parametrize("gate", ["mixed", "strong", "resets", "none"])
+@pytest.mark.parametrize("start,end", [(False, False), (True, False), (False, True), (True, True)])
+def test_backward_gates(dtype, gate, start, end):
+    _check_backward(_inputs(21, 1, 2, 200, 64, 64, dtype, gate=gate, start=start), 22, end=end)
+
+
+@pytest.mark.parametrize("dtype", TYPES)
+@pytest.mark.parametrize("dk,dv,L", [(64, 64, 2049), (128, 128, 1100), (16, 32, 4000), (32, 128, 777)])
+def test_backward_in_segments(dtype, dk, dv, L):
+    x = _inputs(23, 1, 2, L, dk, dv, dtype, gate="mixed")
+    got = _check_backward(x, 24)
+    again = _backward(x, 24)[2]
+    assert all(torch.equal(got[n], again[n]) for n in got)
+
+
+def test_backward_of_many_chains():
+    """Segments of 1024 tokens whatever the number of chains."""
+    _check_backward(_inputs(25, 30, 40, 1100, 16, 16, torch.bfloat16, gate="resets"), 26)
+
+
+def test_backward_against_differences():
+    """Along random directions, central differences of the fp64 recurrence: their own
+    error is about 1e-8 of values of order one, the kernels' 1e-5 of the absolute sum."""
+    x = _inputs(27, 1, 2, 100, 32, 64, torch.float32)
+    dO, dS, d = _backward(x, 28)
+    base = [_np(x[n]) for n in ("q", "k", "v", "log_a", "S0")]
+    r = np.random.default_rng(29)
+    for i, n in enumerate(("dq", "dk", "dv", "dlog_a", "dS0")):
+        u = r.standard_normal(base[i].shape)
+
+        def f(h):
+            y = list(base)
+            y[i] = y[i] + h * u
+            o, S = bo.gated_recurrence(*y)
+            return np.sum(o * _np(dO)) + np.sum(S * _np(dS))
+        want, have = (f(1e-5) - f(-1e-5)) / 2e-5, np.sum(_np(d[n]) * u)
+        assert abs(want - have) <= 1e-6 + 1e-5 * np.sum(np.abs(_np(d[n]) * u)), n

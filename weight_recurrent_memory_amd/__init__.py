@@ -9,5 +9,5 @@ from .binding import (  # noqa: F401
     VARIANT_NAMES, FalconError, bwd_chunk, bwd_chunk_noalloc, decode_step, fwd_chunk,
     fwd_masked, fwd_recurrent, library_path, load_library,
 )
-from .gated import gated_decode_step, gated_fwd_chunk  # noqa: F401
+from .gated import gated_bwd_chunk, gated_decode_step, gated_fwd_chunk  # noqa: F401
 from .norms import norm_in, norm_in_bwd, norm_out, norm_out_bwd  # noqa: F401

@@ -94,6 +94,10 @@ def load_library():
     lib.falcon_gated_fwd_workspace_bytes.argtypes = [i] * 6
     lib.falcon_gated_fwd_chunk.restype = i
     lib.falcon_gated_fwd_chunk.argtypes = [i] * 6 + [vp] * 8 + [ull, vp]
+    lib.falcon_gated_bwd_workspace_bytes.restype = ull
+    lib.falcon_gated_bwd_workspace_bytes.argtypes = [i] * 6
+    lib.falcon_gated_bwd_chunk.restype = i
+    lib.falcon_gated_bwd_chunk.argtypes = [i] * 6 + [vp] * 13 + [ull, vp]
     lib.falcon_gated_decode_step.restype = i
     lib.falcon_gated_decode_step.argtypes = [i] * 5 + [vp] * 7
     _LIB = lib

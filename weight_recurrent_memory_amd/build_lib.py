@@ -26,7 +26,7 @@ SOURCES = ["falcon_api.cpp", "falcon_recurrent.hip", "falcon_decode.hip", "falco
            "falcon_chunk_w1.hip", "falcon_chunk_wy.hip", "falcon_chunk_wyb.hip",
            "falcon_chunk_ip.hip", "falcon_backward.hip", "falcon_masked.hip",
            "falcon_norm.hip", "falcon_gated.hip",
-           "falcon_gated_decode.hip"]
+           "falcon_gated_bwd.hip", "falcon_gated_decode.hip"]
 ARCH = os.environ.get("FALCON_OFFLOAD_ARCH", "gfx950")
 
 

@@ -815,3 +815,57 @@ FALCON_EXPORT int falcon_gated_fwd_chunk(int batch, int heads, int seqlen, int d
   return finish_launch(falcon::launch_gated(a, cut ? workspace : nullptr, cut ? need : 0,
                                             (hipStream_t)stream));
 }
+
+namespace {
+
+bool gated_bwd_sizes(int batch, int heads, int seqlen, int dk, int dv) {
+  const double segs = ((double)seqlen + 1023.0) / 1024.0;
+  return (double)batch * heads * (dk > dv ? dk : dv) * segs < 134217728.0;  // 2^27
+}
+
+// Bytes for any combination of the optional arguments: non-null stand-ins.
+size_t gated_bwd_need(int batch, int heads, int seqlen, int dk, int dv, int dtype) {
+  falcon::GatedBwdArgs a{batch, heads, seqlen, dk, dv, dtype};
+  float one = 0.0f;
+  a.log_a = a.dS_L = a.dlog_a = &one;
+  return falcon::gated_bwd_workspace_bytes(a);
+}
+
+}  // namespace
+
+FALCON_EXPORT unsigned long long falcon_gated_bwd_workspace_bytes(int batch, int heads, int seqlen,
+                                                                  int dk, int dv, int dtype) {
+  size_t N, es;
+  if (check_sizes(batch, heads, seqlen, dk, dv, dtype, &N, &es) != FALCON_OK || !supported_dim(dk) ||
+      !supported_dim(dv) || !gated_bwd_sizes(batch, heads, seqlen, dk, dv))
+    return 0;
+  return (unsigned long long)gated_bwd_need(batch, heads, seqlen, dk, dv, dtype);
+}
+
+FALCON_EXPORT int falcon_gated_bwd_chunk(int batch, int heads, int seqlen, int dk, int dv, int dtype,
+                                         const void* q, const void* k, const void* v,
+                                         const float* log_a, const float* S0, const float* dO,
+                                         const float* dS_L, float* dq, float* dk_out, float* dv_out,
+                                         float* dlog_a, float* dS0, void* workspace,
+                                         unsigned long long workspace_bytes, void* stream) {
+  size_t N, es;
+  int st = check_sizes(batch, heads, seqlen, dk, dv, dtype, &N, &es);
+  if (st != FALCON_OK) return st;
+  if (!q || !k || !v || !dO || !dq || !dk_out || !dv_out || !workspace || (dlog_a && !log_a))
+    return FALCON_ERR_INVALID_ARG;
+  const void* ptrs[] = {q, k, v, log_a, S0, dO, dS_L, dq, dk_out, dv_out, dlog_a, dS0, workspace};
+  if (!all_aligned16(ptrs)) return FALCON_ERR_INVALID_ARG;
+  if (!supported_dim(dk) || !supported_dim(dv)) return FALCON_ERR_UNSUPPORTED;
+  if (!gated_bwd_sizes(batch, heads, seqlen, dk, dv)) return FALCON_ERR_UNSUPPORTED;
+  const size_t need = gated_bwd_need(batch, heads, seqlen, dk, dv, dtype);
+  if (workspace_bytes < need) return FALCON_ERR_INVALID_ARG;
+  const size_t NH = N * heads, state = (size_t)batch * heads * dv * dk * 4;
+  const Range outs[] = {{dq, NH * dk * 4}, {dk_out, NH * dk * 4}, {dv_out, NH * dv * 4},
+                        {dlog_a, NH * 4}, {dS0, state}, {workspace, need}};
+  const Range ins[] = {{q, NH * dk * es}, {k, NH * dk * es}, {v, NH * dv * es}, {log_a, NH * 4},
+                       {S0, state}, {dO, NH * dv * 4}, {dS_L, state}};
+  if (any_overlap(outs, ins)) return FALCON_ERR_INVALID_ARG;
+  const falcon::GatedBwdArgs a{batch, heads, seqlen, dk, dv, dtype, q, k, v, log_a, S0, dO, dS_L,
+                               dq, dk_out, dv_out, dlog_a, dS0, static_cast<float*>(workspace)};
+  return finish_launch(falcon::launch_gated_bwd(a, (hipStream_t)stream));
+}

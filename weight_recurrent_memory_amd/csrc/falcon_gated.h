@@ -98,6 +98,10 @@ __device__ __forceinline__ void frag(const uint16_t* p, int stride, int row, int
   for (int i = 0; i < NP; ++i) f[i] = frag_bf16(p + i * stride + at<W>(row, col));
 }
 
+// Token of row `row` of the chunk of tokens t0..t0+63.
+template <bool REV>
+__device__ __forceinline__ long token(long t0, int row) { return t0 + (REV ? C - 1 - row : row); }
+
 // A chunk's rows of one input on its way to LDS: units of two tokens x 8 columns,
 // `units()` of them over the workgroup's threads.
 template <typename T, int D>
@@ -106,16 +110,18 @@ struct Stage {
   static constexpr int G = D / 8, UNITS = (C / 2) * G, N = (UNITS + NT - 1) / NT;
   Raw<T> r[N][2];
 
-  // tokens t0.. of rows of `ld` elements; those from L on are zero
+  // the 64 tokens from t0 on, rows of `ld` elements (REV: the last token first); tokens
+  // from L on are zero
+  template <bool REV>
   __device__ __forceinline__ void load(const T* x, long t0, long L, int ld) {
 #pragma unroll
     for (int i = 0; i < N; ++i) {
       const int u = threadIdx.x + i * NT;
-      const long t = t0 + 2 * (u / G);
       const bool mine = UNITS % NT == 0 || u < UNITS;
 #pragma unroll
       for (int j = 0; j < 2; ++j) {
-        if (mine && t + j < L) r[i][j].load(x + (t + j) * ld + 8 * (u % G));
+        const long t = token<REV>(t0, 2 * (u / G) + j);
+        if (mine && t < L) r[i][j].load(x + t * ld + 8 * (u % G));
         else r[i][j].zero();
       }
     }
@@ -181,19 +187,24 @@ __device__ __forceinline__ void mma(const bf16x8 (&a)[NA], const bf16x8 (&b)[NB]
       if (i + j < 3) acc = mfma16(a[i], b[j], acc);
 }
 
-// How a sequence is cut into segments, one workgroup each: `count` segments of `chunks`
-// chunks (the last one shorter).
-struct Segments {
-  int count, chunks;
+// How the sequences of a launch are cut into segments of whole chunks, one workgroup
+// (and block of z rows) each, and where the segments' states are.
+struct Span {
+  int segs, chunks;      // segments of a chain, chunks of a segment (the last one: fewer)
+  int writes;            // segments, in walking order, whose own write is formed
+  float* states;         // [chain][writes + 1][state]: the write of segment j in slot
+                         // j + 1, then the state that segment j starts from in slot j
+  float* decays;         // [chain][writes]: a segment's whole decay
 };
-// units: workgroups of one segment over all chains.
-inline Segments segments(long units, long seqlen) {
+// units: workgroups of one segment over all chains; most: chunks of a segment at most.
+// Segments until some 768 workgroups run, of four chunks at least.
+inline Span cut(long units, long seqlen, long most) {
   const long chunks = (seqlen + C - 1) / C;
   long n = units < 768 ? 768 / units : 1;
-  const long most = chunks / 4 > 1 ? chunks / 4 : 1;   // four chunks a segment at least
-  if (n > most) n = most;
-  const long per = (chunks + n - 1) / n;
-  return Segments{(int)((chunks + per - 1) / per), (int)per};
+  if (n > chunks / 4) n = chunks / 4 > 1 ? chunks / 4 : 1;
+  long per = (chunks + n - 1) / n;
+  if (per > most) per = most;
+  return Span{(int)((chunks + per - 1) / per), (int)per, 0, nullptr, nullptr};
 }
 
 // Workgroup x of a launch: value-row block and unit (chain, segment), the row blocks of
@@ -205,6 +216,15 @@ __device__ __forceinline__ bool place(int blocks, long units, int& block, long& 
   return unit < units;
 }
 inline unsigned grid_of(int blocks, long units) { return (unsigned)((units + 7) / 8 * 8 * blocks); }
+
+// z rows of a workgroup: 64, or 32 where both x and z are float32 and the planes at 128
+// columns would not fit the LDS.
+template <typename TX, typename TZ, int DX>
+constexpr int most_rows() { return sizeof(TX) == 4 && sizeof(TZ) == 4 && DX == 128 ? 32 : 64; }
+inline int rows_of(bool both_f32, int dx, int nz) {
+  const int most = both_f32 && dx == 128 ? 32 : 64;
+  return nz < most ? nz : most;
+}
 
 }  // namespace gated
 }  // namespace falcon

@@ -1,0 +1,482 @@
+// falcon_gated_chunk.h - the chunk kernels of the gated recurrence, forward and
+// backward.  One form serves all of them: with three sequences x, y (DX columns) and z,
+//   out_t = e_t U y_t + sum_{s<=t} D_ts (x_s . y_t) z_s        (a chunk of 64 tokens)
+//   U    <- d U + sum_s w_s z_s x_s^T
+// D_ts the decay from s to t, e_t from the chunk's start, w_s to its end, d the whole.
+//   forward   o  : x = k,  y = q,  z = v,   U = S
+//   backward  dq : x = v,  y = dO, z = k,   U = S^T
+//             dk : x = dO, y = v,  z = q,   U = R^T   last token first
+//             dv : x = q,  y = k,  z = dO,  U = R     last token first
+// with R the gradient of the state behind a token.  Walked last token first, a decay
+// from s back to t leaves out a_s and takes in a_t's successors: the sums of log decays
+// are exclusive in place of inclusive.
+//
+// Work.  A workgroup (4 waves) takes one segment of one chain for up to 64 z rows and
+// walks its chunks in order; wave w owns rows 16w..16w+15 of the chunk for out, and a part
+// of U (16 z rows at 64), which stays in its accumulators over the whole segment.  All
+// products are 16x16x32 bf16 MFMA over planes.  The scores are formed as P^T = X Y^T: a
+// lane then holds 8 scores of one token y_t, with the x rows taken in such an order that
+// these are the 8 k-slots the next product (Z^T P^T) wants, so decays, mask and split
+// happen in registers.  A chunk's x (by rows and by columns), z (by columns) and U's
+// planes lie in LDS; the next chunk's rows are loaded while this one is computed.
+#pragma once
+#include "falcon_gated.h"
+
+namespace falcon {
+namespace gated {
+
+struct ChunkArgs {
+  const void* x;         // [chain][L][DX]
+  const void* y;
+  const void* z;         // [chain][L][nz]
+  const float* log_a;    // [chain][L], or null
+  const float* U0;       // [chain][state] where the walk starts, or null
+  float* out;            // [chain][L][nz]
+  float* U_out;          // [chain][state], or null; may be U0
+  // gradients of the gates: the part of out_t . u_t that crosses a token's border,
+  // that is without s = t; [block][chain][L], or null
+  const void* u;         // [chain][L][nz]
+  float* dots;
+  long chains;
+  int seqlen, nz;
+};
+
+template <typename TX, typename TZ, int DX, int DZ>
+struct LdsState {
+  static constexpr int NPX = planes<TX>(), NPZ = planes<TZ>();
+  alignas(16) uint16_t xt[NPX][DX * C];             // x by columns
+  alignas(16) uint16_t zt[NPZ][DZ * C];             // z by columns
+  alignas(16) double g[C];                          // sums of log2 decays, row by row
+  alignas(16) float e[C];
+  alignas(16) float w[C];
+  float d;
+};
+template <typename TX, typename TZ, int DX, int DZ>
+struct Lds : LdsState<TX, TZ, DX, DZ> {
+  static constexpr int W = DX < 32 ? 32 : DX;       // k-slots come in 32s: zeros behind 16
+  alignas(16) uint16_t xn[planes<TX>()][C * W];     // x by rows
+  alignas(16) uint16_t s[3][DZ * W];                // U at the chunk's start
+};
+
+// The workgroup's U: wave w holds z rows 16 (w % NDT).. and NK tiles of 16 x columns.
+// A lane's part of a tile: z row lane % 16, x columns 4 (lane / 16) + 0..3.
+template <int DX, int DZ>
+struct State {
+  static constexpr int NDT = DZ / 16, WPD = 4 / NDT, ND = DX / 16, NK = (ND + WPD - 1) / WPD;
+  floatx4 t[NK];
+  static __device__ __forceinline__ int row() { return 16 * ((threadIdx.x >> 6) % NDT) + (threadIdx.x & 15); }
+  static __device__ __forceinline__ int tile(int j) { return ((threadIdx.x >> 6) / NDT) * NK + j; }
+  static __device__ __forceinline__ int col(int j) { return 16 * tile(j) + 4 * ((threadIdx.x & 63) >> 4); }
+  static __device__ __forceinline__ bool has(int j) { return WPD * NK == ND ? true : tile(j) < ND; }
+
+  // U: element (z, x) at z * sz + x * sx from the block's first row; null: zero
+  __device__ __forceinline__ void load(const float* U, long sz, long sx) {
+#pragma unroll
+    for (int j = 0; j < NK; ++j) {
+      t[j] = floatx4{0.f, 0.f, 0.f, 0.f};
+      if (!U || !has(j)) continue;
+      const float* p = U + row() * sz + col(j) * sx;
+      if (sx == 1) t[j] = *reinterpret_cast<const floatx4*>(p);
+      else t[j] = floatx4{p[0], p[sx], p[2 * sx], p[3 * sx]};
+    }
+  }
+  __device__ __forceinline__ void store(float* U, long sz, long sx) const {
+#pragma unroll
+    for (int j = 0; j < NK; ++j) {
+      if (!has(j)) continue;
+      float* p = U + row() * sz + col(j) * sx;
+      if (sx == 1) {
+        *reinterpret_cast<floatx4*>(p) = t[j];
+      } else {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) p[i * sx] = t[j][i];
+      }
+    }
+  }
+  template <int W>
+  __device__ __forceinline__ void to_planes(uint16_t (*s)[DZ * W]) const {
+#pragma unroll
+    for (int j = 0; j < NK; ++j) {
+      if (!has(j)) continue;
+      uint2 h, m, l;
+      split3(t[j].x, t[j].y, h.x, m.x, l.x);
+      split3(t[j].z, t[j].w, h.y, m.y, l.y);
+      const int i = at<W>(row(), col(j));
+      *reinterpret_cast<uint2*>(s[0] + i) = h;
+      *reinterpret_cast<uint2*>(s[1] + i) = m;
+      *reinterpret_cast<uint2*>(s[2] + i) = l;
+    }
+  }
+  // U <- d U + sum_s w_s z_s x_s^T
+  template <class L>
+  __device__ __forceinline__ void update(const L& lds) {
+    constexpr int NPX = L::NPX, NPZ = L::NPZ;
+    const int lane = threadIdx.x & 63, m = lane & 15, g8 = 8 * (lane >> 4);
+    const float d = lds.d;
+#pragma unroll
+    for (int j = 0; j < NK; ++j) t[j] *= d;
+#pragma unroll
+    for (int kk = 0; kk < C; kk += 32) {
+      bf16x8 z[NPZ], zw[3];
+      float v[8], w[8];
+      frag<NPZ, C>(lds.zt[0], DZ * C, row(), kk + g8, z);
+      values<NPZ>(z, v);
+      *reinterpret_cast<float4*>(w) = *reinterpret_cast<const float4*>(lds.w + kk + g8);
+      *reinterpret_cast<float4*>(w + 4) = *reinterpret_cast<const float4*>(lds.w + kk + g8 + 4);
+#pragma unroll
+      for (int e = 0; e < 8; ++e) v[e] *= w[e];
+      frag3(v, zw);
+      bf16x8 x[NK][NPX];
+#pragma unroll
+      for (int j = 0; j < NK; ++j) {
+        const int tj = has(j) ? tile(j) : 0;
+        frag<NPX, C>(lds.xt[0], DX * C, 16 * tj + m, kk + g8, x[j]);
+      }
+#pragma unroll
+      for (int p = 0; p < NPX; ++p)
+#pragma unroll
+        for (int q = 0; p + q < 3; ++q)
+#pragma unroll
+          for (int j = 0; j < NK; ++j) t[j] = mfma16(x[j][p], zw[q], t[j]);
+    }
+  }
+};
+
+// One wave's sums of a chunk's log decays, and their place in LDS.
+struct Decays {
+  double g, total;
+  template <bool REV>
+  __device__ __forceinline__ void sum(const float* log_a, long t0, long L) {
+    const double x = log2_decay(log_a, token<REV>(t0, threadIdx.x & 63), L);
+    g = wave_scan(x);
+    total = __shfl(g, 63, 64);
+    if (REV) g -= x;
+  }
+  template <class S>
+  __device__ __forceinline__ void store(S& lds) const {
+    const int lane = threadIdx.x & 63;
+    lds.g[lane] = g;
+    lds.e[lane] = exp2_of(g);
+    lds.w[lane] = exp2_of(total - g);
+    if (lane == 0) lds.d = exp2_of(total);
+  }
+};
+
+// A segment in walking order: its chunks' first tokens.
+template <bool REV>
+struct Walk {
+  long t0;
+  int n;
+  __device__ __forceinline__ Walk(const Span& sp, int step, long L) {
+    const long seg = REV ? sp.segs - 1 - step : step;
+    t0 = seg * sp.chunks * C;
+    const long left = (L - t0 + C - 1) / C;
+    n = left < sp.chunks ? (int)left : sp.chunks;
+  }
+  __device__ __forceinline__ long at(int c) const { return t0 + (long)(REV ? n - 1 - c : c) * C; }
+};
+
+// A segment's own write: U from zero.
+template <typename TX, typename TZ, int DX, int DZ, bool REV>
+__global__ __launch_bounds__(NT) void state_kernel(ChunkArgs a, Span sp) {
+  extern __shared__ __align__(16) unsigned char smem[];
+  using L = LdsState<TX, TZ, DX, DZ>;
+  L& lds = *reinterpret_cast<L*>(smem);
+  int blk;
+  long unit;
+  if (!place(a.nz / DZ, a.chains * sp.writes, blk, unit)) return;
+  const long chain = unit / sp.writes;
+  const int step = (int)(unit % sp.writes);
+  const int wave = threadIdx.x >> 6;
+  const long len = a.seqlen;
+  const Walk<REV> walk(sp, step, len);
+  const TX* x = static_cast<const TX*>(a.x) + chain * len * DX;
+  const TZ* z = static_cast<const TZ*>(a.z) + chain * len * a.nz + blk * DZ;
+  const float* la = a.log_a ? a.log_a + chain * len : nullptr;
+
+  Stage<TX, DX> sx;
+  Stage<TZ, DZ> sz;
+  State<DX, DZ> st;
+  Decays dec;
+  double total = 0.0;
+  st.load(nullptr, 0, 1);
+  sx.template load<REV>(x, walk.at(0), len, DX);
+  sz.template load<REV>(z, walk.at(0), len, a.nz);
+  if (wave == 0) dec.sum<REV>(la, walk.at(0), len);
+  for (int c = 0; c < walk.n; ++c) {
+    if (c) __syncthreads();
+    sx.template store<C>(nullptr, lds.xt[0]);
+    sz.template store<C>(nullptr, lds.zt[0]);
+    if (wave == 0) {
+      dec.store(lds);
+      total += dec.total;
+    }
+    __syncthreads();
+    if (c + 1 < walk.n) {
+      const long t = walk.at(c + 1);
+      sx.template load<REV>(x, t, len, DX);
+      sz.template load<REV>(z, t, len, a.nz);
+      if (wave == 0) dec.sum<REV>(la, t, len);
+    }
+    st.update(lds);
+  }
+  st.store(sp.states + ((chain * (sp.writes + 1) + step + 1) * a.nz + (long)blk * DZ) * DX, DX, 1);
+  if (threadIdx.x == 0 && blk == 0) sp.decays[unit] = exp2_of(total);
+}
+
+// Four consecutive inputs as floats.
+__device__ __forceinline__ floatx4 load4(const uint16_t* p) {
+  const uint2 u = *reinterpret_cast<const uint2*>(p);
+  return floatx4{__uint_as_float(u.x << 16), __uint_as_float(u.x & 0xFFFF0000u),
+                 __uint_as_float(u.y << 16), __uint_as_float(u.y & 0xFFFF0000u)};
+}
+__device__ __forceinline__ floatx4 load4(const float* p) { return *reinterpret_cast<const floatx4*>(p); }
+
+// GRAD: U is kept transposed in memory ([x][z], a state's own layout for dq and dk), and
+// dots are written.
+template <typename TX, typename TY, typename TZ, int DX, int DZ, bool REV, bool GRAD>
+__global__ __launch_bounds__(NT) void chunk_kernel(ChunkArgs a, Span sp) {
+  extern __shared__ __align__(16) unsigned char smem[];
+  using L = Lds<TX, TZ, DX, DZ>;
+  constexpr int NPX = L::NPX, NPY = planes<TY>(), NPZ = L::NPZ;
+  constexpr int W = L::W, NQ = W / 32, NDT = DZ / 16;
+  L& lds = *reinterpret_cast<L*>(smem);
+  int blk;
+  long unit;
+  if (!place(a.nz / DZ, a.chains * sp.segs, blk, unit)) return;
+  const long chain = unit / sp.segs;
+  const int step = (int)(unit % sp.segs);
+  const int wave = threadIdx.x >> 6, lane = threadIdx.x & 63;
+  const int m = lane & 15, g = lane >> 4;
+  const long len = a.seqlen;
+  const Walk<REV> walk(sp, step, len);
+  const TX* x = static_cast<const TX*>(a.x) + chain * len * DX;
+  const TY* y = static_cast<const TY*>(a.y) + chain * len * DX;
+  const TZ* z = static_cast<const TZ*>(a.z) + chain * len * a.nz + blk * DZ;
+  const TZ* u = GRAD ? static_cast<const TZ*>(a.u) + chain * len * a.nz + blk * DZ : nullptr;
+  const float* la = a.log_a ? a.log_a + chain * len : nullptr;
+  float* out = a.out + chain * len * a.nz + blk * DZ;
+  const long U_sz = GRAD ? 1 : DX, U_sx = GRAD ? a.nz : 1, U_blk = (long)blk * DZ * U_sz;
+  const long state = (long)a.nz * DX;
+
+  Stage<TX, DX> sx;
+  Stage<TZ, DZ> sz;
+  State<DX, DZ> st;
+  Decays dec;
+  Raw<TY> ry[NQ];
+  auto load_y = [&](long base) {
+    const long t = token<REV>(base, 16 * wave + m);
+#pragma unroll
+    for (int i = 0; i < NQ; ++i) {
+      if (t < len && 32 * i + 8 * g < DX) ry[i].load(y + t * DX + 32 * i + 8 * g);
+      else ry[i].zero();
+    }
+  };
+  sx.template load<REV>(x, walk.at(0), len, DX);
+  sz.template load<REV>(z, walk.at(0), len, a.nz);
+  load_y(walk.at(0));
+  if (wave == 0) dec.sum<REV>(la, walk.at(0), len);
+  if (sp.segs > 1) st.load(sp.states + (chain * (sp.writes + 1) + step) * state + U_blk, U_sz, U_sx);
+  else st.load(a.U0 ? a.U0 + chain * state + U_blk : nullptr, U_sz, U_sx);
+  if (DX < W) {      // k-slots behind the last column
+    for (int i = threadIdx.x; i < NPX * C * W / 8; i += NT) reinterpret_cast<uint4*>(lds.xn[0])[i] = uint4{0u, 0u, 0u, 0u};
+    for (int i = threadIdx.x; i < 3 * DZ * W / 8; i += NT) reinterpret_cast<uint4*>(lds.s[0])[i] = uint4{0u, 0u, 0u, 0u};
+    __syncthreads();
+  }
+
+  for (int c = 0; c < walk.n; ++c) {
+    if (c) __syncthreads();
+    sx.template store<W>(lds.xn[0], lds.xt[0]);
+    sz.template store<C>(nullptr, lds.zt[0]);
+    st.template to_planes<W>(lds.s);
+    if (wave == 0) dec.store(lds);
+    bf16x8 yf[NQ][NPY];
+#pragma unroll
+    for (int i = 0; i < NQ; ++i) {
+      uint4 f[NPY];
+      ry[i].split(f);
+#pragma unroll
+      for (int p = 0; p < NPY; ++p) yf[i][p] = __builtin_bit_cast(bf16x8, f[p]);
+    }
+    __syncthreads();
+    if (c + 1 < walk.n) {
+      const long t = walk.at(c + 1);
+      sx.template load<REV>(x, t, len, DX);
+      sz.template load<REV>(z, t, len, a.nz);
+      load_y(t);
+      if (wave == 0) dec.sum<REV>(la, t, len);
+    }
+
+    // out^T: z rows x this wave's 16 tokens; first U's part
+    floatx4 acc[NDT];
+#pragma unroll
+    for (int i = 0; i < NDT; ++i) acc[i] = floatx4{0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+    for (int i = 0; i < NQ; ++i) {
+      bf16x8 s[NDT][3];
+#pragma unroll
+      for (int d = 0; d < NDT; ++d) frag<3, W>(lds.s[0], DZ * W, 16 * d + m, 32 * i + 8 * g, s[d]);
+#pragma unroll
+      for (int p = 0; p < 3; ++p)
+#pragma unroll
+        for (int r = 0; r < NPY; ++r)
+          if (p + r < 3) {
+#pragma unroll
+            for (int d = 0; d < NDT; ++d) acc[d] = mfma16(s[d][p], yf[i][r], acc[d]);
+          }
+    }
+    const int ti = 16 * wave + m;               // this lane's row of the chunk
+    const long t = token<REV>(walk.at(c), ti);
+    const float e = lds.e[ti];
+    const double Gt = lds.g[ti];
+#pragma unroll
+    for (int d = 0; d < NDT; ++d) acc[d] *= e;
+    // then the chunk's own tokens, 32 at a time; none behind the wave's last row
+    float same = 0.0f;                          // x_t . y_t, where this lane holds it
+#pragma unroll
+    for (int kk = 0; kk < C; kk += 32) {
+      if (kk > 16 * wave + 15) break;
+      float v[8];
+#pragma unroll
+      for (int j = 0; j < 2; ++j) {
+        // row m of this tile: chunk row kk + 8 (m / 4) + 4 j + m % 4
+        floatx4 p = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+        for (int i = 0; i < NQ; ++i) {
+          bf16x8 xf[NPX];
+          frag<NPX, W>(lds.xn[0], C * W, kk + 8 * (m >> 2) + 4 * j + (m & 3), 32 * i + 8 * g, xf);
+          mma<NPX, NPY>(xf, yf[i], p);
+        }
+#pragma unroll
+        for (int r = 0; r < 4; ++r) {
+          const int s = kk + 8 * g + 4 * j + r;
+          const float dcy = exp2_of(Gt - lds.g[s]);
+          if (GRAD) {                           // s = t is added behind the dots
+            v[4 * j + r] = s < ti ? p[r] * dcy : 0.0f;
+            same = s == ti ? p[r] : same;
+          } else {
+            // (walked backward too a token's own term has no decay: dcy = 1)
+            v[4 * j + r] = s <= ti ? p[r] * dcy : 0.0f;
+          }
+        }
+      }
+      bf16x8 pf[3];
+      frag3(v, pf);
+      bf16x8 zf[NDT][NPZ];
+#pragma unroll
+      for (int d = 0; d < NDT; ++d) frag<NPZ, C>(lds.zt[0], DZ * C, 16 * d + m, kk + 8 * g, zf[d]);
+#pragma unroll
+      for (int p = 0; p < NPZ; ++p)
+#pragma unroll
+        for (int r = 0; p + r < 3; ++r)
+#pragma unroll
+          for (int d = 0; d < NDT; ++d) acc[d] = mfma16(zf[d][p], pf[r], acc[d]);
+    }
+    if (GRAD) {
+      // one of the four lanes of a row holds x_t . y_t, the others 0
+      same += __shfl_xor(same, 16, 64);
+      same += __shfl_xor(same, 32, 64);
+      float dot = 0.0f;
+      if (t < len) {
+#pragma unroll
+        for (int d = 0; d < NDT; ++d) {
+          const floatx4 uv = load4(u + t * a.nz + 16 * d + 4 * g);
+          const floatx4 zv = load4(z + t * a.nz + 16 * d + 4 * g);
+          dot += acc[d].x * uv.x + acc[d].y * uv.y + acc[d].z * uv.z + acc[d].w * uv.w;
+          acc[d] += same * zv;
+        }
+      }
+      dot += __shfl_xor(dot, 16, 64);
+      dot += __shfl_xor(dot, 32, 64);
+      if (a.dots && g == 0 && t < len) a.dots[(blk * a.chains + chain) * len + t] = dot;
+    }
+    if (t < len) {
+#pragma unroll
+      for (int d = 0; d < NDT; ++d)
+        *reinterpret_cast<floatx4*>(out + t * a.nz + 16 * d + 4 * g) = acc[d];
+    }
+    st.update(lds);
+  }
+  if (a.U_out && step == sp.segs - 1) st.store(a.U_out + chain * state + U_blk, U_sz, U_sx);
+}
+
+// A kernel with more than 64 KB of LDS has to be told so (about a microsecond a call;
+// nothing is kept here).
+template <class K>
+hipError_t lds_limit(K kernel, size_t bytes) {
+  if (bytes <= 65536) return hipSuccess;
+  return hipFuncSetAttribute(reinterpret_cast<const void*>(kernel),
+                             hipFuncAttributeMaxDynamicSharedMemorySize, (int)bytes);
+}
+
+template <typename TX, typename TZ, int DX, int DZ, bool REV>
+hipError_t go_state(const ChunkArgs& a, const Span& sp, hipStream_t stream) {
+  constexpr size_t bytes = sizeof(LdsState<TX, TZ, DX, DZ>);
+  auto kernel = state_kernel<TX, TZ, DX, DZ, REV>;
+  const hipError_t e = lds_limit(kernel, bytes);
+  if (e != hipSuccess) return e;
+  hipLaunchKernelGGL(kernel, dim3(grid_of(a.nz / DZ, a.chains * sp.writes)), dim3(NT), bytes, stream, a, sp);
+  return hipGetLastError();
+}
+template <typename TX, typename TY, typename TZ, int DX, int DZ, bool REV, bool GRAD>
+hipError_t go_chunk(const ChunkArgs& a, const Span& sp, hipStream_t stream) {
+  constexpr size_t bytes = sizeof(Lds<TX, TZ, DX, DZ>);
+  auto kernel = chunk_kernel<TX, TY, TZ, DX, DZ, REV, GRAD>;
+  const hipError_t e = lds_limit(kernel, bytes);
+  if (e != hipSuccess) return e;
+  hipLaunchKernelGGL(kernel, dim3(grid_of(a.nz / DZ, a.chains * sp.segs)), dim3(NT), bytes, stream, a, sp);
+  return hipGetLastError();
+}
+
+// f(size, rows) as constants for dx columns and blocks of z rows of nz.
+template <typename TX, typename TZ, class F>
+hipError_t with_sizes(int dx, int nz, F&& f) {
+  auto rows = [&](auto d) {
+    constexpr int DX = decltype(d)::value;
+    switch (rows_of(sizeof(TX) == 4 && sizeof(TZ) == 4, DX, nz)) {
+      case 16: return f(d, std::integral_constant<int, 16>());
+      case 32: return f(d, std::integral_constant<int, 32>());
+      case 64:
+        if constexpr (most_rows<TX, TZ, DX>() == 64) return f(d, std::integral_constant<int, 64>());
+    }
+    return hipErrorInvalidValue;
+  };
+  switch (dx) {
+    case 16: return rows(std::integral_constant<int, 16>());
+    case 32: return rows(std::integral_constant<int, 32>());
+    case 64: return rows(std::integral_constant<int, 64>());
+    case 128: return rows(std::integral_constant<int, 128>());
+  }
+  return hipErrorInvalidValue;
+}
+
+// The states that segments start from: every segment's own write, then the recurrence
+// over segments (segments_kernel in falcon_gated.hip).
+hipError_t launch_segments(const float* U0, const Span& sp, long chains, long state, hipStream_t stream);
+
+template <typename TX, typename TZ, bool REV>
+hipError_t launch_states(const ChunkArgs& a, int dx, const Span& sp, hipStream_t stream) {
+  if (sp.writes == 0) return hipSuccess;
+  const hipError_t e = with_sizes<TX, TZ>(dx, a.nz, [&](auto d, auto r) {
+    return go_state<TX, TZ, decltype(d)::value, decltype(r)::value, REV>(a, sp, stream);
+  });
+  return e != hipSuccess ? e : launch_segments(a.U0, sp, a.chains, (long)a.nz * dx, stream);
+}
+
+// Floats of a span's workspace.
+inline size_t span_floats(const Span& sp, long chains, long state) {
+  return sp.writes ? (size_t)chains * ((size_t)(sp.writes + 1) * state + sp.writes) : 0;
+}
+// Takes them from p, which moves behind (to a multiple of 16 bytes).
+inline void place_span(Span& sp, long chains, long state, float*& p) {
+  if (sp.writes == 0) return;
+  sp.states = p;
+  sp.decays = p + (size_t)chains * (sp.writes + 1) * state;
+  p += (span_floats(sp, chains, state) + 3) / 4 * 4;
+}
+inline size_t span_bytes(const Span& sp, long chains, long state) {
+  return (span_floats(sp, chains, state) + 3) / 4 * 16;
+}
+
+}  // namespace gated
+}  // namespace falcon

@@ -139,6 +139,26 @@ struct GatedArgs {
 // (0: one segment in any case); without it every chain is one segment.
 size_t gated_workspace_bytes(const GatedArgs& a);
 hipError_t launch_gated(const GatedArgs& a, void* ws, size_t ws_bytes, hipStream_t stream);
+struct GatedBwdArgs {
+  int batch, heads, seqlen, ndk, ndv;
+  int dtype;
+  const void* q;
+  const void* k;
+  const void* v;
+  const float* log_a;    // may be null
+  const float* S0;       // may be null
+  const float* dO;
+  const float* dS_L;     // may be null
+  float* dq;
+  float* dk;
+  float* dv;
+  float* dlog_a;         // null exactly when log_a is
+  float* dS0;            // may be null
+  float* workspace;      // gated_bwd_workspace_bytes(...)
+};
+// (of the pointers only log_a, dS_L and dlog_a count, null or not)
+size_t gated_bwd_workspace_bytes(const GatedBwdArgs& a);
+hipError_t launch_gated_bwd(const GatedBwdArgs& a, hipStream_t stream);
 struct GatedDecodeArgs {
   int nseq, heads, dk, dv;
   int dtype;

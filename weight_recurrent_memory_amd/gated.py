@@ -67,6 +67,37 @@ def gated_fwd_chunk(q, k, v, log_a=None, *, S0=None, out=None, S_out=None, retur
     return (out, S_out) if return_state else out
 
 
+def gated_bwd_chunk(q, k, v, log_a, dO, *, S0=None, dS_L=None, stream=None, workspace="auto"):
+    """Gradients of sum <dO, o> + <dS_L, S_L>: a dict of float32 tensors dq, dk, dv, and
+    dlog_a / dS0 when log_a / S0 are given.  dO [B,H,L,dv] and dS_L [B,H,dv,dk] float32.
+    workspace: "auto", or a device tensor of falcon_gated_bwd_workspace_bytes(...)."""
+    import torch
+    lib = _b.load_library()
+    B, H, L, dk, dv, dcode = _inputs(torch, q, k, v, log_a, S0)
+    dev, f32 = q.device, torch.float32
+    if dO is None:
+        raise ValueError("dO must be given")
+    _b._check(torch, "dO", dO, (B, H, L, dv), f32, dev)
+    _b._check(torch, "dS_L", dS_L, (B, H, dv, dk), f32, dev)
+    with _b._guard(torch, dev, stream):
+        res = dict(dq=torch.empty((B, H, L, dk), device=dev, dtype=f32),
+                   dk=torch.empty((B, H, L, dk), device=dev, dtype=f32),
+                   dv=torch.empty((B, H, L, dv), device=dev, dtype=f32))
+        if log_a is not None:
+            res["dlog_a"] = torch.empty((B, H, L), device=dev, dtype=f32)
+        if S0 is not None:
+            res["dS0"] = torch.empty((B, H, dv, dk), device=dev, dtype=f32)
+        need = lib.falcon_gated_bwd_workspace_bytes(B, H, L, dk, dv, dcode)
+        ws, wp, wb = _workspace(torch, workspace, max(int(need), 16), dev)
+        status = lib.falcon_gated_bwd_chunk(
+            B, H, L, dk, dv, dcode, _b._ptr(q), _b._ptr(k), _b._ptr(v), _b._ptr(log_a), _b._ptr(S0),
+            _b._ptr(dO), _b._ptr(dS_L), _b._ptr(res["dq"]), _b._ptr(res["dk"]), _b._ptr(res["dv"]),
+            _b._ptr(res.get("dlog_a")), _b._ptr(res.get("dS0")), wp, wb,
+            _b._stream(torch, dev, stream))
+    _b._raise(lib, "falcon_gated_bwd_chunk", status)
+    return res
+
+
 def gated_decode_step(S, q, k, v, log_a=None, *, out=None, stream=None):
     """One token: S [N,H,dv,dk] float32 is updated in place, returns o [N,H,dv] float32.
     q, k [N,H,dk], v [N,H,dv] bfloat16 or float32; log_a [N,H] float32, None: no decay."""
