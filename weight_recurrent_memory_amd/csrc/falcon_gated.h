@@ -24,14 +24,13 @@ constexpr int NT = 256;        // threads of a workgroup, 16 tokens of a chunk a
 template <typename T>
 constexpr int planes() { return sizeof(T) == 2 ? 1 : 3; }
 
-// Element offset of (row, col) in a plane of rows of W (32, 64 or 128) bf16: groups of
-// 8 elements (16 bytes) are XORed with bits of the row, so that the 16-byte reads of 8
-// consecutive rows, of rows 0-3 and 8-11 together, and the transposing writes to rows 8
-// apart each fall into different banks.
+// Element offset of (row, col) in a plane of rows of W (16 to 128) bf16: groups of 8
+// elements (16 bytes) are XORed with bits of the row, so that the 16-byte reads of 8
+// consecutive rows, of rows 0-3 and 8-11 together, and the transposed reads of 4 rows each
+// fall into different banks.  Rows 16 apart are XORed alike: one address serves them all.
 template <int W>
 __device__ __forceinline__ int at(int row, int col) {
-  const int x = row >> 3;
-  const int f = (row & 7) ^ (((x & 1) << 2) | (x & 2) | ((x >> 2) & 1));
+  const int f = (row & 7) ^ (((row >> 3) & 1) << 2);
   return row * W + (((col >> 3) ^ (f & (W / 8 - 1))) << 3) + (col & 7);
 }
 
@@ -102,13 +101,33 @@ __device__ __forceinline__ void frag(const uint16_t* p, int stride, int row, int
 template <bool REV>
 __device__ __forceinline__ long token(long t0, int row) { return t0 + (REV ? C - 1 - row : row); }
 
-// A chunk's rows of one input on its way to LDS: units of two tokens x 8 columns,
-// `units()` of them over the workgroup's threads.
+typedef short short4_t __attribute__((ext_vector_type(4)));
+
+// One MFMA operand fragment (NP planes) of the transposed plane: columns col..col+15, one
+// a lane of 16, and rows row..row+7 for each group of 16 lanes.  ds_read_b64_tr_b16: in a
+// group of 16 lanes, lane i gives the address of 4 columns from 4 (i % 4) on of row i / 4,
+// and lane i gets column i of the 4 rows.
+template <int NP, int W>
+__device__ __forceinline__ void frag_t(const uint16_t* p, int stride, int row, int col,
+                                       bf16x8 (&f)[NP]) {
+  typedef __attribute__((address_space(3))) short4_t* lds_ptr;
+  const int m = threadIdx.x & 15;
+  const int a = at<W>(row + (m >> 2), col + 4 * (m & 3)), b = at<W>(row + 4 + (m >> 2), col + 4 * (m & 3));
+#pragma unroll
+  for (int i = 0; i < NP; ++i) {
+    struct { short4_t lo, hi; } x;
+    x.lo = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_ptr)(p + i * stride + a));
+    x.hi = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_ptr)(p + i * stride + b));
+    f[i] = __builtin_bit_cast(bf16x8, x);
+  }
+}
+
+// A chunk's rows of one input on its way to LDS: units of 8 columns of a token.
 template <typename T, int D>
 struct Stage {
   static constexpr int NP = planes<T>();
-  static constexpr int G = D / 8, UNITS = (C / 2) * G, N = (UNITS + NT - 1) / NT;
-  Raw<T> r[N][2];
+  static constexpr int G = D / 8, UNITS = C * G, N = (UNITS + NT - 1) / NT;
+  Raw<T> r[N];
 
   // the 64 tokens from t0 on, rows of `ld` elements (REV: the last token first); tokens
   // from L on are zero
@@ -117,44 +136,23 @@ struct Stage {
 #pragma unroll
     for (int i = 0; i < N; ++i) {
       const int u = threadIdx.x + i * NT;
-      const bool mine = UNITS % NT == 0 || u < UNITS;
-#pragma unroll
-      for (int j = 0; j < 2; ++j) {
-        const long t = token<REV>(t0, 2 * (u / G) + j);
-        if (mine && t < L) r[i][j].load(x + t * ld + 8 * (u % G));
-        else r[i][j].zero();
-      }
+      const long t = token<REV>(t0, u / G);
+      if ((UNITS % NT == 0 || u < UNITS) && t < L) r[i].load(x + t * ld + 8 * (u % G));
+      else r[i].zero();
     }
   }
-  // to rows[token][column] (W wide, or null) and cols[column][token] (64 wide, or null)
+  // to planes of rows W wide
   template <int W>
-  __device__ __forceinline__ void store(uint16_t* rows, uint16_t* cols) const {
+  __device__ __forceinline__ void store(uint16_t* rows) const {
 #pragma unroll
     for (int i = 0; i < N; ++i) {
       const int u = threadIdx.x + i * NT;
       if (UNITS % NT != 0 && u >= UNITS) continue;
-      const int s = 2 * (u / G), c = 8 * (u % G);
-      uint4 a[NP], b[NP];
-      r[i][0].split(a);
-      r[i][1].split(b);
+      uint4 a[NP];
+      r[i].split(a);
 #pragma unroll
-      for (int p = 0; p < NP; ++p) {
-        if (rows) {
-          *reinterpret_cast<uint4*>(rows + p * C * W + at<W>(s, c)) = a[p];
-          *reinterpret_cast<uint4*>(rows + p * C * W + at<W>(s + 1, c)) = b[p];
-        }
-        if (cols) {
-          const uint32_t x[4] = {a[p].x, a[p].y, a[p].z, a[p].w};
-          const uint32_t y[4] = {b[p].x, b[p].y, b[p].z, b[p].w};
-#pragma unroll
-          for (int e = 0; e < 8; ++e) {
-            // (token s, token s + 1) of column c + e
-            const uint32_t lo = e & 1 ? x[e / 2] >> 16 : x[e / 2] & 0xFFFFu;
-            const uint32_t hi = e & 1 ? y[e / 2] & 0xFFFF0000u : y[e / 2] << 16;
-            *reinterpret_cast<uint32_t*>(cols + p * D * C + at<C>(c + e, s)) = lo | hi;
-          }
-        }
-      }
+      for (int p = 0; p < NP; ++p)
+        *reinterpret_cast<uint4*>(rows + p * C * W + at<W>(u / G, 8 * (u % G))) = a[p];
     }
   }
 };
@@ -217,14 +215,8 @@ __device__ __forceinline__ bool place(int blocks, long units, int& block, long& 
 }
 inline unsigned grid_of(int blocks, long units) { return (unsigned)((units + 7) / 8 * 8 * blocks); }
 
-// z rows of a workgroup: 64, or 32 where both x and z are float32 and the planes at 128
-// columns would not fit the LDS.
-template <typename TX, typename TZ, int DX>
-constexpr int most_rows() { return sizeof(TX) == 4 && sizeof(TZ) == 4 && DX == 128 ? 32 : 64; }
-inline int rows_of(bool both_f32, int dx, int nz) {
-  const int most = both_f32 && dx == 128 ? 32 : 64;
-  return nz < most ? nz : most;
-}
+// z rows of a workgroup.
+inline int rows_of(int nz) { return nz < 64 ? nz : 64; }
 
 }  // namespace gated
 }  // namespace falcon

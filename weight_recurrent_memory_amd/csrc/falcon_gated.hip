@@ -4,8 +4,6 @@
 // segments until some 768 workgroups run: a first kernel forms each segment's own write to
 // the state from zero (k and v only), a second runs the short recurrence over segments,
 // and the main kernel starts each segment from its state.
-#include <type_traits>
-
 #include "falcon_gated_chunk.h"
 
 namespace falcon {
@@ -50,7 +48,7 @@ namespace {
 
 // One workgroup's walk takes any number of chunks.
 Span cut_of(const GatedArgs& a) {
-  const long blocks = a.dv / rows_of(a.dtype == 1, a.dk, a.dv);
+  const long blocks = a.dv / rows_of(a.dv);
   Span sp = cut((long)a.batch * a.heads * blocks, a.seqlen, 1l << 40);
   sp.writes = sp.segs - 1;
   return sp;
@@ -62,7 +60,7 @@ hipError_t run(const GatedArgs& a, const Span& sp, hipStream_t stream) {
                     (long)a.batch * a.heads, a.seqlen, a.dv};
   const hipError_t e = launch_states<T, T, false>(c, a.dk, sp, stream);
   if (e != hipSuccess) return e;
-  return with_sizes<T, T>(a.dk, a.dv, [&](auto d, auto r) {
+  return with_sizes(a.dk, a.dv, [&](auto d, auto r) {
     return go_chunk<T, T, T, decltype(d)::value, decltype(r)::value, false, false>(c, sp, stream);
   });
 }

@@ -11,8 +11,6 @@
 // leave its rounding behind; then inside a segment
 //   dlog_a_t = X + sum_{t'>=t} r_t' - sum_{s>=t} c_s,   X = <R, S> at the segment's end,
 // summed in float64.  Segments are 16 chunks at most, so that an X is never far away.
-#include <type_traits>
-
 #include "falcon_gated_chunk.h"
 
 namespace falcon {
@@ -24,9 +22,9 @@ constexpr int kMostChunks = 16;            // of a segment: 1024 tokens
 struct GateArgs {
   const float* log_a;
   const float* dS_L;       // or null
-  const float* r;          // [rb][chain][L]
-  const float* c;          // [cb][chain][L]
-  int rb, cb;
+  const float* r;          // [block][chain][L]
+  const float* c;
+  int blocks;
   float* dlog_a;
   long chains, state;
   int seqlen;
@@ -67,8 +65,10 @@ __global__ __launch_bounds__(NT) void gate_kernel(GateArgs a, Span s, Span r) {
     const long t = end - 1 - 4 * (long)threadIdx.x - j;
     double rr = 0.0, cc = 0.0;
     if (t >= t0) {
-      for (int b = 0; b < a.rb; ++b) rr += a.r[(b * a.chains + chain) * len + t];
-      for (int b = 0; b < a.cb; ++b) cc += a.c[(b * a.chains + chain) * len + t];
+      for (int b = 0; b < a.blocks; ++b) {
+        rr += a.r[(b * a.chains + chain) * len + t];
+        cc += a.c[(b * a.chains + chain) * len + t];
+      }
     }
     mine += rr - cc;
     sum[j] = mine;
@@ -91,7 +91,7 @@ __global__ __launch_bounds__(NT) void gate_kernel(GateArgs a, Span s, Span r) {
 // and its workspace.
 struct Plan {
   Span s, r;
-  int rb, cb;              // blocks of dq and of dk columns
+  int blocks;              // of dq's and dk's columns
   long chains, state;
   size_t bytes() const {
     return span_bytes(s, chains, state) + span_bytes(r, chains, state);
@@ -100,12 +100,10 @@ struct Plan {
 
 Plan plan_of(const GatedBwdArgs& a) {
   Plan p;
-  const bool f32 = a.dtype == 1;
   p.chains = (long)a.batch * a.heads;
   p.state = (long)a.ndv * a.ndk;
-  p.rb = a.ndk / rows_of(f32, a.ndv, a.ndk);                    // x = v, z = k
-  p.cb = a.ndk / rows_of(f32, a.ndv, a.ndk);                    // x = dO, z = q
-  p.s = cut(p.chains * p.rb, a.seqlen, kMostChunks);
+  p.blocks = a.ndk / rows_of(a.ndk);
+  p.s = cut(p.chains * p.blocks, a.seqlen, kMostChunks);
   p.r = p.s;
   // the end's state only where its gradient meets it
   p.s.writes = a.dS_L && a.dlog_a ? p.s.segs : p.s.segs - 1;
@@ -113,7 +111,7 @@ Plan plan_of(const GatedBwdArgs& a) {
   return p;
 }
 size_t dot_floats(const Plan& p, const GatedBwdArgs& a) {
-  return a.dlog_a ? (size_t)(p.rb + p.cb) * p.chains * a.seqlen : 0;
+  return a.dlog_a ? (size_t)2 * p.blocks * p.chains * a.seqlen : 0;
 }
 
 template <typename T>
@@ -122,28 +120,28 @@ hipError_t run(const GatedBwdArgs& a, Plan p, hipStream_t stream) {
   place_span(p.s, p.chains, p.state, w);
   place_span(p.r, p.chains, p.state, w);
   float* r = a.dlog_a ? w : nullptr;
-  float* c = a.dlog_a ? w + (size_t)p.rb * p.chains * a.seqlen : nullptr;
+  float* c = a.dlog_a ? w + (size_t)p.blocks * p.chains * a.seqlen : nullptr;
   hipError_t e;
   const ChunkArgs S{a.k, nullptr, a.v, a.log_a, a.S0, nullptr, nullptr, nullptr, nullptr, p.chains, a.seqlen, a.ndv};
   if ((e = launch_states<T, T, false>(S, a.ndk, p.s, stream)) != hipSuccess) return e;
   const ChunkArgs R{a.q, nullptr, a.dO, a.log_a, a.dS_L, nullptr, nullptr, nullptr, nullptr, p.chains, a.seqlen, a.ndv};
   if ((e = launch_states<T, float, true>(R, a.ndk, p.r, stream)) != hipSuccess) return e;
   const ChunkArgs dq{a.v, a.dO, a.k, a.log_a, a.S0, a.dq, nullptr, a.q, r, p.chains, a.seqlen, a.ndk};
-  e = with_sizes<T, T>(a.ndv, a.ndk, [&](auto d, auto z) {
+  e = with_sizes(a.ndv, a.ndk, [&](auto d, auto z) {
     return go_chunk<T, float, T, decltype(d)::value, decltype(z)::value, false, true>(dq, p.s, stream);
   });
   if (e != hipSuccess) return e;
   const ChunkArgs dk{a.dO, a.v, a.q, a.log_a, a.dS_L, a.dk, nullptr, a.k, c, p.chains, a.seqlen, a.ndk};
-  e = with_sizes<float, T>(a.ndv, a.ndk, [&](auto d, auto z) {
+  e = with_sizes(a.ndv, a.ndk, [&](auto d, auto z) {
     return go_chunk<float, T, T, decltype(d)::value, decltype(z)::value, true, true>(dk, p.r, stream);
   });
   if (e != hipSuccess) return e;
   const ChunkArgs dv{a.q, a.k, a.dO, a.log_a, a.dS_L, a.dv, a.dS0, nullptr, nullptr, p.chains, a.seqlen, a.ndv};
-  e = with_sizes<T, float>(a.ndk, a.ndv, [&](auto d, auto z) {
+  e = with_sizes(a.ndk, a.ndv, [&](auto d, auto z) {
     return go_chunk<T, T, float, decltype(d)::value, decltype(z)::value, true, false>(dv, p.r, stream);
   });
   if (e != hipSuccess || !a.dlog_a) return e;
-  const GateArgs g{a.log_a, a.dS_L, r, c, p.rb, p.cb, a.dlog_a, p.chains, p.state, a.seqlen};
+  const GateArgs g{a.log_a, a.dS_L, r, c, p.blocks, a.dlog_a, p.chains, p.state, a.seqlen};
   hipLaunchKernelGGL(gate_kernel, dim3((unsigned)(p.chains * p.s.segs)), dim3(NT), 0, stream, g, p.s, p.r);
   return hipGetLastError();
 }

@@ -17,9 +17,11 @@
 // products are 16x16x32 bf16 MFMA over planes.  The scores are formed as P^T = X Y^T: a
 // lane then holds 8 scores of one token y_t, with the x rows taken in such an order that
 // these are the 8 k-slots the next product (Z^T P^T) wants, so decays, mask and split
-// happen in registers.  A chunk's x (by rows and by columns), z (by columns) and U's
-// planes lie in LDS; the next chunk's rows are loaded while this one is computed.
+// happen in registers.  A chunk's x, z and U lie in LDS by rows; products over
+// tokens read x and z transposed; the next chunk's rows are loaded while this one is computed.
 #pragma once
+#include <type_traits>
+
 #include "falcon_gated.h"
 
 namespace falcon {
@@ -44,8 +46,9 @@ struct ChunkArgs {
 template <typename TX, typename TZ, int DX, int DZ>
 struct LdsState {
   static constexpr int NPX = planes<TX>(), NPZ = planes<TZ>();
-  alignas(16) uint16_t xt[NPX][DX * C];             // x by columns
-  alignas(16) uint16_t zt[NPZ][DZ * C];             // z by columns
+  static constexpr int W = DX < 32 ? 32 : DX;       // k-slots come in 32s: zeros behind 16
+  alignas(16) uint16_t x[NPX][C * W];
+  alignas(16) uint16_t z[NPZ][C * DZ];
   alignas(16) double g[C];                          // sums of log2 decays, row by row
   alignas(16) float e[C];
   alignas(16) float w[C];
@@ -53,9 +56,7 @@ struct LdsState {
 };
 template <typename TX, typename TZ, int DX, int DZ>
 struct Lds : LdsState<TX, TZ, DX, DZ> {
-  static constexpr int W = DX < 32 ? 32 : DX;       // k-slots come in 32s: zeros behind 16
-  alignas(16) uint16_t xn[planes<TX>()][C * W];     // x by rows
-  alignas(16) uint16_t s[3][DZ * W];                // U at the chunk's start
+  alignas(16) uint16_t s[3][DZ * LdsState<TX, TZ, DX, DZ>::W];   // U at the chunk's start
 };
 
 // The workgroup's U: wave w holds z rows 16 (w % NDT).. and NK tiles of 16 x columns.
@@ -64,7 +65,8 @@ template <int DX, int DZ>
 struct State {
   static constexpr int NDT = DZ / 16, WPD = 4 / NDT, ND = DX / 16, NK = (ND + WPD - 1) / WPD;
   floatx4 t[NK];
-  static __device__ __forceinline__ int row() { return 16 * ((threadIdx.x >> 6) % NDT) + (threadIdx.x & 15); }
+  static __device__ __forceinline__ int row0() { return 16 * ((threadIdx.x >> 6) % NDT); }
+  static __device__ __forceinline__ int row() { return row0() + (threadIdx.x & 15); }
   static __device__ __forceinline__ int tile(int j) { return ((threadIdx.x >> 6) / NDT) * NK + j; }
   static __device__ __forceinline__ int col(int j) { return 16 * tile(j) + 4 * ((threadIdx.x & 63) >> 4); }
   static __device__ __forceinline__ bool has(int j) { return WPD * NK == ND ? true : tile(j) < ND; }
@@ -111,7 +113,7 @@ struct State {
   template <class L>
   __device__ __forceinline__ void update(const L& lds) {
     constexpr int NPX = L::NPX, NPZ = L::NPZ;
-    const int lane = threadIdx.x & 63, m = lane & 15, g8 = 8 * (lane >> 4);
+    const int g8 = 8 * ((threadIdx.x & 63) >> 4);
     const float d = lds.d;
 #pragma unroll
     for (int j = 0; j < NK; ++j) t[j] *= d;
@@ -119,25 +121,30 @@ struct State {
     for (int kk = 0; kk < C; kk += 32) {
       bf16x8 z[NPZ], zw[3];
       float v[8], w[8];
-      frag<NPZ, C>(lds.zt[0], DZ * C, row(), kk + g8, z);
+      frag_t<NPZ, DZ>(lds.z[0], DZ * C, kk + g8, row0(), z);
       values<NPZ>(z, v);
       *reinterpret_cast<float4*>(w) = *reinterpret_cast<const float4*>(lds.w + kk + g8);
       *reinterpret_cast<float4*>(w + 4) = *reinterpret_cast<const float4*>(lds.w + kk + g8 + 4);
 #pragma unroll
       for (int e = 0; e < 8; ++e) v[e] *= w[e];
       frag3(v, zw);
-      bf16x8 x[NK][NPX];
+      constexpr int J = NK < 4 ? NK : 4;        // tiles at a time
 #pragma unroll
-      for (int j = 0; j < NK; ++j) {
-        const int tj = has(j) ? tile(j) : 0;
-        frag<NPX, C>(lds.xt[0], DX * C, 16 * tj + m, kk + g8, x[j]);
+      for (int j0 = 0; j0 < NK; j0 += J) {
+        if (NK > J) __builtin_amdgcn_sched_barrier(0);
+        bf16x8 x[J][NPX];
+#pragma unroll
+        for (int j = 0; j < J; ++j) {
+          const int tj = has(j0 + j) ? tile(j0 + j) : 0;
+          frag_t<NPX, L::W>(lds.x[0], C * L::W, kk + g8, 16 * tj, x[j]);
+        }
+#pragma unroll
+        for (int p = 0; p < NPX; ++p)
+#pragma unroll
+          for (int q = 0; p + q < 3; ++q)
+#pragma unroll
+            for (int j = 0; j < J; ++j) t[j0 + j] = mfma16(x[j][p], zw[q], t[j0 + j]);
       }
-#pragma unroll
-      for (int p = 0; p < NPX; ++p)
-#pragma unroll
-        for (int q = 0; p + q < 3; ++q)
-#pragma unroll
-          for (int j = 0; j < NK; ++j) t[j] = mfma16(x[j][p], zw[q], t[j]);
     }
   }
 };
@@ -205,8 +212,8 @@ __global__ __launch_bounds__(NT) void state_kernel(ChunkArgs a, Span sp) {
   if (wave == 0) dec.sum<REV>(la, walk.at(0), len);
   for (int c = 0; c < walk.n; ++c) {
     if (c) __syncthreads();
-    sx.template store<C>(nullptr, lds.xt[0]);
-    sz.template store<C>(nullptr, lds.zt[0]);
+    sx.template store<L::W>(lds.x[0]);
+    sz.template store<DZ>(lds.z[0]);
     if (wave == 0) {
       dec.store(lds);
       total += dec.total;
@@ -232,10 +239,18 @@ __device__ __forceinline__ floatx4 load4(const uint16_t* p) {
 }
 __device__ __forceinline__ floatx4 load4(const float* p) { return *reinterpret_cast<const floatx4*>(p); }
 
+// Workgroups on a compute unit that the registers are held to: three with bf16 operands
+// up to 64 columns, two up to 64 columns and at 128 with bf16 operands, else one.
+template <typename TX, typename TY, typename TZ, int DX>
+constexpr int groups() {
+  constexpr int n = planes<TX>() + planes<TY>() + planes<TZ>();
+  return n == 3 && DX <= 64 ? 3 : n < 9 || DX <= 64 ? 2 : 1;
+}
+
 // GRAD: U is kept transposed in memory ([x][z], a state's own layout for dq and dk), and
 // dots are written.
 template <typename TX, typename TY, typename TZ, int DX, int DZ, bool REV, bool GRAD>
-__global__ __launch_bounds__(NT) void chunk_kernel(ChunkArgs a, Span sp) {
+__global__ __launch_bounds__(NT, (groups<TX, TY, TZ, DX>())) void chunk_kernel(ChunkArgs a, Span sp) {
   extern __shared__ __align__(16) unsigned char smem[];
   using L = Lds<TX, TZ, DX, DZ>;
   constexpr int NPX = L::NPX, NPY = planes<TY>(), NPZ = L::NPZ;
@@ -279,15 +294,15 @@ __global__ __launch_bounds__(NT) void chunk_kernel(ChunkArgs a, Span sp) {
   if (sp.segs > 1) st.load(sp.states + (chain * (sp.writes + 1) + step) * state + U_blk, U_sz, U_sx);
   else st.load(a.U0 ? a.U0 + chain * state + U_blk : nullptr, U_sz, U_sx);
   if (DX < W) {      // k-slots behind the last column
-    for (int i = threadIdx.x; i < NPX * C * W / 8; i += NT) reinterpret_cast<uint4*>(lds.xn[0])[i] = uint4{0u, 0u, 0u, 0u};
+    for (int i = threadIdx.x; i < NPX * C * W / 8; i += NT) reinterpret_cast<uint4*>(lds.x[0])[i] = uint4{0u, 0u, 0u, 0u};
     for (int i = threadIdx.x; i < 3 * DZ * W / 8; i += NT) reinterpret_cast<uint4*>(lds.s[0])[i] = uint4{0u, 0u, 0u, 0u};
     __syncthreads();
   }
 
   for (int c = 0; c < walk.n; ++c) {
     if (c) __syncthreads();
-    sx.template store<W>(lds.xn[0], lds.xt[0]);
-    sz.template store<C>(nullptr, lds.zt[0]);
+    sx.template store<W>(lds.x[0]);
+    sz.template store<DZ>(lds.z[0]);
     st.template to_planes<W>(lds.s);
     if (wave == 0) dec.store(lds);
     bf16x8 yf[NQ][NPY];
@@ -313,6 +328,7 @@ __global__ __launch_bounds__(NT) void chunk_kernel(ChunkArgs a, Span sp) {
     for (int i = 0; i < NDT; ++i) acc[i] = floatx4{0.f, 0.f, 0.f, 0.f};
 #pragma unroll
     for (int i = 0; i < NQ; ++i) {
+      if (NQ > 2) __builtin_amdgcn_sched_barrier(0);
       bf16x8 s[NDT][3];
 #pragma unroll
       for (int d = 0; d < NDT; ++d) frag<3, W>(lds.s[0], DZ * W, 16 * d + m, 32 * i + 8 * g, s[d]);
@@ -336,6 +352,7 @@ __global__ __launch_bounds__(NT) void chunk_kernel(ChunkArgs a, Span sp) {
 #pragma unroll
     for (int kk = 0; kk < C; kk += 32) {
       if (kk > 16 * wave + 15) break;
+      __builtin_amdgcn_sched_barrier(0);        // (keeps the reads of a part in that part: registers)
       float v[8];
 #pragma unroll
       for (int j = 0; j < 2; ++j) {
@@ -344,7 +361,7 @@ __global__ __launch_bounds__(NT) void chunk_kernel(ChunkArgs a, Span sp) {
 #pragma unroll
         for (int i = 0; i < NQ; ++i) {
           bf16x8 xf[NPX];
-          frag<NPX, W>(lds.xn[0], C * W, kk + 8 * (m >> 2) + 4 * j + (m & 3), 32 * i + 8 * g, xf);
+          frag<NPX, W>(lds.x[0], C * W, kk + 8 * (m >> 2) + 4 * j + (m & 3), 32 * i + 8 * g, xf);
           mma<NPX, NPY>(xf, yf[i], p);
         }
 #pragma unroll
@@ -364,7 +381,7 @@ __global__ __launch_bounds__(NT) void chunk_kernel(ChunkArgs a, Span sp) {
       frag3(v, pf);
       bf16x8 zf[NDT][NPZ];
 #pragma unroll
-      for (int d = 0; d < NDT; ++d) frag<NPZ, C>(lds.zt[0], DZ * C, 16 * d + m, kk + 8 * g, zf[d]);
+      for (int d = 0; d < NDT; ++d) frag_t<NPZ, DZ>(lds.z[0], DZ * C, kk + 8 * g, 16 * d, zf[d]);
 #pragma unroll
       for (int p = 0; p < NPZ; ++p)
 #pragma unroll
@@ -429,15 +446,13 @@ hipError_t go_chunk(const ChunkArgs& a, const Span& sp, hipStream_t stream) {
 }
 
 // f(size, rows) as constants for dx columns and blocks of z rows of nz.
-template <typename TX, typename TZ, class F>
+template <class F>
 hipError_t with_sizes(int dx, int nz, F&& f) {
   auto rows = [&](auto d) {
-    constexpr int DX = decltype(d)::value;
-    switch (rows_of(sizeof(TX) == 4 && sizeof(TZ) == 4, DX, nz)) {
+    switch (rows_of(nz)) {
       case 16: return f(d, std::integral_constant<int, 16>());
       case 32: return f(d, std::integral_constant<int, 32>());
-      case 64:
-        if constexpr (most_rows<TX, TZ, DX>() == 64) return f(d, std::integral_constant<int, 64>());
+      case 64: return f(d, std::integral_constant<int, 64>());
     }
     return hipErrorInvalidValue;
   };
@@ -457,7 +472,7 @@ hipError_t launch_segments(const float* U0, const Span& sp, long chains, long st
 template <typename TX, typename TZ, bool REV>
 hipError_t launch_states(const ChunkArgs& a, int dx, const Span& sp, hipStream_t stream) {
   if (sp.writes == 0) return hipSuccess;
-  const hipError_t e = with_sizes<TX, TZ>(dx, a.nz, [&](auto d, auto r) {
+  const hipError_t e = with_sizes(dx, a.nz, [&](auto d, auto r) {
     return go_state<TX, TZ, decltype(d)::value, decltype(r)::value, REV>(a, sp, stream);
   });
   return e != hipSuccess ? e : launch_segments(a.U0, sp, a.chains, (long)a.nz * dx, stream);
