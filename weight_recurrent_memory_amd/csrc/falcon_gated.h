@@ -157,20 +157,28 @@ struct Stage {
   }
 };
 
-// log2 of the decay of token t (0 from L on and without gates), at least -1000 log2 e.
-__device__ __forceinline__ double log2_decay(const float* log_a, long t, long L) {
-  float g = log_a && t < L ? log_a[t] : 0.0f;
+// log2 of a decay of log g: at least -1000 log2 e (and a NaN stays one).
+__device__ __forceinline__ double log2_decay(float g) {
   g = g < -1000.0f ? -1000.0f : g;
   return (double)g * 1.4426950408889634;
 }
-// Inclusive sum over the lanes of a wave, first lane first.
+// x of the lane that a DPP control names, 0 where it names none.
+template <int CTRL, int ROWS>
+__device__ __forceinline__ double dpp(double x) {
+  const long long u = __builtin_bit_cast(long long, x);
+  const int lo = __builtin_amdgcn_update_dpp(0, (int)u, CTRL, ROWS, 0xf, false);
+  const int hi = __builtin_amdgcn_update_dpp(0, (int)(u >> 32), CTRL, ROWS, 0xf, false);
+  return __builtin_bit_cast(double, ((long long)hi << 32) | (unsigned int)lo);
+}
+// Inclusive sum over the lanes of a wave, first lane first: inside the rows of 16 lanes,
+// then the rows' last lanes on to the rows behind.
 __device__ __forceinline__ double wave_scan(double x) {
-  const int lane = threadIdx.x & 63;
-#pragma unroll
-  for (int m = 1; m < 64; m <<= 1) {
-    const double y = __shfl_up(x, m, 64);
-    if (lane >= m) x += y;
-  }
+  x += dpp<0x111, 0xf>(x);      // row_shr 1, 2, 4, 8
+  x += dpp<0x112, 0xf>(x);
+  x += dpp<0x114, 0xf>(x);
+  x += dpp<0x118, 0xf>(x);
+  x += dpp<0x142, 0xa>(x);      // row_bcast 15 to rows 1 and 3
+  x += dpp<0x143, 0xc>(x);      // row_bcast 31 to rows 2 and 3
   return x;
 }
 __device__ __forceinline__ float exp2_of(double x) { return __builtin_amdgcn_exp2f((float)x); }

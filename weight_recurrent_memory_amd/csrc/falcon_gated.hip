@@ -11,36 +11,36 @@ namespace gated {
 
 // The recurrence over segments: start of step j + 1 = decay_j start_j + write_j, in place,
 // slot 0 set to U0 (so that the last segment may write its result over U0).
-__global__ __launch_bounds__(256) void segments_kernel(const float* U0, Span sp, long size4) {
-  const long per = (size4 + 255) / 256;
+__global__ __launch_bounds__(256) void segments_kernel(const float* U0, Span sp, long size) {
+  const long per = size / 256;               // size is a multiple of 256
   const long chain = blockIdx.x / per, i = (blockIdx.x % per) * 256 + threadIdx.x;
-  if (i >= size4) return;
-  float4* s = reinterpret_cast<float4*>(sp.states) + chain * (sp.writes + 1) * size4 + i;
+  float* s = sp.states + chain * (sp.writes + 1) * size + i;
   const float* d = sp.decays + chain * sp.writes;
-  float4 x = {0.f, 0.f, 0.f, 0.f};
-  if (U0) x = reinterpret_cast<const float4*>(U0)[chain * size4 + i];
+  float x = U0 ? U0[chain * size + i] : 0.0f;
   *s = x;
-  s += size4;
-  for (int j0 = 0; j0 < sp.writes; j0 += 8) {
-    float4 w[8];
+  s += size;
+  constexpr int N = 16;                      // loads in flight
+  for (int j0 = 0; j0 < sp.writes; j0 += N) {
+    float w[N], a[N];
 #pragma unroll
-    for (int j = 0; j < 8; ++j)
-      if (j0 + j < sp.writes) w[j] = s[(j0 + j) * size4];
+    for (int j = 0; j < N; ++j) {
+      const bool in = j0 + j < sp.writes;
+      w[j] = in ? s[(j0 + j) * size] : 0.0f;
+      a[j] = in ? d[j0 + j] : 0.0f;
+    }
 #pragma unroll
-    for (int j = 0; j < 8; ++j) {
+    for (int j = 0; j < N; ++j) {
       if (j0 + j < sp.writes) {
-        const float a = d[j0 + j];
-        x = float4{a * x.x + w[j].x, a * x.y + w[j].y, a * x.z + w[j].z, a * x.w + w[j].w};
-        s[(j0 + j) * size4] = x;
+        x = a[j] * x + w[j];
+        s[(j0 + j) * size] = x;
       }
     }
   }
 }
 
 hipError_t launch_segments(const float* U0, const Span& sp, long chains, long state, hipStream_t stream) {
-  const long size4 = state / 4;
-  hipLaunchKernelGGL(segments_kernel, dim3((unsigned)(chains * ((size4 + 255) / 256))), dim3(256), 0,
-                     stream, U0, sp, size4);
+  hipLaunchKernelGGL(segments_kernel, dim3((unsigned)(chains * (state / 256))), dim3(256), 0, stream,
+                     U0, sp, state);
   return hipGetLastError();
 }
 

@@ -149,12 +149,20 @@ struct State {
   }
 };
 
-// One wave's sums of a chunk's log decays, and their place in LDS.
+// One wave's sums of a chunk's log decays, and their place in LDS.  The log decays are
+// loaded a chunk earlier than they are summed: a wait for this one load would also be a
+// wait for every load issued before it.
 struct Decays {
   double g, total;
+  float raw;
   template <bool REV>
-  __device__ __forceinline__ void sum(const float* log_a, long t0, long L) {
-    const double x = log2_decay(log_a, token<REV>(t0, threadIdx.x & 63), L);
+  __device__ __forceinline__ void load(const float* log_a, long t0, long L) {
+    const long t = token<REV>(t0, threadIdx.x & 63);
+    raw = log_a && t < L ? log_a[t] : 0.0f;
+  }
+  template <bool REV>
+  __device__ __forceinline__ void sum() {
+    const double x = log2_decay(raw);
     g = wave_scan(x);
     total = __shfl(g, 63, 64);
     if (REV) g -= x;
@@ -207,9 +215,11 @@ __global__ __launch_bounds__(NT) void state_kernel(ChunkArgs a, Span sp) {
   Decays dec;
   double total = 0.0;
   st.load(nullptr, 0, 1);
+  dec.load<REV>(la, walk.at(0), len);
   sx.template load<REV>(x, walk.at(0), len, DX);
   sz.template load<REV>(z, walk.at(0), len, a.nz);
-  if (wave == 0) dec.sum<REV>(la, walk.at(0), len);
+  dec.sum<REV>();
+  if (walk.n > 1) dec.load<REV>(la, walk.at(1), len);
   for (int c = 0; c < walk.n; ++c) {
     if (c) __syncthreads();
     sx.template store<L::W>(lds.x[0]);
@@ -219,11 +229,11 @@ __global__ __launch_bounds__(NT) void state_kernel(ChunkArgs a, Span sp) {
       total += dec.total;
     }
     __syncthreads();
+    if (wave == 0) dec.sum<REV>();
+    if (c + 2 < walk.n) dec.load<REV>(la, walk.at(c + 2), len);
     if (c + 1 < walk.n) {
-      const long t = walk.at(c + 1);
-      sx.template load<REV>(x, t, len, DX);
-      sz.template load<REV>(z, t, len, a.nz);
-      if (wave == 0) dec.sum<REV>(la, t, len);
+      sx.template load<REV>(x, walk.at(c + 1), len, DX);
+      sz.template load<REV>(z, walk.at(c + 1), len, a.nz);
     }
     st.update(lds);
   }
@@ -287,10 +297,12 @@ __global__ __launch_bounds__(NT, (groups<TX, TY, TZ, DX>())) void chunk_kernel(C
       else ry[i].zero();
     }
   };
+  dec.load<REV>(la, walk.at(0), len);
   sx.template load<REV>(x, walk.at(0), len, DX);
   sz.template load<REV>(z, walk.at(0), len, a.nz);
   load_y(walk.at(0));
-  if (wave == 0) dec.sum<REV>(la, walk.at(0), len);
+  dec.sum<REV>();
+  if (walk.n > 1) dec.load<REV>(la, walk.at(1), len);
   if (sp.segs > 1) st.load(sp.states + (chain * (sp.writes + 1) + step) * state + U_blk, U_sz, U_sx);
   else st.load(a.U0 ? a.U0 + chain * state + U_blk : nullptr, U_sz, U_sx);
   if (DX < W) {      // k-slots behind the last column
@@ -314,12 +326,13 @@ __global__ __launch_bounds__(NT, (groups<TX, TY, TZ, DX>())) void chunk_kernel(C
       for (int p = 0; p < NPY; ++p) yf[i][p] = __builtin_bit_cast(bf16x8, f[p]);
     }
     __syncthreads();
+    if (wave == 0) dec.sum<REV>();
+    if (c + 2 < walk.n) dec.load<REV>(la, walk.at(c + 2), len);
     if (c + 1 < walk.n) {
       const long t = walk.at(c + 1);
       sx.template load<REV>(x, t, len, DX);
       sz.template load<REV>(z, t, len, a.nz);
       load_y(t);
-      if (wave == 0) dec.sum<REV>(la, t, len);
     }
 
     // out^T: z rows x this wave's 16 tokens; first U's part
