@@ -241,13 +241,38 @@ __global__ __launch_bounds__(NT) void state_kernel(ChunkArgs a, Span sp) {
   if (threadIdx.x == 0 && blk == 0) sp.decays[unit] = exp2_of(total);
 }
 
-// Four consecutive inputs as floats.
-__device__ __forceinline__ floatx4 load4(const uint16_t* p) {
-  const uint2 u = *reinterpret_cast<const uint2*>(p);
-  return floatx4{__uint_as_float(u.x << 16), __uint_as_float(u.x & 0xFFFF0000u),
-                 __uint_as_float(u.y << 16), __uint_as_float(u.y & 0xFFFF0000u)};
+// Four consecutive inputs as they are in memory, and as floats.
+template <typename T>
+struct Raw4;
+template <>
+struct Raw4<uint16_t> {
+  uint2 u;
+  __device__ __forceinline__ void load(const uint16_t* p) { u = *reinterpret_cast<const uint2*>(p); }
+  __device__ __forceinline__ void zero() { u = uint2{0u, 0u}; }
+  __device__ __forceinline__ floatx4 values() const {
+    return floatx4{__uint_as_float(u.x << 16), __uint_as_float(u.x & 0xFFFF0000u),
+                   __uint_as_float(u.y << 16), __uint_as_float(u.y & 0xFFFF0000u)};
+  }
+};
+template <>
+struct Raw4<float> {
+  floatx4 u;
+  __device__ __forceinline__ void load(const float* p) { u = *reinterpret_cast<const floatx4*>(p); }
+  __device__ __forceinline__ void zero() { u = floatx4{0.f, 0.f, 0.f, 0.f}; }
+  __device__ __forceinline__ floatx4 values() const { return u; }
+};
+// Four values of NP planes in LDS.
+template <int NP>
+__device__ __forceinline__ floatx4 values4(const uint16_t* p, int stride) {
+  floatx4 x = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+  for (int i = NP - 1; i >= 0; --i) {
+    Raw4<uint16_t> r;
+    r.load(p + i * stride);
+    x += r.values();
+  }
+  return x;
 }
-__device__ __forceinline__ floatx4 load4(const float* p) { return *reinterpret_cast<const floatx4*>(p); }
 
 // Workgroups on a compute unit that the registers are held to: three with bf16 operands
 // up to 64 columns, two up to 64 columns and at 128 with bf16 operands, else one.
@@ -326,13 +351,23 @@ __global__ __launch_bounds__(NT, (groups<TX, TY, TZ, DX>())) void chunk_kernel(C
       for (int p = 0; p < NPY; ++p) yf[i][p] = __builtin_bit_cast(bf16x8, f[p]);
     }
     __syncthreads();
+    const int ti = 16 * wave + m;               // this lane's row of the chunk
+    const long t = token<REV>(walk.at(c), ti);
+    // (loads come back in order: the one needed first is issued first)
+    Raw4<TZ> ru[NDT];
+    if (GRAD) {
+#pragma unroll
+      for (int d = 0; d < NDT; ++d) {
+        if (t < len) ru[d].load(u + t * a.nz + 16 * d + 4 * g);
+        else ru[d].zero();
+      }
+    }
     if (wave == 0) dec.sum<REV>();
     if (c + 2 < walk.n) dec.load<REV>(la, walk.at(c + 2), len);
     if (c + 1 < walk.n) {
-      const long t = walk.at(c + 1);
-      sx.template load<REV>(x, t, len, DX);
-      sz.template load<REV>(z, t, len, a.nz);
-      load_y(t);
+      sx.template load<REV>(x, walk.at(c + 1), len, DX);
+      sz.template load<REV>(z, walk.at(c + 1), len, a.nz);
+      load_y(walk.at(c + 1));
     }
 
     // out^T: z rows x this wave's 16 tokens; first U's part
@@ -354,8 +389,6 @@ __global__ __launch_bounds__(NT, (groups<TX, TY, TZ, DX>())) void chunk_kernel(C
             for (int d = 0; d < NDT; ++d) acc[d] = mfma16(s[d][p], yf[i][r], acc[d]);
           }
     }
-    const int ti = 16 * wave + m;               // this lane's row of the chunk
-    const long t = token<REV>(walk.at(c), ti);
     const float e = lds.e[ti];
     const double Gt = lds.g[ti];
 #pragma unroll
@@ -407,14 +440,12 @@ __global__ __launch_bounds__(NT, (groups<TX, TY, TZ, DX>())) void chunk_kernel(C
       same += __shfl_xor(same, 16, 64);
       same += __shfl_xor(same, 32, 64);
       float dot = 0.0f;
-      if (t < len) {
 #pragma unroll
-        for (int d = 0; d < NDT; ++d) {
-          const floatx4 uv = load4(u + t * a.nz + 16 * d + 4 * g);
-          const floatx4 zv = load4(z + t * a.nz + 16 * d + 4 * g);
-          dot += acc[d].x * uv.x + acc[d].y * uv.y + acc[d].z * uv.z + acc[d].w * uv.w;
-          acc[d] += same * zv;
-        }
+      for (int d = 0; d < NDT; ++d) {
+        const floatx4 uv = ru[d].values();
+        const floatx4 zv = values4<NPZ>(lds.z[0] + at<DZ>(ti, 16 * d + 4 * g), DZ * C);
+        dot += acc[d].x * uv.x + acc[d].y * uv.y + acc[d].z * uv.z + acc[d].w * uv.w;
+        acc[d] += same * zv;
       }
       dot += __shfl_xor(dot, 16, 64);
       dot += __shfl_xor(dot, 32, 64);
