@@ -10,8 +10,15 @@ namespace falcon {
 namespace gated {
 
 // The recurrence over segments: start of step j + 1 = decay_j start_j + write_j, in place,
-// slot 0 set to U0 (so that the last segment may write its result over U0).
-__global__ __launch_bounds__(256) void segments_kernel(const float* U0, Span sp, long size) {
+// slot 0 set to U0 (so that the last segment may write its result over U0).  Of one span
+// (blockIdx.y 0) or two.
+__global__ __launch_bounds__(256) void segments_kernel(const float* U0, Span sp, const float* U1, Span sp1,
+                                                       long size) {
+  if (blockIdx.y) {
+    U0 = U1;
+    sp = sp1;
+  }
+  if (sp.writes == 0) return;
   const long per = size / 256;               // size is a multiple of 256
   const long chain = blockIdx.x / per, i = (blockIdx.x % per) * 256 + threadIdx.x;
   float* s = sp.states + chain * (sp.writes + 1) * size + i;
@@ -38,9 +45,10 @@ __global__ __launch_bounds__(256) void segments_kernel(const float* U0, Span sp,
   }
 }
 
-hipError_t launch_segments(const float* U0, const Span& sp, long chains, long state, hipStream_t stream) {
-  hipLaunchKernelGGL(segments_kernel, dim3((unsigned)(chains * (state / 256))), dim3(256), 0, stream,
-                     U0, sp, state);
+hipError_t launch_segments(const float* U0, const Span& sp, const float* U1, const Span& sp1, long chains,
+                           long state, hipStream_t stream) {
+  hipLaunchKernelGGL(segments_kernel, dim3((unsigned)(chains * (state / 256)), sp1.writes ? 2 : 1),
+                     dim3(256), 0, stream, U0, sp, U1, sp1, state);
   return hipGetLastError();
 }
 

@@ -87,6 +87,73 @@ __global__ __launch_bounds__(NT) void gate_kernel(GateArgs a, Span s, Span r) {
   }
 }
 
+// Both directions' states, and all three gradients, in one launch each: the workgroups
+// of one chain's segment run near each other in time and share its rows in the L2, and
+// one launch's last workgroups leave no part of the GPU idle.  (Up to 64 columns; at 128
+// the largest of the LDS needs, dk's 104 KB, would hold the others to one workgroup a
+// compute unit.)
+template <typename T, int DK, int DV>
+__global__ __launch_bounds__(NT) void both_states_kernel(ChunkArgs S, Span s, ChunkArgs R, Span r) {
+  extern __shared__ __align__(16) unsigned char smem[];
+  int blk;
+  long unit;
+  const long ns = S.chains * s.writes, nr = R.chains * r.writes;
+  if (!place(2, ns > nr ? ns : nr, blk, unit)) return;
+  if (blk == 0) {
+    if (unit < ns) state_body<T, T, DK, DV, false>(S, s, 0, unit, smem);
+  } else {
+    if (unit < nr) state_body<T, float, DK, DV, true>(R, r, 0, unit, smem);
+  }
+}
+template <typename T, int DK, int DV>
+__global__ __launch_bounds__(NT, 2) void gradients_kernel(ChunkArgs q, ChunkArgs k, ChunkArgs v, Span s, Span r) {
+  extern __shared__ __align__(16) unsigned char smem[];
+  int blk;
+  long unit;
+  if (!place(3, q.chains * s.segs, blk, unit)) return;
+  if (blk == 0) chunk_body<float, T, T, DV, DK, true, true>(k, r, 0, unit, smem);
+  else if (blk == 1) chunk_body<T, float, T, DV, DK, false, true>(q, s, 0, unit, smem);
+  else chunk_body<T, T, float, DK, DV, true, false>(v, r, 0, unit, smem);
+}
+template <typename T, int DK, int DV>
+hipError_t both(const ChunkArgs& S, const ChunkArgs& R, const ChunkArgs& q, const ChunkArgs& k,
+                const ChunkArgs& v, const Span& s, const Span& r, hipStream_t stream) {
+  hipError_t e;
+  const long writes = s.writes > r.writes ? s.writes : r.writes;
+  if (writes > 0) {
+    constexpr size_t bytes = sizeof(LdsState<T, float, DK, DV>);
+    auto kernel = both_states_kernel<T, DK, DV>;
+    if ((e = lds_limit(kernel, bytes)) != hipSuccess) return e;
+    hipLaunchKernelGGL(kernel, dim3(grid_of(2, S.chains * writes)), dim3(NT), bytes, stream, S, s, R, r);
+    if ((e = hipGetLastError()) != hipSuccess) return e;
+    if ((e = launch_segments(S.U0, s, R.U0, r, S.chains, (long)DK * DV, stream)) != hipSuccess) return e;
+  }
+  constexpr size_t a = sizeof(Lds<float, T, DV, DK>), b = sizeof(Lds<T, float, DK, DV>);
+  constexpr size_t bytes = a > b ? a : b;
+  auto kernel = gradients_kernel<T, DK, DV>;
+  if ((e = lds_limit(kernel, bytes)) != hipSuccess) return e;
+  hipLaunchKernelGGL(kernel, dim3(grid_of(3, S.chains * s.segs)), dim3(NT), bytes, stream, q, k, v, s, r);
+  return hipGetLastError();
+}
+// f(dk, dv) as constants up to 64
+template <class F>
+hipError_t with_small(int dk, int dv, F&& f) {
+  auto cols = [&](auto k) {
+    switch (dv) {
+      case 16: return f(k, std::integral_constant<int, 16>());
+      case 32: return f(k, std::integral_constant<int, 32>());
+      case 64: return f(k, std::integral_constant<int, 64>());
+    }
+    return hipErrorInvalidValue;
+  };
+  switch (dk) {
+    case 16: return cols(std::integral_constant<int, 16>());
+    case 32: return cols(std::integral_constant<int, 32>());
+    case 64: return cols(std::integral_constant<int, 64>());
+  }
+  return hipErrorInvalidValue;
+}
+
 // The two spans of a call (states first token first, their gradients last token first)
 // and its workspace.
 struct Plan {
@@ -123,23 +190,29 @@ hipError_t run(const GatedBwdArgs& a, Plan p, hipStream_t stream) {
   float* c = a.dlog_a ? w + (size_t)p.blocks * p.chains * a.seqlen : nullptr;
   hipError_t e;
   const ChunkArgs S{a.k, nullptr, a.v, a.log_a, a.S0, nullptr, nullptr, nullptr, nullptr, p.chains, a.seqlen, a.ndv};
-  if ((e = launch_states<T, T, false>(S, a.ndk, p.s, stream)) != hipSuccess) return e;
   const ChunkArgs R{a.q, nullptr, a.dO, a.log_a, a.dS_L, nullptr, nullptr, nullptr, nullptr, p.chains, a.seqlen, a.ndv};
-  if ((e = launch_states<T, float, true>(R, a.ndk, p.r, stream)) != hipSuccess) return e;
   const ChunkArgs dq{a.v, a.dO, a.k, a.log_a, a.S0, a.dq, nullptr, a.q, r, p.chains, a.seqlen, a.ndk};
-  e = with_sizes(a.ndv, a.ndk, [&](auto d, auto z) {
-    return go_chunk<T, float, T, decltype(d)::value, decltype(z)::value, false, true>(dq, p.s, stream);
-  });
-  if (e != hipSuccess) return e;
   const ChunkArgs dk{a.dO, a.v, a.q, a.log_a, a.dS_L, a.dk, nullptr, a.k, c, p.chains, a.seqlen, a.ndk};
-  e = with_sizes(a.ndv, a.ndk, [&](auto d, auto z) {
-    return go_chunk<float, T, T, decltype(d)::value, decltype(z)::value, true, true>(dk, p.r, stream);
-  });
-  if (e != hipSuccess) return e;
   const ChunkArgs dv{a.q, a.k, a.dO, a.log_a, a.dS_L, a.dv, a.dS0, nullptr, nullptr, p.chains, a.seqlen, a.ndv};
-  e = with_sizes(a.ndk, a.ndv, [&](auto d, auto z) {
-    return go_chunk<T, T, float, decltype(d)::value, decltype(z)::value, true, false>(dv, p.r, stream);
-  });
+  if (a.ndk <= 64 && a.ndv <= 64) {
+    e = with_small(a.ndk, a.ndv, [&](auto nk, auto nv) {
+      return both<T, decltype(nk)::value, decltype(nv)::value>(S, R, dq, dk, dv, p.s, p.r, stream);
+    });
+  } else {
+    if ((e = launch_states<T, T, false>(S, a.ndk, p.s, stream)) != hipSuccess) return e;
+    if ((e = launch_states<T, float, true>(R, a.ndk, p.r, stream)) != hipSuccess) return e;
+    e = with_sizes(a.ndv, a.ndk, [&](auto d, auto z) {
+      return go_chunk<T, float, T, decltype(d)::value, decltype(z)::value, false, true>(dq, p.s, stream);
+    });
+    if (e != hipSuccess) return e;
+    e = with_sizes(a.ndv, a.ndk, [&](auto d, auto z) {
+      return go_chunk<float, T, T, decltype(d)::value, decltype(z)::value, true, true>(dk, p.r, stream);
+    });
+    if (e != hipSuccess) return e;
+    e = with_sizes(a.ndk, a.ndv, [&](auto d, auto z) {
+      return go_chunk<T, T, float, decltype(d)::value, decltype(z)::value, true, false>(dv, p.r, stream);
+    });
+  }
   if (e != hipSuccess || !a.dlog_a) return e;
   const GateArgs g{a.log_a, a.dS_L, r, c, p.blocks, a.dlog_a, p.chains, p.state, a.seqlen};
   hipLaunchKernelGGL(gate_kernel, dim3((unsigned)(p.chains * p.s.segs)), dim3(NT), 0, stream, g, p.s, p.r);

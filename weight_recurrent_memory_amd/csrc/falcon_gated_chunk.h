@@ -193,13 +193,10 @@ struct Walk {
 
 // A segment's own write: U from zero.
 template <typename TX, typename TZ, int DX, int DZ, bool REV>
-__global__ __launch_bounds__(NT) void state_kernel(ChunkArgs a, Span sp) {
-  extern __shared__ __align__(16) unsigned char smem[];
+__device__ __forceinline__ void state_body(const ChunkArgs& a, const Span& sp, int blk, long unit,
+                                           unsigned char* smem) {
   using L = LdsState<TX, TZ, DX, DZ>;
   L& lds = *reinterpret_cast<L*>(smem);
-  int blk;
-  long unit;
-  if (!place(a.nz / DZ, a.chains * sp.writes, blk, unit)) return;
   const long chain = unit / sp.writes;
   const int step = (int)(unit % sp.writes);
   const int wave = threadIdx.x >> 6;
@@ -239,6 +236,13 @@ __global__ __launch_bounds__(NT) void state_kernel(ChunkArgs a, Span sp) {
   }
   st.store(sp.states + ((chain * (sp.writes + 1) + step + 1) * a.nz + (long)blk * DZ) * DX, DX, 1);
   if (threadIdx.x == 0 && blk == 0) sp.decays[unit] = exp2_of(total);
+}
+template <typename TX, typename TZ, int DX, int DZ, bool REV>
+__global__ __launch_bounds__(NT) void state_kernel(ChunkArgs a, Span sp) {
+  extern __shared__ __align__(16) unsigned char smem[];
+  int blk;
+  long unit;
+  if (place(a.nz / DZ, a.chains * sp.writes, blk, unit)) state_body<TX, TZ, DX, DZ, REV>(a, sp, blk, unit, smem);
 }
 
 // Four consecutive inputs as they are in memory, and as floats.
@@ -285,15 +289,12 @@ constexpr int groups() {
 // GRAD: U is kept transposed in memory ([x][z], a state's own layout for dq and dk), and
 // dots are written.
 template <typename TX, typename TY, typename TZ, int DX, int DZ, bool REV, bool GRAD>
-__global__ __launch_bounds__(NT, (groups<TX, TY, TZ, DX>())) void chunk_kernel(ChunkArgs a, Span sp) {
-  extern __shared__ __align__(16) unsigned char smem[];
+__device__ __forceinline__ void chunk_body(const ChunkArgs& a, const Span& sp, int blk, long unit,
+                                           unsigned char* smem) {
   using L = Lds<TX, TZ, DX, DZ>;
   constexpr int NPX = L::NPX, NPY = planes<TY>(), NPZ = L::NPZ;
   constexpr int W = L::W, NQ = W / 32, NDT = DZ / 16;
   L& lds = *reinterpret_cast<L*>(smem);
-  int blk;
-  long unit;
-  if (!place(a.nz / DZ, a.chains * sp.segs, blk, unit)) return;
   const long chain = unit / sp.segs;
   const int step = (int)(unit % sp.segs);
   const int wave = threadIdx.x >> 6, lane = threadIdx.x & 63;
@@ -460,6 +461,14 @@ __global__ __launch_bounds__(NT, (groups<TX, TY, TZ, DX>())) void chunk_kernel(C
   }
   if (a.U_out && step == sp.segs - 1) st.store(a.U_out + chain * state + U_blk, U_sz, U_sx);
 }
+template <typename TX, typename TY, typename TZ, int DX, int DZ, bool REV, bool GRAD>
+__global__ __launch_bounds__(NT, (groups<TX, TY, TZ, DX>())) void chunk_kernel(ChunkArgs a, Span sp) {
+  extern __shared__ __align__(16) unsigned char smem[];
+  int blk;
+  long unit;
+  if (place(a.nz / DZ, a.chains * sp.segs, blk, unit))
+    chunk_body<TX, TY, TZ, DX, DZ, REV, GRAD>(a, sp, blk, unit, smem);
+}
 
 // A kernel with more than 64 KB of LDS has to be told so (about a microsecond a call;
 // nothing is kept here).
@@ -511,7 +520,9 @@ hipError_t with_sizes(int dx, int nz, F&& f) {
 
 // The states that segments start from: every segment's own write, then the recurrence
 // over segments (segments_kernel in falcon_gated.hip).
-hipError_t launch_segments(const float* U0, const Span& sp, long chains, long state, hipStream_t stream);
+// Of one span, or of two (sp1.writes > 0) with as many chains and states as large.
+hipError_t launch_segments(const float* U0, const Span& sp, const float* U1, const Span& sp1, long chains,
+                           long state, hipStream_t stream);
 
 template <typename TX, typename TZ, bool REV>
 hipError_t launch_states(const ChunkArgs& a, int dx, const Span& sp, hipStream_t stream) {
@@ -519,7 +530,7 @@ hipError_t launch_states(const ChunkArgs& a, int dx, const Span& sp, hipStream_t
   const hipError_t e = with_sizes(dx, a.nz, [&](auto d, auto r) {
     return go_state<TX, TZ, decltype(d)::value, decltype(r)::value, REV>(a, sp, stream);
   });
-  return e != hipSuccess ? e : launch_segments(a.U0, sp, a.chains, (long)a.nz * dx, stream);
+  return e != hipSuccess ? e : launch_segments(a.U0, sp, nullptr, Span{}, a.chains, (long)a.nz * dx, stream);
 }
 
 // Floats of a span's workspace.
