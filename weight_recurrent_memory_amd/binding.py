@@ -148,6 +148,29 @@ def _stream(torch, device, stream):
     return ctypes.c_void_p(torch.cuda.current_stream(device).cuda_stream)
 
 
+def _expect(torch, name, t, shape, dtype, device):
+    """_check for a tensor or None; returns its address.  One comparison of each property
+    where all is well (a decode step's checks are a good part of its host time)."""
+    if t is None:
+        return None
+    if (t.dtype is dtype and t.shape == shape and t.get_device() == device.index
+            and t.is_contiguous()):
+        return t.data_ptr()
+    _check(torch, name, t, shape, dtype, device)
+    return t.data_ptr()
+
+
+def _address(t):
+    return None if t is None else t.data_ptr()
+
+
+def _raw_stream(torch, device, stream):
+    """The hipStream_t of a call as an integer."""
+    if stream is None:
+        return torch._C._cuda_getCurrentRawStream(device.index)
+    return stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)
+
+
 class _NoGuard:
     def __enter__(self):
         return None
@@ -163,7 +186,7 @@ def _guard(torch, device, stream):
     """Context of one call: `device` current, and with an explicit stream that stream,
     so that what the call allocates belongs to the stream it runs on."""
     if stream is None:
-        if torch.cuda.current_device() == device.index:
+        if torch._C._cuda_getDevice() == device.index:
             return _NO_GUARD
         return torch.cuda.device(device)
     if not isinstance(stream, torch.cuda.Stream):

@@ -7,8 +7,6 @@ entry points take them.
 """
 from __future__ import annotations
 
-import ctypes
-
 from . import binding as _b
 
 GATE_KINDS = {"silu": 0, "sigmoid": 1}
@@ -22,7 +20,7 @@ def _rows(torch, name, t, shape, dtype, device):
         raise ValueError("%s must live on %s" % (name, device))
     if t.dtype != dtype:
         raise TypeError("%s must be %s, got %s" % (name, dtype, t.dtype))
-    if tuple(t.shape) != shape:
+    if t.shape != shape:
         raise ValueError("%s shape %s != %s" % (name, tuple(t.shape), shape))
     B, L, H, d = shape
     s0, s1, s2, s3 = t.stride()
@@ -30,7 +28,7 @@ def _rows(torch, name, t, shape, dtype, device):
     if s3 != 1 or (H > 1 and s2 != d) or ld < H * d or (B > 1 and s0 != L * ld):
         raise ValueError("%s: strides %s of %s are not rows of %d elements at one distance"
                          % (name, t.stride(), shape, H * d))
-    return ctypes.c_void_p(t.data_ptr()), ld
+    return t.data_ptr(), ld
 
 
 def _token_major(torch, name, t):
@@ -62,19 +60,19 @@ def norm_in(q_in, k_in, v_in=None, *, eps=1e-6, out=None, stream=None):
     vp, ldv = _rows(torch, "v_in", v_in, (B, L, H, dv), dt, dev)
     with _b._guard(torch, dev, stream):
         if out is None:
-            q = torch.empty((B, H, L, dk), device=dev, dtype=dt)
-            k = torch.empty((B, H, L, dk), device=dev, dtype=dt)
-            v = None if v_in is None else torch.empty((B, H, L, dv), device=dev, dtype=dt)
+            q = q_in.new_empty((B, H, L, dk))
+            k = q_in.new_empty((B, H, L, dk))
+            v = None if v_in is None else q_in.new_empty((B, H, L, dv))
         else:
             q, k, v = out
             if q is None or k is None:
                 raise ValueError("out must hold q and k")
-            _b._check(torch, "out[0]", q, (B, H, L, dk), dt, dev)
-            _b._check(torch, "out[1]", k, (B, H, L, dk), dt, dev)
-            _b._check(torch, "out[2]", v, (B, H, L, dv), dt, dev)
+            _b._expect(torch, "out[0]", q, (B, H, L, dk), dt, dev)
+            _b._expect(torch, "out[1]", k, (B, H, L, dk), dt, dev)
+            _b._expect(torch, "out[2]", v, (B, H, L, dv), dt, dev)
         status = lib.falcon_norm_in(B, H, L, dk, dv, dcode, qp, ldq, kp, ldk, vp, ldv, float(eps),
-                                    _b._ptr(q), _b._ptr(k), _b._ptr(v),
-                                    _b._stream(torch, dev, stream))
+                                    _b._address(q), _b._address(k), _b._address(v),
+                                    _b._raw_stream(torch, dev, stream))
     _b._raise(lib, "falcon_norm_in", status)
     return q, k, v
 
@@ -94,9 +92,9 @@ def norm_in_bwd(q_in, k_in, dq, dk, dv=None, *, eps=1e-6, out=None, stream=None)
     kp, ldk = _rows(torch, "k_in", k_in, (B, L, H, ndk), dt, dev)
     if dq is None or dk is None:
         raise ValueError("dq and dk must be given")
-    _b._check(torch, "dq", dq, (B, H, L, ndk), f32, dev)
-    _b._check(torch, "dk", dk, (B, H, L, ndk), f32, dev)
-    _b._check(torch, "dv", dv, (B, H, L, ndv), f32, dev)
+    _b._expect(torch, "dq", dq, (B, H, L, ndk), f32, dev)
+    _b._expect(torch, "dk", dk, (B, H, L, ndk), f32, dev)
+    _b._expect(torch, "dv", dv, (B, H, L, ndv), f32, dev)
     with _b._guard(torch, dev, stream):
         if out is None:
             out = (torch.empty((B, L, H, ndk), device=dev, dtype=dt),
@@ -106,8 +104,8 @@ def norm_in_bwd(q_in, k_in, dq, dk, dv=None, *, eps=1e-6, out=None, stream=None)
         okp, ldok = _rows(torch, "out[1]", out[1], (B, L, H, ndk), dt, dev)
         ovp, ldov = _rows(torch, "out[2]", out[2], (B, L, H, ndv), dt, dev)
         status = lib.falcon_norm_in_bwd(B, H, L, ndk, ndv, dcode, qp, ldq, kp, ldk, float(eps),
-                                        _b._ptr(dq), _b._ptr(dk), _b._ptr(dv), oqp, ldoq, okp,
-                                        ldok, ovp, ldov, _b._stream(torch, dev, stream))
+                                        _b._address(dq), _b._address(dk), _b._address(dv), oqp, ldoq, okp,
+                                        ldok, ovp, ldov, _b._raw_stream(torch, dev, stream))
     _b._raise(lib, "falcon_norm_in_bwd", status)
     return tuple(out)
 
@@ -129,8 +127,8 @@ def norm_out(o, weight, gate=None, *, gate_kind="silu", residual=None, scale=1.0
     dt = given[0] if given else (dtype or torch.bfloat16)
     if dtype is not None and dtype != dt:
         raise TypeError("dtype %s, but the tensors given are %s" % (dtype, dt))
-    _b._check(torch, "o", o, (B, H, L, dv), torch.float32, dev)
-    _b._check(torch, "weight", weight, (dv,), torch.float32, dev)
+    _b._expect(torch, "o", o, (B, H, L, dv), torch.float32, dev)
+    _b._expect(torch, "weight", weight, (dv,), torch.float32, dev)
     gp, ldg = _rows(torch, "gate", gate, (B, L, H, dv), dt, dev)
     rp, ldr = _rows(torch, "residual", residual, (B, L, H, dv), dt, dev)
     with _b._guard(torch, dev, stream):
@@ -138,9 +136,9 @@ def norm_out(o, weight, gate=None, *, gate_kind="silu", residual=None, scale=1.0
             out = torch.empty((B, L, H, dv), device=dev, dtype=dt)
         dcode = _b._dtype_code(torch, out)
         yp, ldy = _rows(torch, "out", out, (B, L, H, dv), dt, dev)
-        status = lib.falcon_norm_out(B, H, L, dv, dcode, _b._ptr(o), _b._ptr(weight), gp, ldg, kind,
+        status = lib.falcon_norm_out(B, H, L, dv, dcode, _b._address(o), _b._address(weight), gp, ldg, kind,
                                      rp, ldr, float(scale), float(eps), yp, ldy,
-                                     _b._stream(torch, dev, stream))
+                                     _b._raw_stream(torch, dev, stream))
     _b._raise(lib, "falcon_norm_out", status)
     return out
 
@@ -158,8 +156,8 @@ def norm_out_bwd(o, weight, dy, gate=None, *, gate_kind="silu", scale=1.0, eps=1
     dev, dt, f32 = o.device, dy.dtype, torch.float32
     kind = _gate_kind(gate_kind)
     dcode = _b._dtype_code(torch, dy)
-    _b._check(torch, "o", o, (B, H, L, dv), f32, dev)
-    _b._check(torch, "weight", weight, (dv,), f32, dev)
+    _b._expect(torch, "o", o, (B, H, L, dv), f32, dev)
+    _b._expect(torch, "weight", weight, (dv,), f32, dev)
     dp, ldd = _rows(torch, "dy", dy, (B, L, H, dv), dt, dev)
     gp, ldg = _rows(torch, "gate", gate, (B, L, H, dv), dt, dev)
     if gate is None and dgate is not None:
@@ -173,9 +171,9 @@ def norm_out_bwd(o, weight, dy, gate=None, *, gate_kind="silu", scale=1.0, eps=1
         gop, ldgo = _rows(torch, "dgate", res.get("dgate"), (B, L, H, dv), dt, dev)
         need = int(lib.falcon_norm_out_bwd_workspace_bytes(B, L, dv))
         ws = torch.empty(max(need, 16), device=dev, dtype=torch.uint8)
-        status = lib.falcon_norm_out_bwd(B, H, L, dv, dcode, _b._ptr(o), _b._ptr(weight), gp, ldg,
+        status = lib.falcon_norm_out_bwd(B, H, L, dv, dcode, _b._address(o), _b._address(weight), gp, ldg,
                                          kind, float(scale), float(eps), dp, ldd,
-                                         _b._ptr(res["dO"]), gop, ldgo, _b._ptr(res["dweight"]),
-                                         _b._ptr(ws), need, _b._stream(torch, dev, stream))
+                                         _b._address(res["dO"]), gop, ldgo, _b._address(res["dweight"]),
+                                         _b._address(ws), need, _b._raw_stream(torch, dev, stream))
     _b._raise(lib, "falcon_norm_out_bwd", status)
     return res
