@@ -7,10 +7,10 @@
 // matrix cores' bf16 rate (16 times the float32 one) at float32's precision, three
 // passes with one float32 operand and six with two.
 //
-// Decays.  G_t = sum of log2 a over the chunk up to t, in float64: the decay from s to
-// t is 2^(G_t - G_s), one subtraction and one v_exp.  In float32 a reset (a log decay
-// of -1000) would leave the differences behind it wrong by 2^-24 of 1000.  A decay is
-// never divided by.
+// Decays.  G_t = sum of log2 a over the chunk up to t, in float64 and kept as two floats:
+// the decay from s to t is 2^(G_t - G_s), three additions and one v_exp.  In one float a
+// reset (a log decay of -1000) would leave the differences behind it wrong by 2^-24 of
+// 1000.  A decay is never divided by.
 #pragma once
 #include "falcon_device.h"
 #include "falcon_launch.h"
@@ -182,6 +182,17 @@ __device__ __forceinline__ double wave_scan(double x) {
   return x;
 }
 __device__ __forceinline__ float exp2_of(double x) { return __builtin_amdgcn_exp2f((float)x); }
+
+// A sum of log2 decays as two floats, and the decay 2^(t - s): the difference of the first
+// parts is exact where they are near each other and else good to 2^-24 of an exponent
+// whose decay is small.
+__device__ __forceinline__ float2 two_floats(double x) {
+  const float h = (float)x;
+  return float2{h, (float)(x - (double)h)};
+}
+__device__ __forceinline__ float decay(float2 t, float2 s) {
+  return __builtin_amdgcn_exp2f((t.x - s.x) + (t.y - s.y));
+}
 
 // acc += A B over the plane pairs that count.
 template <int NA, int NB>

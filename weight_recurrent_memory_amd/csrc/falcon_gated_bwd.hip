@@ -87,9 +87,250 @@ __global__ __launch_bounds__(NT) void gate_kernel(GateArgs a, Span s, Span r) {
   }
 }
 
-// Both directions' states, and all three gradients, in one launch each: the workgroups
-// of one chain's segment run near each other in time and share its rows in the L2, and
-// one launch's last workgroups leave no part of the GPU idle.  (Up to 64 columns; at 128
+// dk and dv together, up to 64 columns each, last token first: one R for both, read by
+// rows for dv and transposed for dk, and one place in LDS for q and dO, which are x and z
+// of the one and z and x of the other.
+template <typename T, int DK, int DV>
+struct LdsKV {
+  static constexpr int NPX = planes<T>(), NPZ = 3;
+  static constexpr int W = DK < 32 ? 32 : DK, WZ = DV < 32 ? 32 : DV;   // k-slots in 32s
+  alignas(16) uint16_t x[NPX][C * W];               // q
+  alignas(16) uint16_t z[NPZ][C * WZ];              // dO
+  alignas(16) uint16_t s[3][WZ * W];                // R at the chunk's start
+  alignas(16) float2 g[C];
+  alignas(16) float e[C];
+  alignas(16) float w[C];
+  float d;
+};
+
+struct KVArgs {
+  const void* q;
+  const void* k;
+  const void* v;
+  const float* dO;
+  const float* log_a;
+  const float* dS_L;
+  float* dk;
+  float* dv;
+  float* dS0;
+  float* dots;             // or null
+  long chains;
+  int seqlen;
+};
+
+template <typename T, int D, int W>
+struct Rows {              // this lane's token's row as the second operand's fragments
+  static constexpr int NP = planes<T>(), N = W / 32;
+  Raw<T> r[N];
+  __device__ __forceinline__ void load(const T* p, bool in) {
+    const int g8 = 8 * ((threadIdx.x & 63) >> 4);
+#pragma unroll
+    for (int i = 0; i < N; ++i) {
+      if (in && 32 * i + g8 < D) r[i].load(p + 32 * i + g8);
+      else r[i].zero();
+    }
+  }
+  __device__ __forceinline__ void frags(bf16x8 (&f)[N][NP]) const {
+#pragma unroll
+    for (int i = 0; i < N; ++i) {
+      uint4 u[NP];
+      r[i].split(u);
+#pragma unroll
+      for (int p = 0; p < NP; ++p) f[i][p] = __builtin_bit_cast(bf16x8, u[p]);
+    }
+  }
+};
+
+template <typename T, int DK, int DV>
+__device__ __forceinline__ void kv_body(const KVArgs& a, const Span& sp, long unit, unsigned char* smem) {
+  using L = LdsKV<T, DK, DV>;
+  constexpr int NP = L::NPX, W = L::W, WZ = L::WZ, NK = W / 32, NV = WZ / 32, TK = DK / 16, TV = DV / 16;
+  L& lds = *reinterpret_cast<L*>(smem);
+  const long chain = unit / sp.segs, len = a.seqlen;
+  const int step = (int)(unit % sp.segs);
+  const int wave = threadIdx.x >> 6, lane = threadIdx.x & 63, m = lane & 15, g = lane >> 4;
+  const Walk<true> walk(sp, step, len);
+  const T* q = static_cast<const T*>(a.q) + chain * len * DK;
+  const T* k = static_cast<const T*>(a.k) + chain * len * DK;
+  const T* v = static_cast<const T*>(a.v) + chain * len * DV;
+  const float* dO = a.dO + chain * len * DV;
+  const float* la = a.log_a ? a.log_a + chain * len : nullptr;
+  float* dk = a.dk + chain * len * DK;
+  float* dv = a.dv + chain * len * DV;
+  constexpr long state = (long)DV * DK;
+  const int ti = 16 * wave + m;
+
+  Stage<T, DK> sx;
+  Stage<float, DV> sz;
+  State<DK, DV> st;
+  Decays dec;
+  Rows<T, DK, W> rk;
+  Rows<T, DV, WZ> rv;
+  auto fetch = [&](long base) {
+    sx.template load<true>(q, base, len, DK);
+    sz.template load<true>(dO, base, len, DV);
+    const long t = token<true>(base, ti);
+    rk.load(k + t * DK, t < len);
+    rv.load(v + t * DV, t < len);
+  };
+  dec.load<true>(la, walk.at(0), len);
+  fetch(walk.at(0));
+  dec.sum<true>();
+  if (walk.n > 1) dec.load<true>(la, walk.at(1), len);
+  if (sp.segs > 1) st.load(sp.states + (chain * (sp.writes + 1) + step) * state, DK, 1);
+  else st.load(a.dS_L ? a.dS_L + chain * state : nullptr, DK, 1);
+  if (DK < W || DV < WZ) {
+    for (int i = threadIdx.x; i < NP * C * W / 8; i += NT) reinterpret_cast<uint4*>(lds.x[0])[i] = uint4{0u, 0u, 0u, 0u};
+    for (int i = threadIdx.x; i < 3 * C * WZ / 8; i += NT) reinterpret_cast<uint4*>(lds.z[0])[i] = uint4{0u, 0u, 0u, 0u};
+    for (int i = threadIdx.x; i < 3 * WZ * W / 8; i += NT) reinterpret_cast<uint4*>(lds.s[0])[i] = uint4{0u, 0u, 0u, 0u};
+    __syncthreads();
+  }
+
+  for (int c = 0; c < walk.n; ++c) {
+    if (c) __syncthreads();
+    sx.template store<W>(lds.x[0]);
+    sz.template store<WZ>(lds.z[0]);
+    st.template to_planes<W>(lds.s[0], WZ * W);
+    if (wave == 0) dec.store(lds);
+    bf16x8 kf[NK][NP], vf[NV][NP];
+    rk.frags(kf);
+    rv.frags(vf);
+    __syncthreads();
+    const long t = token<true>(walk.at(c), ti);
+    Raw4<T> ru[TK];        // k again, as dk's columns lie on the lanes
+#pragma unroll
+    for (int d = 0; d < TK; ++d) {
+      if (t < len) ru[d].load(k + t * DK + 16 * d + 4 * g);
+      else ru[d].zero();
+    }
+    if (wave == 0) dec.sum<true>();
+    if (c + 2 < walk.n) dec.load<true>(la, walk.at(c + 2), len);
+    if (c + 1 < walk.n) fetch(walk.at(c + 1));
+
+    // the part of what lies behind the chunk: e R k and e R^T v
+    floatx4 av[TV], ak[TK];
+#pragma unroll
+    for (int d = 0; d < TV; ++d) av[d] = floatx4{0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+    for (int d = 0; d < TK; ++d) ak[d] = floatx4{0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+    for (int i = 0; i < NK; ++i) {
+      bf16x8 s[TV][3];
+#pragma unroll
+      for (int d = 0; d < TV; ++d) frag<3, W>(lds.s[0], WZ * W, 16 * d + m, 32 * i + 8 * g, s[d]);
+#pragma unroll
+      for (int p = 0; p < 3; ++p)
+#pragma unroll
+        for (int r = 0; r < NP; ++r)
+          if (p + r < 3) {
+#pragma unroll
+            for (int d = 0; d < TV; ++d) av[d] = mfma16(s[d][p], kf[i][r], av[d]);
+          }
+    }
+#pragma unroll
+    for (int i = 0; i < NV; ++i) {
+      __builtin_amdgcn_sched_barrier(0);
+      bf16x8 s[TK][3];
+#pragma unroll
+      for (int d = 0; d < TK; ++d) frag_t<3, W>(lds.s[0], WZ * W, 32 * i + 8 * g, 16 * d, s[d]);
+#pragma unroll
+      for (int p = 0; p < 3; ++p)
+#pragma unroll
+        for (int r = 0; r < NP; ++r)
+          if (p + r < 3) {
+#pragma unroll
+            for (int d = 0; d < TK; ++d) ak[d] = mfma16(s[d][p], vf[i][r], ak[d]);
+          }
+    }
+    const float e = lds.e[ti];
+    const float2 Gt = lds.g[ti];
+#pragma unroll
+    for (int d = 0; d < TV; ++d) av[d] *= e;
+#pragma unroll
+    for (int d = 0; d < TK; ++d) ak[d] *= e;
+    float same = 0.0f;     // v_t . dO_t, where this lane holds it
+#pragma unroll
+    for (int kk = 0; kk < C; kk += 32) {
+      if (kk > 16 * wave + 15) break;
+      __builtin_amdgcn_sched_barrier(0);
+      float x[8], y[8];
+#pragma unroll
+      for (int j = 0; j < 2; ++j) {
+        const int row = kk + 8 * (m >> 2) + 4 * j + (m & 3);
+        floatx4 pq = {0.f, 0.f, 0.f, 0.f}, pv = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+        for (int i = 0; i < NK; ++i) {
+          bf16x8 f[NP];
+          frag<NP, W>(lds.x[0], C * W, row, 32 * i + 8 * g, f);
+          mma<NP, NP>(f, kf[i], pq);
+        }
+#pragma unroll
+        for (int i = 0; i < NV; ++i) {
+          bf16x8 f[3];
+          frag<3, WZ>(lds.z[0], C * WZ, row, 32 * i + 8 * g, f);
+          mma<3, NP>(f, vf[i], pv);
+        }
+#pragma unroll
+        for (int r = 0; r < 4; ++r) {
+          const int s = kk + 8 * g + 4 * j + r;
+          const float dcy = decay(Gt, lds.g[s]);
+          x[4 * j + r] = s <= ti ? pq[r] * dcy : 0.0f;
+          y[4 * j + r] = s < ti ? pv[r] * dcy : 0.0f;
+          same = s == ti ? pv[r] : same;
+        }
+      }
+      bf16x8 pf[3];
+      frag3(x, pf);
+#pragma unroll
+      for (int p = 0; p < 3; ++p) {
+        bf16x8 f[TV][1];
+#pragma unroll
+        for (int d = 0; d < TV; ++d) frag_t<1, WZ>(lds.z[p], 0, kk + 8 * g, 16 * d, f[d]);
+#pragma unroll
+        for (int r = 0; p + r < 3; ++r)
+#pragma unroll
+          for (int d = 0; d < TV; ++d) av[d] = mfma16(f[d][0], pf[r], av[d]);
+      }
+      __builtin_amdgcn_sched_barrier(0);
+      frag3(y, pf);
+#pragma unroll
+      for (int p = 0; p < NP; ++p) {
+        bf16x8 f[TK][1];
+#pragma unroll
+        for (int d = 0; d < TK; ++d) frag_t<1, W>(lds.x[p], 0, kk + 8 * g, 16 * d, f[d]);
+#pragma unroll
+        for (int r = 0; p + r < 3; ++r)
+#pragma unroll
+          for (int d = 0; d < TK; ++d) ak[d] = mfma16(f[d][0], pf[r], ak[d]);
+      }
+    }
+    same += __shfl_xor(same, 16, 64);
+    same += __shfl_xor(same, 32, 64);
+    float dot = 0.0f;
+#pragma unroll
+    for (int d = 0; d < TK; ++d) {
+      const floatx4 uv = ru[d].values();
+      const floatx4 qv = values4<NP>(lds.x[0] + at<W>(ti, 16 * d + 4 * g), C * W);
+      dot += ak[d].x * uv.x + ak[d].y * uv.y + ak[d].z * uv.z + ak[d].w * uv.w;
+      ak[d] += same * qv;
+    }
+    dot += __shfl_xor(dot, 16, 64);
+    dot += __shfl_xor(dot, 32, 64);
+    if (t < len) {
+      if (a.dots && g == 0) a.dots[chain * len + t] = dot;
+#pragma unroll
+      for (int d = 0; d < TV; ++d) *reinterpret_cast<floatx4*>(dv + t * DV + 16 * d + 4 * g) = av[d];
+#pragma unroll
+      for (int d = 0; d < TK; ++d) *reinterpret_cast<floatx4*>(dk + t * DK + 16 * d + 4 * g) = ak[d];
+    }
+    __builtin_amdgcn_sched_barrier(0);
+    st.update(lds);
+  }
+  if (a.dS0 && step == sp.segs - 1) st.store(a.dS0 + chain * state, DK, 1);
+}
+
+// Both directions' states, and all three gradients, in one launch each: one launch's
+// last workgroups leave no part of the GPU idle.  (Up to 64 columns; at 128
 // the largest of the LDS needs, dk's 104 KB, would hold the others to one workgroup a
 // compute unit.)
 template <typename T, int DK, int DV>
@@ -106,18 +347,20 @@ __global__ __launch_bounds__(NT) void both_states_kernel(ChunkArgs S, Span s, Ch
   }
 }
 template <typename T, int DK, int DV>
-__global__ __launch_bounds__(NT, 2) void gradients_kernel(ChunkArgs q, ChunkArgs k, ChunkArgs v, Span s, Span r) {
+__global__ __launch_bounds__(NT, sizeof(T) == 2 ? 2 : 1) void gradients_kernel(ChunkArgs q, KVArgs kv, Span s, Span r) {
   extern __shared__ __align__(16) unsigned char smem[];
-  int blk;
-  long unit;
-  if (!place(3, q.chains * s.segs, blk, unit)) return;
-  if (blk == 0) chunk_body<float, T, T, DV, DK, true, true>(k, r, 0, unit, smem);
-  else if (blk == 1) chunk_body<T, float, T, DV, DK, false, true>(q, s, 0, unit, smem);
-  else chunk_body<T, T, float, DK, DV, true, false>(v, r, 0, unit, smem);
+  // the longer work first: the shorter fills what its last workgroups leave idle
+  // (8x12x2048x64: 152 us a call against 160 with the two of a segment side by side)
+  const long n = q.chains * s.segs, n8 = (n + 7) / 8 * 8;
+  const bool second = blockIdx.x >= n8;
+  const long unit = second ? blockIdx.x - n8 : blockIdx.x;
+  if (unit >= n) return;
+  if (!second) kv_body<T, DK, DV>(kv, r, unit, smem);
+  else chunk_body<T, float, T, DV, DK, false, true>(q, s, 0, unit, smem);
 }
 template <typename T, int DK, int DV>
-hipError_t both(const ChunkArgs& S, const ChunkArgs& R, const ChunkArgs& q, const ChunkArgs& k,
-                const ChunkArgs& v, const Span& s, const Span& r, hipStream_t stream) {
+hipError_t both(const ChunkArgs& S, const ChunkArgs& R, const ChunkArgs& q, const KVArgs& kv,
+                const Span& s, const Span& r, hipStream_t stream) {
   hipError_t e;
   const long writes = s.writes > r.writes ? s.writes : r.writes;
   if (writes > 0) {
@@ -128,11 +371,11 @@ hipError_t both(const ChunkArgs& S, const ChunkArgs& R, const ChunkArgs& q, cons
     if ((e = hipGetLastError()) != hipSuccess) return e;
     if ((e = launch_segments(S.U0, s, R.U0, r, S.chains, (long)DK * DV, stream)) != hipSuccess) return e;
   }
-  constexpr size_t a = sizeof(Lds<float, T, DV, DK>), b = sizeof(Lds<T, float, DK, DV>);
-  constexpr size_t bytes = a > b ? a : b;
+  constexpr size_t b1 = sizeof(LdsKV<T, DK, DV>), b2 = sizeof(Lds<T, T, DV, DK>);
+  constexpr size_t bytes = b1 > b2 ? b1 : b2;
   auto kernel = gradients_kernel<T, DK, DV>;
   if ((e = lds_limit(kernel, bytes)) != hipSuccess) return e;
-  hipLaunchKernelGGL(kernel, dim3(grid_of(3, S.chains * s.segs)), dim3(NT), bytes, stream, q, k, v, s, r);
+  hipLaunchKernelGGL(kernel, dim3(grid_of(2, S.chains * s.segs)), dim3(NT), bytes, stream, q, kv, s, r);
   return hipGetLastError();
 }
 // f(dk, dv) as constants up to 64
@@ -196,7 +439,8 @@ hipError_t run(const GatedBwdArgs& a, Plan p, hipStream_t stream) {
   const ChunkArgs dv{a.q, a.k, a.dO, a.log_a, a.dS_L, a.dv, a.dS0, nullptr, nullptr, p.chains, a.seqlen, a.ndv};
   if (a.ndk <= 64 && a.ndv <= 64) {
     e = with_small(a.ndk, a.ndv, [&](auto nk, auto nv) {
-      return both<T, decltype(nk)::value, decltype(nv)::value>(S, R, dq, dk, dv, p.s, p.r, stream);
+      const KVArgs kv{a.q, a.k, a.v, a.dO, a.log_a, a.dS_L, a.dk, a.dv, a.dS0, c, p.chains, a.seqlen};
+      return both<T, decltype(nk)::value, decltype(nv)::value>(S, R, dq, kv, p.s, p.r, stream);
     });
   } else {
     if ((e = launch_states<T, T, false>(S, a.ndk, p.s, stream)) != hipSuccess) return e;

@@ -47,9 +47,10 @@ template <typename TX, typename TZ, int DX, int DZ>
 struct LdsState {
   static constexpr int NPX = planes<TX>(), NPZ = planes<TZ>();
   static constexpr int W = DX < 32 ? 32 : DX;       // k-slots come in 32s: zeros behind 16
+  static constexpr int WZ = DZ;
   alignas(16) uint16_t x[NPX][C * W];
   alignas(16) uint16_t z[NPZ][C * DZ];
-  alignas(16) double g[C];                          // sums of log2 decays, row by row
+  alignas(16) float2 g[C];                          // sums of log2 decays, row by row
   alignas(16) float e[C];
   alignas(16) float w[C];
   float d;
@@ -96,7 +97,7 @@ struct State {
     }
   }
   template <int W>
-  __device__ __forceinline__ void to_planes(uint16_t (*s)[DZ * W]) const {
+  __device__ __forceinline__ void to_planes(uint16_t* s, int stride) const {
 #pragma unroll
     for (int j = 0; j < NK; ++j) {
       if (!has(j)) continue;
@@ -104,9 +105,9 @@ struct State {
       split3(t[j].x, t[j].y, h.x, m.x, l.x);
       split3(t[j].z, t[j].w, h.y, m.y, l.y);
       const int i = at<W>(row(), col(j));
-      *reinterpret_cast<uint2*>(s[0] + i) = h;
-      *reinterpret_cast<uint2*>(s[1] + i) = m;
-      *reinterpret_cast<uint2*>(s[2] + i) = l;
+      *reinterpret_cast<uint2*>(s + i) = h;
+      *reinterpret_cast<uint2*>(s + stride + i) = m;
+      *reinterpret_cast<uint2*>(s + 2 * stride + i) = l;
     }
   }
   // U <- d U + sum_s w_s z_s x_s^T
@@ -121,7 +122,7 @@ struct State {
     for (int kk = 0; kk < C; kk += 32) {
       bf16x8 z[NPZ], zw[3];
       float v[8], w[8];
-      frag_t<NPZ, DZ>(lds.z[0], DZ * C, kk + g8, row0(), z);
+      frag_t<NPZ, L::WZ>(lds.z[0], L::WZ * C, kk + g8, row0(), z);
       values<NPZ>(z, v);
       *reinterpret_cast<float4*>(w) = *reinterpret_cast<const float4*>(lds.w + kk + g8);
       *reinterpret_cast<float4*>(w + 4) = *reinterpret_cast<const float4*>(lds.w + kk + g8 + 4);
@@ -170,7 +171,7 @@ struct Decays {
   template <class S>
   __device__ __forceinline__ void store(S& lds) const {
     const int lane = threadIdx.x & 63;
-    lds.g[lane] = g;
+    lds.g[lane] = two_floats(g);
     lds.e[lane] = exp2_of(g);
     lds.w[lane] = exp2_of(total - g);
     if (lane == 0) lds.d = exp2_of(total);
@@ -341,7 +342,7 @@ __device__ __forceinline__ void chunk_body(const ChunkArgs& a, const Span& sp, i
     if (c) __syncthreads();
     sx.template store<W>(lds.x[0]);
     sz.template store<DZ>(lds.z[0]);
-    st.template to_planes<W>(lds.s);
+    st.template to_planes<W>(lds.s[0], DZ * W);
     if (wave == 0) dec.store(lds);
     bf16x8 yf[NQ][NPY];
 #pragma unroll
@@ -391,7 +392,7 @@ __device__ __forceinline__ void chunk_body(const ChunkArgs& a, const Span& sp, i
           }
     }
     const float e = lds.e[ti];
-    const double Gt = lds.g[ti];
+    const float2 Gt = lds.g[ti];
 #pragma unroll
     for (int d = 0; d < NDT; ++d) acc[d] *= e;
     // then the chunk's own tokens, 32 at a time; none behind the wave's last row
@@ -414,7 +415,7 @@ __device__ __forceinline__ void chunk_body(const ChunkArgs& a, const Span& sp, i
 #pragma unroll
         for (int r = 0; r < 4; ++r) {
           const int s = kk + 8 * g + 4 * j + r;
-          const float dcy = exp2_of(Gt - lds.g[s]);
+          const float dcy = decay(Gt, lds.g[s]);
           if (GRAD) {                           // s = t is added behind the dots
             v[4 * j + r] = s < ti ? p[r] * dcy : 0.0f;
             same = s == ti ? p[r] : same;
