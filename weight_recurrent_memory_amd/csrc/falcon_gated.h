@@ -62,29 +62,82 @@ __device__ __forceinline__ void values(const bf16x8 (&f)[NP], float (&x)[8]) {
   }
 }
 
+// Place of row `row` among a chunk's 64 tokens (REV: the last token is row 0), and the
+// token itself in the chunk of tokens t0..t0+63.
+template <bool REV>
+__device__ __forceinline__ int row_at(int row) { return REV ? C - 1 - row : row; }
+template <bool REV>
+__device__ __forceinline__ long token(long t0, int row) { return t0 + row_at<REV>(row); }
+
+// The tokens of one chunk in one sequence, as a buffer: an offset behind the last token's
+// row reads 0, whatever the row of the chunk.  Bases are the same for a whole wave, and
+// the offsets inside a chunk are the same for every chunk.
+typedef unsigned int uint4_t __attribute__((ext_vector_type(4)));
+typedef unsigned int uint2_t __attribute__((ext_vector_type(2)));
+struct Window {
+  __amdgpu_buffer_rsrc_t r;
+  // p: the first token's row; `rows` tokens are left in the sequence; rows `ld` elements
+  // apart, of which the first `before` lie before p
+  template <typename T>
+  __device__ __forceinline__ Window(const T* p, long rows, int ld, int before) {
+    const int n = (rows < C ? (int)rows : C) * ld - before;
+    r = __builtin_amdgcn_make_buffer_rsrc(const_cast<T*>(p), 0, n * (int)sizeof(T), 0x00027000);
+  }
+  __device__ __forceinline__ uint4 load16b(int at) const {
+    const uint4_t u = __builtin_amdgcn_raw_buffer_load_b128(r, at, 0, 0);
+    return uint4{u.x, u.y, u.z, u.w};
+  }
+  __device__ __forceinline__ uint2 load8b(int at) const {
+    const uint2_t u = __builtin_amdgcn_raw_buffer_load_b64(r, at, 0, 0);
+    return uint2{u.x, u.y};
+  }
+  __device__ __forceinline__ unsigned load4b(int at) const {
+    return __builtin_amdgcn_raw_buffer_load_b32(r, at, 0, 0);
+  }
+};
+constexpr int kNowhere = 1 << 30;      // an offset that reads 0
+
 // Eight consecutive inputs as they are in memory, and as planes.
 template <typename T>
 struct Raw;
 template <>
 struct Raw<uint16_t> {
   uint4 u;
-  __device__ __forceinline__ void load(const uint16_t* p) { u = *reinterpret_cast<const uint4*>(p); }
-  __device__ __forceinline__ void zero() { u = uint4{0u, 0u, 0u, 0u}; }
+  __device__ __forceinline__ void load(const Window& w, int at) { u = w.load16b(at); }
   __device__ __forceinline__ void split(uint4 (&f)[1]) const { f[0] = u; }
 };
 template <>
 struct Raw<float> {
-  float4 a, b;
-  __device__ __forceinline__ void load(const float* p) {
-    a = *reinterpret_cast<const float4*>(p);
-    b = *reinterpret_cast<const float4*>(p + 4);
+  uint4 a, b;
+  __device__ __forceinline__ void load(const Window& w, int at) {
+    a = w.load16b(at);
+    b = w.load16b(at + 16);
   }
-  __device__ __forceinline__ void zero() { a = b = float4{0.f, 0.f, 0.f, 0.f}; }
   __device__ __forceinline__ void split(uint4 (&f)[3]) const {
-    split3(a.x, a.y, f[0].x, f[1].x, f[2].x);
-    split3(a.z, a.w, f[0].y, f[1].y, f[2].y);
-    split3(b.x, b.y, f[0].z, f[1].z, f[2].z);
-    split3(b.z, b.w, f[0].w, f[1].w, f[2].w);
+    split3(__uint_as_float(a.x), __uint_as_float(a.y), f[0].x, f[1].x, f[2].x);
+    split3(__uint_as_float(a.z), __uint_as_float(a.w), f[0].y, f[1].y, f[2].y);
+    split3(__uint_as_float(b.x), __uint_as_float(b.y), f[0].z, f[1].z, f[2].z);
+    split3(__uint_as_float(b.z), __uint_as_float(b.w), f[0].w, f[1].w, f[2].w);
+  }
+};
+// Four consecutive inputs as they are in memory, and as floats.
+template <typename T>
+struct Raw4;
+template <>
+struct Raw4<uint16_t> {
+  uint2 u;
+  __device__ __forceinline__ void load(const Window& w, int at) { u = w.load8b(at); }
+  __device__ __forceinline__ floatx4 values() const {
+    return floatx4{__uint_as_float(u.x << 16), __uint_as_float(u.x & 0xFFFF0000u),
+                   __uint_as_float(u.y << 16), __uint_as_float(u.y & 0xFFFF0000u)};
+  }
+};
+template <>
+struct Raw4<float> {
+  uint4 u;
+  __device__ __forceinline__ void load(const Window& w, int at) { u = w.load16b(at); }
+  __device__ __forceinline__ floatx4 values() const {
+    return floatx4{__uint_as_float(u.x), __uint_as_float(u.y), __uint_as_float(u.z), __uint_as_float(u.w)};
   }
 };
 
@@ -97,9 +150,6 @@ __device__ __forceinline__ void frag(const uint16_t* p, int stride, int row, int
   for (int i = 0; i < NP; ++i) f[i] = frag_bf16(p + i * stride + at<W>(row, col));
 }
 
-// Token of row `row` of the chunk of tokens t0..t0+63.
-template <bool REV>
-__device__ __forceinline__ long token(long t0, int row) { return t0 + (REV ? C - 1 - row : row); }
 
 typedef short short4_t __attribute__((ext_vector_type(4)));
 
@@ -123,23 +173,24 @@ __device__ __forceinline__ void frag_t(const uint16_t* p, int stride, int row, i
 }
 
 // A chunk's rows of one input on its way to LDS: units of 8 columns of a token.
-template <typename T, int D>
+template <typename T, int D, bool REV>
 struct Stage {
   static constexpr int NP = planes<T>();
   static constexpr int G = D / 8, UNITS = C * G, N = (UNITS + NT - 1) / NT;
   Raw<T> r[N];
+  int from[N];             // of the chunk's first token
 
-  // the 64 tokens from t0 on, rows of `ld` elements (REV: the last token first); tokens
-  // from L on are zero
-  template <bool REV>
-  __device__ __forceinline__ void load(const T* x, long t0, long L, int ld) {
+  // rows of `ld` elements (REV: the last token is row 0)
+  __device__ __forceinline__ explicit Stage(int ld) {
 #pragma unroll
     for (int i = 0; i < N; ++i) {
       const int u = threadIdx.x + i * NT;
-      const long t = token<REV>(t0, u / G);
-      if ((UNITS % NT == 0 || u < UNITS) && t < L) r[i].load(x + t * ld + 8 * (u % G));
-      else r[i].zero();
+      from[i] = UNITS % NT == 0 || u < UNITS ? (row_at<REV>(u / G) * ld + 8 * (u % G)) * (int)sizeof(T) : kNowhere;
     }
+  }
+  __device__ __forceinline__ void load(const Window& w) {
+#pragma unroll
+    for (int i = 0; i < N; ++i) r[i].load(w, from[i]);
   }
   // to planes of rows W wide
   template <int W>
@@ -153,6 +204,31 @@ struct Stage {
 #pragma unroll
       for (int p = 0; p < NP; ++p)
         *reinterpret_cast<uint4*>(rows + p * C * W + at<W>(u / G, 8 * (u % G))) = a[p];
+    }
+  }
+};
+
+// One token's row (lane % 16 of the wave's 16) as a product's second operand.
+template <typename T, int D, bool REV>
+struct Row {
+  static constexpr int NP = planes<T>(), N = (D + 31) / 32;
+  Raw<T> r[N];
+  int from;
+  __device__ __forceinline__ Row() {
+    const int lane = threadIdx.x & 63, col = 8 * (lane >> 4);
+    from = D >= 32 || col < D ? (row_at<REV>(16 * (threadIdx.x >> 6) + (lane & 15)) * D + col) * (int)sizeof(T) : kNowhere;
+  }
+  __device__ __forceinline__ void load(const Window& w) {
+#pragma unroll
+    for (int i = 0; i < N; ++i) r[i].load(w, from + 32 * i * (int)sizeof(T));
+  }
+  __device__ __forceinline__ void frags(bf16x8 (&f)[N][NP]) const {
+#pragma unroll
+    for (int i = 0; i < N; ++i) {
+      uint4 u[NP];
+      r[i].split(u);
+#pragma unroll
+      for (int p = 0; p < NP; ++p) f[i][p] = __builtin_bit_cast(bf16x8, u[p]);
     }
   }
 };

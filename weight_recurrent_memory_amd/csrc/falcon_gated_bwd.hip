@@ -118,29 +118,6 @@ struct KVArgs {
   int seqlen;
 };
 
-template <typename T, int D, int W>
-struct Rows {              // this lane's token's row as the second operand's fragments
-  static constexpr int NP = planes<T>(), N = W / 32;
-  Raw<T> r[N];
-  __device__ __forceinline__ void load(const T* p, bool in) {
-    const int g8 = 8 * ((threadIdx.x & 63) >> 4);
-#pragma unroll
-    for (int i = 0; i < N; ++i) {
-      if (in && 32 * i + g8 < D) r[i].load(p + 32 * i + g8);
-      else r[i].zero();
-    }
-  }
-  __device__ __forceinline__ void frags(bf16x8 (&f)[N][NP]) const {
-#pragma unroll
-    for (int i = 0; i < N; ++i) {
-      uint4 u[NP];
-      r[i].split(u);
-#pragma unroll
-      for (int p = 0; p < NP; ++p) f[i][p] = __builtin_bit_cast(bf16x8, u[p]);
-    }
-  }
-};
-
 template <typename T, int DK, int DV>
 __device__ __forceinline__ void kv_body(const KVArgs& a, const Span& sp, long unit, unsigned char* smem) {
   using L = LdsKV<T, DK, DV>;
@@ -160,18 +137,18 @@ __device__ __forceinline__ void kv_body(const KVArgs& a, const Span& sp, long un
   constexpr long state = (long)DV * DK;
   const int ti = 16 * wave + m;
 
-  Stage<T, DK> sx;
-  Stage<float, DV> sz;
+  Stage<T, DK, true> sx(DK);
+  Stage<float, DV, true> sz(DV);
   State<DK, DV> st;
   Decays dec;
-  Rows<T, DK, W> rk;
-  Rows<T, DV, WZ> rv;
-  auto fetch = [&](long base) {
-    sx.template load<true>(q, base, len, DK);
-    sz.template load<true>(dO, base, len, DV);
-    const long t = token<true>(base, ti);
-    rk.load(k + t * DK, t < len);
-    rv.load(v + t * DV, t < len);
+  Row<T, DK, true> rk;
+  Row<T, DV, true> rv;
+  const int u_at = (row_at<true>(ti) * DK + 4 * g) * (int)sizeof(T);
+  auto fetch = [&](long t0) {
+    sx.load(Window(q + t0 * DK, len - t0, DK, 0));
+    sz.load(Window(dO + t0 * DV, len - t0, DV, 0));
+    rk.load(Window(k + t0 * DK, len - t0, DK, 0));
+    rv.load(Window(v + t0 * DV, len - t0, DV, 0));
   };
   dec.load<true>(la, walk.at(0), len);
   fetch(walk.at(0));
@@ -198,11 +175,9 @@ __device__ __forceinline__ void kv_body(const KVArgs& a, const Span& sp, long un
     __syncthreads();
     const long t = token<true>(walk.at(c), ti);
     Raw4<T> ru[TK];        // k again, as dk's columns lie on the lanes
+    const Window wk(k + walk.at(c) * DK, len - walk.at(c), DK, 0);
 #pragma unroll
-    for (int d = 0; d < TK; ++d) {
-      if (t < len) ru[d].load(k + t * DK + 16 * d + 4 * g);
-      else ru[d].zero();
-    }
+    for (int d = 0; d < TK; ++d) ru[d].load(wk, u_at + 16 * d * (int)sizeof(T));
     if (wave == 0) dec.sum<true>();
     if (c + 2 < walk.n) dec.load<true>(la, walk.at(c + 2), len);
     if (c + 1 < walk.n) fetch(walk.at(c + 1));
@@ -319,9 +294,9 @@ __device__ __forceinline__ void kv_body(const KVArgs& a, const Span& sp, long un
     if (t < len) {
       if (a.dots && g == 0) a.dots[chain * len + t] = dot;
 #pragma unroll
-      for (int d = 0; d < TV; ++d) *reinterpret_cast<floatx4*>(dv + t * DV + 16 * d + 4 * g) = av[d];
+      for (int d = 0; d < TV; ++d) __builtin_nontemporal_store(av[d], reinterpret_cast<floatx4*>(dv + t * DV + 16 * d + 4 * g));
 #pragma unroll
-      for (int d = 0; d < TK; ++d) *reinterpret_cast<floatx4*>(dk + t * DK + 16 * d + 4 * g) = ak[d];
+      for (int d = 0; d < TK; ++d) __builtin_nontemporal_store(ak[d], reinterpret_cast<floatx4*>(dk + t * DK + 16 * d + 4 * g));
     }
     __builtin_amdgcn_sched_barrier(0);
     st.update(lds);

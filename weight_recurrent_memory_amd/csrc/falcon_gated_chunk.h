@@ -158,8 +158,8 @@ struct Decays {
   float raw;
   template <bool REV>
   __device__ __forceinline__ void load(const float* log_a, long t0, long L) {
-    const long t = token<REV>(t0, threadIdx.x & 63);
-    raw = log_a && t < L ? log_a[t] : 0.0f;
+    const Window w(log_a ? log_a + t0 : nullptr, log_a ? L - t0 : 0, 1, 0);
+    raw = __builtin_bit_cast(float, w.load4b(4 * row_at<REV>(threadIdx.x & 63)));
   }
   template <bool REV>
   __device__ __forceinline__ void sum() {
@@ -207,15 +207,15 @@ __device__ __forceinline__ void state_body(const ChunkArgs& a, const Span& sp, i
   const TZ* z = static_cast<const TZ*>(a.z) + chain * len * a.nz + blk * DZ;
   const float* la = a.log_a ? a.log_a + chain * len : nullptr;
 
-  Stage<TX, DX> sx;
-  Stage<TZ, DZ> sz;
+  Stage<TX, DX, REV> sx(DX);
+  Stage<TZ, DZ, REV> sz(a.nz);
   State<DX, DZ> st;
   Decays dec;
   double total = 0.0;
   st.load(nullptr, 0, 1);
   dec.load<REV>(la, walk.at(0), len);
-  sx.template load<REV>(x, walk.at(0), len, DX);
-  sz.template load<REV>(z, walk.at(0), len, a.nz);
+  sx.load(Window(x + walk.at(0) * DX, len - walk.at(0), DX, 0));
+  sz.load(Window(z + walk.at(0) * a.nz, len - walk.at(0), a.nz, blk * DZ));
   dec.sum<REV>();
   if (walk.n > 1) dec.load<REV>(la, walk.at(1), len);
   for (int c = 0; c < walk.n; ++c) {
@@ -230,8 +230,9 @@ __device__ __forceinline__ void state_body(const ChunkArgs& a, const Span& sp, i
     if (wave == 0) dec.sum<REV>();
     if (c + 2 < walk.n) dec.load<REV>(la, walk.at(c + 2), len);
     if (c + 1 < walk.n) {
-      sx.template load<REV>(x, walk.at(c + 1), len, DX);
-      sz.template load<REV>(z, walk.at(c + 1), len, a.nz);
+      const long n0 = walk.at(c + 1);
+      sx.load(Window(x + n0 * DX, len - n0, DX, 0));
+      sz.load(Window(z + n0 * a.nz, len - n0, a.nz, blk * DZ));
     }
     st.update(lds);
   }
@@ -246,26 +247,6 @@ __global__ __launch_bounds__(NT) void state_kernel(ChunkArgs a, Span sp) {
   if (place(a.nz / DZ, a.chains * sp.writes, blk, unit)) state_body<TX, TZ, DX, DZ, REV>(a, sp, blk, unit, smem);
 }
 
-// Four consecutive inputs as they are in memory, and as floats.
-template <typename T>
-struct Raw4;
-template <>
-struct Raw4<uint16_t> {
-  uint2 u;
-  __device__ __forceinline__ void load(const uint16_t* p) { u = *reinterpret_cast<const uint2*>(p); }
-  __device__ __forceinline__ void zero() { u = uint2{0u, 0u}; }
-  __device__ __forceinline__ floatx4 values() const {
-    return floatx4{__uint_as_float(u.x << 16), __uint_as_float(u.x & 0xFFFF0000u),
-                   __uint_as_float(u.y << 16), __uint_as_float(u.y & 0xFFFF0000u)};
-  }
-};
-template <>
-struct Raw4<float> {
-  floatx4 u;
-  __device__ __forceinline__ void load(const float* p) { u = *reinterpret_cast<const floatx4*>(p); }
-  __device__ __forceinline__ void zero() { u = floatx4{0.f, 0.f, 0.f, 0.f}; }
-  __device__ __forceinline__ floatx4 values() const { return u; }
-};
 // Four values of NP planes in LDS.
 template <int NP>
 __device__ __forceinline__ floatx4 values4(const uint16_t* p, int stride) {
@@ -273,7 +254,7 @@ __device__ __forceinline__ floatx4 values4(const uint16_t* p, int stride) {
 #pragma unroll
   for (int i = NP - 1; i >= 0; --i) {
     Raw4<uint16_t> r;
-    r.load(p + i * stride);
+    r.u = *reinterpret_cast<const uint2*>(p + i * stride);
     x += r.values();
   }
   return x;
@@ -311,23 +292,17 @@ __device__ __forceinline__ void chunk_body(const ChunkArgs& a, const Span& sp, i
   const long U_sz = GRAD ? 1 : DX, U_sx = GRAD ? a.nz : 1, U_blk = (long)blk * DZ * U_sz;
   const long state = (long)a.nz * DX;
 
-  Stage<TX, DX> sx;
-  Stage<TZ, DZ> sz;
+  Stage<TX, DX, REV> sx(DX);
+  Stage<TZ, DZ, REV> sz(a.nz);
   State<DX, DZ> st;
   Decays dec;
-  Raw<TY> ry[NQ];
-  auto load_y = [&](long base) {
-    const long t = token<REV>(base, 16 * wave + m);
-#pragma unroll
-    for (int i = 0; i < NQ; ++i) {
-      if (t < len && 32 * i + 8 * g < DX) ry[i].load(y + t * DX + 32 * i + 8 * g);
-      else ry[i].zero();
-    }
-  };
+  const int ti = 16 * wave + m;                 // this lane's row of the chunk
+  Row<TY, DX, REV> ry;
+  const int u_at = (row_at<REV>(ti) * a.nz + 4 * g) * (int)sizeof(TZ);
   dec.load<REV>(la, walk.at(0), len);
-  sx.template load<REV>(x, walk.at(0), len, DX);
-  sz.template load<REV>(z, walk.at(0), len, a.nz);
-  load_y(walk.at(0));
+  sx.load(Window(x + walk.at(0) * DX, len - walk.at(0), DX, 0));
+  sz.load(Window(z + walk.at(0) * a.nz, len - walk.at(0), a.nz, blk * DZ));
+  ry.load(Window(y + walk.at(0) * DX, len - walk.at(0), DX, 0));
   dec.sum<REV>();
   if (walk.n > 1) dec.load<REV>(la, walk.at(1), len);
   if (sp.segs > 1) st.load(sp.states + (chain * (sp.writes + 1) + step) * state + U_blk, U_sz, U_sx);
@@ -345,31 +320,23 @@ __device__ __forceinline__ void chunk_body(const ChunkArgs& a, const Span& sp, i
     st.template to_planes<W>(lds.s[0], DZ * W);
     if (wave == 0) dec.store(lds);
     bf16x8 yf[NQ][NPY];
-#pragma unroll
-    for (int i = 0; i < NQ; ++i) {
-      uint4 f[NPY];
-      ry[i].split(f);
-#pragma unroll
-      for (int p = 0; p < NPY; ++p) yf[i][p] = __builtin_bit_cast(bf16x8, f[p]);
-    }
+    ry.frags(yf);
     __syncthreads();
-    const int ti = 16 * wave + m;               // this lane's row of the chunk
     const long t = token<REV>(walk.at(c), ti);
     // (loads come back in order: the one needed first is issued first)
     Raw4<TZ> ru[NDT];
     if (GRAD) {
+      const Window w(u + walk.at(c) * a.nz, len - walk.at(c), a.nz, blk * DZ);
 #pragma unroll
-      for (int d = 0; d < NDT; ++d) {
-        if (t < len) ru[d].load(u + t * a.nz + 16 * d + 4 * g);
-        else ru[d].zero();
-      }
+      for (int d = 0; d < NDT; ++d) ru[d].load(w, u_at + 16 * d * (int)sizeof(TZ));
     }
     if (wave == 0) dec.sum<REV>();
     if (c + 2 < walk.n) dec.load<REV>(la, walk.at(c + 2), len);
     if (c + 1 < walk.n) {
-      sx.template load<REV>(x, walk.at(c + 1), len, DX);
-      sz.template load<REV>(z, walk.at(c + 1), len, a.nz);
-      load_y(walk.at(c + 1));
+      const long n0 = walk.at(c + 1);
+      sx.load(Window(x + n0 * DX, len - n0, DX, 0));
+      sz.load(Window(z + n0 * a.nz, len - n0, a.nz, blk * DZ));
+      ry.load(Window(y + n0 * DX, len - n0, DX, 0));
     }
 
     // out^T: z rows x this wave's 16 tokens; first U's part
@@ -456,7 +423,7 @@ __device__ __forceinline__ void chunk_body(const ChunkArgs& a, const Span& sp, i
     if (t < len) {
 #pragma unroll
       for (int d = 0; d < NDT; ++d)
-        *reinterpret_cast<floatx4*>(out + t * a.nz + 16 * d + 4 * g) = acc[d];
+        __builtin_nontemporal_store(acc[d], reinterpret_cast<floatx4*>(out + t * a.nz + 16 * d + 4 * g));
     }
     st.update(lds);
   }
