@@ -289,12 +289,17 @@ struct Span {
                          // j + 1, then the state that segment j starts from in slot j
   float* decays;         // [chain][writes]: a segment's whole decay
 };
-// units: workgroups of one segment over all chains; most: chunks of a segment at most.
-// Segments until some 768 workgroups run, of four chunks at least.
-inline Span cut(long units, long seqlen, long most) {
+// units: workgroups of one segment over all chains; slots: how many the GPU holds at once,
+// which is what is aimed at; most: chunks of a segment at most; whole: sequences of fewer
+// chunks are not cut (the extra launches would cost more).  Segments have two chunks at
+// least.  Measured, us: 1x4x32771x128 forward 92 with 512 workgroups (what the GPU holds
+// of that kernel) against 104 with 768; 1x8xLx64 forward cut and whole: L 320 21 and 15,
+// L 512 21 and 22, L 1024 21 and 40; backward 1x8x256x64 29 and 27, 2x8x512x64 31 and 41;
+// two chunks against four: backward 1x5x4099x128x64 84 and 108.
+inline Span cut(long units, long seqlen, long slots, long most, long whole) {
   const long chunks = (seqlen + C - 1) / C;
-  long n = units < 768 ? 768 / units : 1;
-  if (n > chunks / 4) n = chunks / 4 > 1 ? chunks / 4 : 1;
+  long n = units < slots && chunks >= whole ? slots / units : 1;
+  if (n > chunks / 2) n = chunks / 2 > 1 ? chunks / 2 : 1;
   long per = (chunks + n - 1) / n;
   if (per > most) per = most;
   return Span{(int)((chunks + per - 1) / per), (int)per, 0, nullptr, nullptr};

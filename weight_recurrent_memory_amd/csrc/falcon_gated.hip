@@ -54,10 +54,12 @@ hipError_t launch_segments(const float* U0, const Span& sp, const float* U1, con
 
 namespace {
 
-// One workgroup's walk takes any number of chunks.
+// One workgroup's walk takes any number of chunks.  256 compute units hold two or three
+// workgroups of the chunk kernel each, one with float32 inputs at 128 columns.
 Span cut_of(const GatedArgs& a) {
   const long blocks = a.dv / rows_of(a.dv);
-  Span sp = cut((long)a.batch * a.heads * blocks, a.seqlen, 1l << 40);
+  const long held = a.dtype == 0 ? (a.dk <= 64 ? 3 : 2) : (a.dk <= 64 ? 2 : 1);
+  Span sp = cut((long)a.batch * a.heads * blocks, a.seqlen, 256 * held, 1l << 40, 8);
   sp.writes = sp.segs - 1;
   return sp;
 }

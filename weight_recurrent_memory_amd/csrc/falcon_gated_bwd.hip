@@ -388,7 +388,7 @@ Plan plan_of(const GatedBwdArgs& a) {
   p.chains = (long)a.batch * a.heads;
   p.state = (long)a.ndv * a.ndk;
   p.blocks = a.ndk / rows_of(a.ndk);
-  p.s = cut(p.chains * p.blocks, a.seqlen, kMostChunks);
+  p.s = cut(p.chains * p.blocks, a.seqlen, 512, kMostChunks, 5);
   p.r = p.s;
   // the end's state only where its gradient meets it
   p.s.writes = a.dS_L && a.dlog_a ? p.s.segs : p.s.segs - 1;
