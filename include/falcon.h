@@ -411,7 +411,8 @@ int falcon_bwd_chunk_noalloc(int variant, int window, int flags, float beta, con
  *   workspace          falcon_norm_out_bwd_workspace_bytes(...) bytes of device
  *                      memory, 16-byte aligned
  *
- * dk, dv in {16, 32, 64, 128}, bf16 or fp32; batch * L < 2^31.  Outputs overlap no
+ * dk, dv in {16, 32, 64, 128}, bf16 or fp32; batch * L < 2^31.  Rows are independent: a
+ * NaN or an infinity stays in its row (and in dweight).  Outputs overlap no
  * other argument, except that token-major outputs may interleave (views of one
  * fused buffer with one ld) and y as above.  Errors as elsewhere.
  */
@@ -455,7 +456,10 @@ int falcon_norm_out_bwd(int batch, int heads, int seqlen, int dv, int dtype, con
  *             rounding.
  * Finite inputs (log_a: also -inf) give the recurrence to float32 rounding: products
  * run on bf16 matrix cores with float32 operands in three bf16 parts, decays as
- * differences of float64 sums.  log_a > 0 (growth) is taken as given.
+ * differences of float64 sums.  log_a > 0 (growth) is taken as given.  A NaN or an
+ * infinity in a token reaches every output of its 64-token chunk, also of earlier
+ * tokens: rows of padding have to be finite (whatever they hold, no earlier token
+ * reads them).
  * batch * heads * dv < 2^27 (FALCON_ERR_UNSUPPORTED from there on).
  *
  * falcon_gated_bwd_chunk - gradients of sum <dO, o> + <dS_L, S_L>
@@ -467,8 +471,9 @@ int falcon_norm_out_bwd(int batch, int heads, int seqlen, int dv, int dtype, con
  *   dS0       [batch, heads, dv, dk] float32, or NULL (with S0 NULL: the gradient of
  *             the zero state)
  *   workspace falcon_gated_bwd_workspace_bytes(...) bytes, 16-byte aligned
- * Outputs and workspace overlap no other argument.  FALCON_ERR_UNSUPPORTED as the
- * forward, and from batch * heads * max(dk, dv) * ceil(L / 1024) = 2^27 on.
+ * Outputs and workspace overlap no other argument.  FALCON_ERR_UNSUPPORTED from
+ * batch * heads * max(dk, dv) * (L + 1023) / 1024 = 2^26 and from
+ * batch * heads * dk * dv = 2^32 on.
  *
  * falcon_gated_decode_step - one token for serving: S [nseq, heads, dv, dk]
  * float32 updated in place, q, k [nseq, heads, dk], v [nseq, heads, dv], log_a

@@ -222,6 +222,68 @@ def test_backward_of_many_chains():
     _check_backward(_inputs(25, 30, 40, 1100, 16, 16, torch.bfloat16, gate="resets"), 26)
 
 
+@pytest.mark.parametrize("dtype,d", [(torch.bfloat16, 128), (torch.float32, 64), (torch.float32, 128)])
+def test_captured_with_large_lds(dtype, d):
+    """Kernels with more than 64 KB of LDS, captured and replayed on other inputs."""
+    xs = [_inputs(40 + i, 1, 2, 600, d, d, dtype) for i in range(2)]
+    dO = _up(np.random.default_rng(42).standard_normal((1, 2, 600, d)))
+
+    def run(x):
+        o, S = fw.gated_fwd_chunk(x["q"], x["k"], x["v"], x["log_a"], S0=x["S0"], return_state=True)
+        g = fw.gated_bwd_chunk(x["q"], x["k"], x["v"], x["log_a"], dO, S0=x["S0"], dS_L=S)
+        return [o, S] + [g[n] for n in sorted(g)]
+    want = [[t.clone() for t in run(x)] for x in xs]
+    bound = {n: t.clone() for n, t in xs[0].items()}
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        outs = run(bound)
+    for rep in (0, 1, 0, 1):
+        for n, t in bound.items():
+            t.copy_(xs[rep][n])
+        graph.replay()
+        run(xs[rep])
+        torch.cuda.synchronize()
+        assert all(torch.equal(a, b) for a, b in zip(outs, want[rep])), rep
+
+
+def test_growing_state():
+    """log_a > 0: gates above one, the state grows by e^(0.05 L)."""
+    x = _inputs(43, 1, 2, 200, 32, 64, torch.bfloat16)
+    x["log_a"] = x["log_a"].abs() * 0.5
+    x["log_a"][..., ::7] *= -1
+    _check_forward(x)
+    _check_backward(x, 44)
+
+
+def test_offsets_beyond_32_bits():
+    """One chain of nine million tokens of 128 columns (o is 4.6 GB): the last 100 tokens,
+    behind a reset, are a sequence of their own, and their gradients too."""
+    L, n, d = 9_000_011, 100, 128
+    tail = _inputs(45, 1, 1, n, d, d, torch.bfloat16, start=False)
+    tail["log_a"][..., 0] = -float("inf")
+    x = {m: torch.full((1, 1, L, d), 0.01, device="cuda", dtype=torch.bfloat16) for m in ("q", "k", "v")}
+    x["log_a"] = torch.full((1, 1, L), -0.1, device="cuda")
+    for m, t in x.items():
+        t[:, :, -n:] = tail[m]
+    dO = torch.zeros((1, 1, L, d), device="cuda")
+    dO[:, :, -n:] = 1.0
+    o, S = fw.gated_fwd_chunk(x["q"], x["k"], x["v"], x["log_a"], return_state=True)
+    ro, rS, ao, aS = _forward_ref(tail)
+    _meets("o", o[:, :, -n:], ro, ao, _factor(n + 64, d, d))
+    _meets("S", S, rS, aS, _factor(n + 64, d, d))
+    del o
+    g = fw.gated_bwd_chunk(x["q"], x["k"], x["v"], x["log_a"], dO)
+    a = [_np(tail[m]) for m in ("q", "k", "v", "log_a")]
+    ones = np.ones((1, 1, n, d))
+    ref = bo.gated_backward(*a, ones)
+    size = bo.gated_backward(*[np.abs(y) for y in a[:3]], a[3], ones)
+    for m in ("dq", "dk", "dv"):
+        _meets(m, g[m][:, :, -n:], ref[m], size[m], _factor(n + 64, d, d) + d)
+        assert not g[m][:, :, :-n].any()                # nothing passes the reset
+    assert not g["dlog_a"][:, :, :-n + 1].any()
+
+
 def test_backward_against_differences():
     """Along random directions, central differences of the fp64 recurrence: their own
     error is about 1e-8 of values of order one, the kernels' 1e-5 of the absolute sum."""

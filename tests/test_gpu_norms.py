@@ -173,6 +173,29 @@ def test_norm_out_bwd(shape, dtype, kind):
     _meets(d["dO"], ref["dO"], _heads_first((3 * dv + 64) * U * size))
 
 
+def test_offsets_beyond_32_bits():
+    """2^31 elements and more: the last tokens' rows, zeros before them."""
+    L, H, d, n = (1 << 20) + 5, 16, 128, 9
+    x = torch.zeros((1, L, H, d), device="cuda", dtype=torch.bfloat16)
+    x[:, -n:] = _rand(50, 1, n, H, d, dtype=torch.bfloat16)
+    q, k, _ = fw.norm_in(x, x)
+    small = fw.norm_in(x[:, -n:].contiguous(), x[:, -n:].contiguous())
+    assert torch.equal(q[:, :, -n:], small[0]) and torch.equal(k[:, :, -n:], small[1])
+    assert not q[:, :, :1000].any() and not q[:, :, -2000:-n].any()
+    del q, k
+    o = torch.zeros((1, H, L, d), device="cuda")
+    o[:, :, -n:] = _rand(51, 1, H, n, d)
+    w = 1 + _rand(52, d, std=0.1)
+    y = fw.norm_out(o, w, x)
+    cut = o[:, :, -n:].contiguous(), w, x[:, -n:].contiguous()
+    assert torch.equal(y[:, -n:], fw.norm_out(*cut)) and not y[:, :-n].any()
+    got = fw.norm_out_bwd(o, w, y, x)
+    ref = fw.norm_out_bwd(cut[0], w, y[:, -n:].contiguous(), cut[2])
+    assert torch.equal(got["dO"][:, :, -n:], ref["dO"]) and torch.equal(got["dgate"][:, -n:], ref["dgate"])
+    # other workgroups' zeros beside the same terms: the sums' order may differ
+    assert torch.allclose(got["dweight"], ref["dweight"], rtol=1e-5, atol=1e-4)
+
+
 def test_norm_out_gradient_against_differences():
     """The kernels' gradients along random directions against central differences of
     the fp64 definition: they agree to the differences' own error (about 1e-9) and the

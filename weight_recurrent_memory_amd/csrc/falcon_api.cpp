@@ -819,8 +819,9 @@ FALCON_EXPORT int falcon_gated_fwd_chunk(int batch, int heads, int seqlen, int d
 namespace {
 
 bool gated_bwd_sizes(int batch, int heads, int seqlen, int dk, int dv) {
-  const double segs = ((double)seqlen + 1023.0) / 1024.0;
-  return (double)batch * heads * (dk > dv ? dk : dv) * segs < 134217728.0;  // 2^27
+  const double chains = (double)batch * heads, segs = ((double)seqlen + 1023.0) / 1024.0;
+  return chains * (dk > dv ? dk : dv) * segs < 67108864.0 &&  // 2^26
+         chains * dk * dv < 4294967296.0;                     // one thread per state element
 }
 
 // Bytes for any combination of the optional arguments: non-null stand-ins.

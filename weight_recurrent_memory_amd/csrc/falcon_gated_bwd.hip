@@ -10,7 +10,8 @@
 // both without the product of a token with itself, which passes no border and would only
 // leave its rounding behind; then inside a segment
 //   dlog_a_t = X + sum_{t'>=t} r_t' - sum_{s>=t} c_s,   X = <R, S> at the segment's end,
-// summed in float64.  Segments are 16 chunks at most, so that an X is never far away.
+// summed in float64.  Segments are 16 chunks at most, so that an X is never far away; at
+// a reset the sum is 0 and begins anew, so that nothing of one document is left in another.
 #include "falcon_gated_chunk.h"
 
 namespace falcon {
@@ -58,32 +59,59 @@ __global__ __launch_bounds__(NT) void gate_kernel(GateArgs a, Span s, Span r) {
   const double X = block_sum(x, lds);
   const long len = a.seqlen, t0 = (long)seg * s.chunks * C;
   const long end = t0 + (long)s.chunks * C < len ? t0 + (long)s.chunks * C : len;
-  // thread i: the four tokens 4 i .. from the segment's last one backward
+  // thread i: the four tokens 4 i .. from the segment's last one backward; `cut` once a
+  // reset has begun the sum anew
   double sum[4], mine = 0.0;
+  bool cut = false, reset[4];
 #pragma unroll
   for (int j = 0; j < 4; ++j) {
     const long t = end - 1 - 4 * (long)threadIdx.x - j;
     double rr = 0.0, cc = 0.0;
+    reset[j] = false;
     if (t >= t0) {
       for (int b = 0; b < a.blocks; ++b) {
         rr += a.r[(b * a.chains + chain) * len + t];
         cc += a.c[(b * a.chains + chain) * len + t];
       }
+      reset[j] = a.log_a[chain * len + t] < -1000.0f;
     }
     mine += rr - cc;
     sum[j] = mine;
+    if (reset[j]) {
+      mine = 0.0;
+      cut = true;
+    }
   }
-  const double upto = wave_scan(mine);
+  // the sum, and whether a reset lies in it, up to and with each thread, then before it
+  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+  double upto = mine;
+  int any = cut;
+#pragma unroll
+  for (int m = 1; m < 64; m <<= 1) {
+    const double y = __shfl_up(upto, m, 64);
+    const int f = __shfl_up(any, m, 64);
+    if (lane >= m) {
+      if (!any) upto += y;
+      any |= f;
+    }
+  }
   __syncthreads();
-  if ((threadIdx.x & 63) == 63) lds[threadIdx.x >> 6] = upto;
+  __shared__ int flag[4];
+  if (lane == 63) {
+    lds[wave] = upto;
+    flag[wave] = any;
+  }
   __syncthreads();
-  double before = X + upto - mine;
-  for (int w = 0; w < (int)(threadIdx.x >> 6); ++w) before += lds[w];
+  double before = X;
+  for (int w = 0; w < wave; ++w) before = flag[w] ? lds[w] : before + lds[w];
+  const double up = __shfl_up(upto, 1, 64);
+  const int upf = __shfl_up(any, 1, 64);
+  if (lane > 0) before = upf ? up : before + up;
 #pragma unroll
   for (int j = 0; j < 4; ++j) {
     const long t = end - 1 - 4 * (long)threadIdx.x - j;
-    // nothing passes a reset
-    if (t >= t0) a.dlog_a[chain * len + t] = a.log_a[chain * len + t] < -1000.0f ? 0.0f : (float)(before + sum[j]);
+    if (t >= t0) a.dlog_a[chain * len + t] = reset[j] ? 0.0f : (float)(before + sum[j]);
+    if (reset[j]) before = 0.0;
   }
 }
 
