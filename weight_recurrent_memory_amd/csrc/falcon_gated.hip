@@ -8,6 +8,7 @@
 
 namespace falcon {
 namespace gated {
+namespace {
 
 // The recurrence over segments: start of step j + 1 = decay_j start_j + write_j, in place,
 // slot 0 set to U0 (so that the last segment may write its result over U0).  Of one span
@@ -44,6 +45,8 @@ __global__ __launch_bounds__(256) void segments_kernel(const float* U0, Span sp,
     }
   }
 }
+
+}  // namespace
 
 hipError_t launch_segments(const float* U0, const Span& sp, const float* U1, const Span& sp1, long chains,
                            long state, hipStream_t stream) {

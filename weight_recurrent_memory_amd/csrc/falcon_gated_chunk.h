@@ -27,6 +27,13 @@
 namespace falcon {
 namespace gated {
 
+// Of two spans (sp1.writes > 0) or one: the states that segments start from, out of every
+// segment's own write (falcon_gated.hip).
+hipError_t launch_segments(const float* U0, const Span& sp, const float* U1, const Span& sp1, long chains,
+                           long state, hipStream_t stream);
+
+namespace {        // (a kernel's name would be exported from the library)
+
 struct ChunkArgs {
   const void* x;         // [chain][L][DX]
   const void* y;
@@ -487,11 +494,7 @@ hipError_t with_sizes(int dx, int nz, F&& f) {
 }
 
 // The states that segments start from: every segment's own write, then the recurrence
-// over segments (segments_kernel in falcon_gated.hip).
-// Of one span, or of two (sp1.writes > 0) with as many chains and states as large.
-hipError_t launch_segments(const float* U0, const Span& sp, const float* U1, const Span& sp1, long chains,
-                           long state, hipStream_t stream);
-
+// over segments.
 template <typename TX, typename TZ, bool REV>
 hipError_t launch_states(const ChunkArgs& a, int dx, const Span& sp, hipStream_t stream) {
   if (sp.writes == 0) return hipSuccess;
@@ -516,5 +519,6 @@ inline size_t span_bytes(const Span& sp, long chains, long state) {
   return (span_floats(sp, chains, state) + 3) / 4 * 16;
 }
 
+}  // namespace
 }  // namespace gated
 }  // namespace falcon
