@@ -315,8 +315,15 @@ __device__ __forceinline__ bool place(int blocks, long units, int& block, long& 
 }
 inline unsigned grid_of(int blocks, long units) { return (unsigned)((units + 7) / 8 * 8 * blocks); }
 
-// z rows of a workgroup.
-inline int rows_of(int nz) { return nz < 64 ? nz : 64; }
+// z rows of a workgroup: 64, or less where chains and segments (of two chunks) alone leave
+// compute units without work.  Each row block forms the scores anew, so a full GPU takes
+// as few as it can.
+inline int rows_of(int nz, long chains, long seqlen, long whole) {
+  const long chunks = (seqlen + C - 1) / C, segs = chunks >= whole ? chunks / 2 : 1;
+  int rows = nz < 64 ? nz : 64;
+  while (rows > 16 && chains * segs * (nz / rows) < 256) rows /= 2;
+  return rows;
+}
 
 }  // namespace gated
 }  // namespace falcon

@@ -59,10 +59,12 @@ namespace {
 
 // One workgroup's walk takes any number of chunks.  256 compute units hold two or three
 // workgroups of the chunk kernel each, one with float32 inputs at 128 columns.
+constexpr long kWhole = 8;
+int block_of(const GatedArgs& a) { return rows_of(a.dv, (long)a.batch * a.heads, a.seqlen, kWhole); }
 Span cut_of(const GatedArgs& a) {
-  const long blocks = a.dv / rows_of(a.dv);
+  const long blocks = a.dv / block_of(a);
   const long held = a.dtype == 0 ? (a.dk <= 64 ? 3 : 2) : (a.dk <= 64 ? 2 : 1);
-  Span sp = cut((long)a.batch * a.heads * blocks, a.seqlen, 256 * held, 1l << 40, 8);
+  Span sp = cut((long)a.batch * a.heads * blocks, a.seqlen, 256 * held, 1l << 40, kWhole);
   sp.writes = sp.segs - 1;
   return sp;
 }
@@ -71,9 +73,9 @@ template <typename T>
 hipError_t run(const GatedArgs& a, const Span& sp, hipStream_t stream) {
   const ChunkArgs c{a.k, a.q, a.v, a.log_a, a.S0, a.o, a.S_out, nullptr, nullptr,
                     (long)a.batch * a.heads, a.seqlen, a.dv};
-  const hipError_t e = launch_states<T, T, false>(c, a.dk, sp, stream);
+  const hipError_t e = launch_states<T, T, false>(c, a.dk, block_of(a), sp, stream);
   if (e != hipSuccess) return e;
-  return with_sizes(a.dk, a.dv, [&](auto d, auto r) {
+  return with_sizes(a.dk, block_of(a), [&](auto d, auto r) {
     return go_chunk<T, T, T, decltype(d)::value, decltype(r)::value, false, false>(c, sp, stream);
   });
 }

@@ -19,6 +19,7 @@ namespace gated {
 namespace {
 
 constexpr int kMostChunks = 16;            // of a segment: 1024 tokens
+constexpr long kWhole = 5;                 // chunks from which a sequence is cut
 
 struct GateArgs {
   const float* log_a;
@@ -404,6 +405,7 @@ hipError_t with_small(int dk, int dv, F&& f) {
 // and its workspace.
 struct Plan {
   Span s, r;
+  int block_k, block_v;    // columns of a workgroup of dq and dk, and of dv
   int blocks;              // of dq's and dk's columns
   long chains, state;
   size_t bytes() const {
@@ -415,8 +417,11 @@ Plan plan_of(const GatedBwdArgs& a) {
   Plan p;
   p.chains = (long)a.batch * a.heads;
   p.state = (long)a.ndv * a.ndk;
-  p.blocks = a.ndk / rows_of(a.ndk);
-  p.s = cut(p.chains * p.blocks, a.seqlen, 512, kMostChunks, 5);
+  const bool both = a.ndk <= 64 && a.ndv <= 64;      // dk and dv in one workgroup: all columns
+  p.block_k = both ? a.ndk : rows_of(a.ndk, p.chains, a.seqlen, kWhole);
+  p.block_v = both ? a.ndv : rows_of(a.ndv, p.chains, a.seqlen, kWhole);
+  p.blocks = a.ndk / p.block_k;
+  p.s = cut(p.chains * p.blocks, a.seqlen, 512, kMostChunks, kWhole);
   p.r = p.s;
   // the end's state only where its gradient meets it
   p.s.writes = a.dS_L && a.dlog_a ? p.s.segs : p.s.segs - 1;
@@ -446,17 +451,17 @@ hipError_t run(const GatedBwdArgs& a, Plan p, hipStream_t stream) {
       return both<T, decltype(nk)::value, decltype(nv)::value>(S, R, dq, kv, p.s, p.r, stream);
     });
   } else {
-    if ((e = launch_states<T, T, false>(S, a.ndk, p.s, stream)) != hipSuccess) return e;
-    if ((e = launch_states<T, float, true>(R, a.ndk, p.r, stream)) != hipSuccess) return e;
-    e = with_sizes(a.ndv, a.ndk, [&](auto d, auto z) {
+    if ((e = launch_states<T, T, false>(S, a.ndk, p.block_v, p.s, stream)) != hipSuccess) return e;
+    if ((e = launch_states<T, float, true>(R, a.ndk, p.block_v, p.r, stream)) != hipSuccess) return e;
+    e = with_sizes(a.ndv, p.block_k, [&](auto d, auto z) {
       return go_chunk<T, float, T, decltype(d)::value, decltype(z)::value, false, true>(dq, p.s, stream);
     });
     if (e != hipSuccess) return e;
-    e = with_sizes(a.ndv, a.ndk, [&](auto d, auto z) {
+    e = with_sizes(a.ndv, p.block_k, [&](auto d, auto z) {
       return go_chunk<float, T, T, decltype(d)::value, decltype(z)::value, true, true>(dk, p.r, stream);
     });
     if (e != hipSuccess) return e;
-    e = with_sizes(a.ndk, a.ndv, [&](auto d, auto z) {
+    e = with_sizes(a.ndk, p.block_v, [&](auto d, auto z) {
       return go_chunk<T, T, float, decltype(d)::value, decltype(z)::value, true, false>(dv, p.r, stream);
     });
   }

@@ -473,11 +473,11 @@ hipError_t go_chunk(const ChunkArgs& a, const Span& sp, hipStream_t stream) {
   return hipGetLastError();
 }
 
-// f(size, rows) as constants for dx columns and blocks of z rows of nz.
+// f(size, rows) as constants for dx columns and blocks of `block` z rows.
 template <class F>
-hipError_t with_sizes(int dx, int nz, F&& f) {
+hipError_t with_sizes(int dx, int block, F&& f) {
   auto rows = [&](auto d) {
-    switch (rows_of(nz)) {
+    switch (block) {
       case 16: return f(d, std::integral_constant<int, 16>());
       case 32: return f(d, std::integral_constant<int, 32>());
       case 64: return f(d, std::integral_constant<int, 64>());
@@ -496,9 +496,9 @@ hipError_t with_sizes(int dx, int nz, F&& f) {
 // The states that segments start from: every segment's own write, then the recurrence
 // over segments.
 template <typename TX, typename TZ, bool REV>
-hipError_t launch_states(const ChunkArgs& a, int dx, const Span& sp, hipStream_t stream) {
+hipError_t launch_states(const ChunkArgs& a, int dx, int block, const Span& sp, hipStream_t stream) {
   if (sp.writes == 0) return hipSuccess;
-  const hipError_t e = with_sizes(dx, a.nz, [&](auto d, auto r) {
+  const hipError_t e = with_sizes(dx, block, [&](auto d, auto r) {
     return go_state<TX, TZ, decltype(d)::value, decltype(r)::value, REV>(a, sp, stream);
   });
   return e != hipSuccess ? e : launch_segments(a.U0, sp, nullptr, Span{}, a.chains, (long)a.nz * dx, stream);
