@@ -382,14 +382,73 @@ hipError_t both(const ChunkArgs& S, const ChunkArgs& R, const ChunkArgs& q, cons
   hipLaunchKernelGGL(kernel, dim3(grid_of(2, S.chains * s.segs)), dim3(NT), bytes, stream, q, kv, s, r);
   return hipGetLastError();
 }
-// f(dk, dv) as constants up to 64
-template <class F>
-hipError_t with_small(int dk, int dv, F&& f) {
+// The same with a size of 128, in blocks of B columns: dk, dq and dv one after the other.
+template <typename T, int DK, int DV, int B>
+struct Wide {
+  static constexpr int BK = DK < B ? DK : B, BV = DV < B ? DV : B, NK = DK / BK, NV = DV / BV;
+  static constexpr size_t a = sizeof(Lds<float, T, DV, BK>), b = sizeof(Lds<T, T, DV, BK>),
+                          c = sizeof(Lds<T, float, DK, BV>);
+  static constexpr size_t bytes = a > b ? (a > c ? a : c) : (b > c ? b : c);
+  static constexpr int held = sizeof(T) == 2 && 2 * bytes <= 163840 ? 2 : 1;     // on a compute unit
+};
+template <typename T, int DK, int DV, int B>
+__global__ __launch_bounds__(NT) void wide_states_kernel(ChunkArgs S, Span s, ChunkArgs R, Span r) {
+  extern __shared__ __align__(16) unsigned char smem[];
+  using X = Wide<T, DK, DV, B>;
+  int blk;
+  long unit;
+  const long ns = S.chains * s.writes, nr = R.chains * r.writes;
+  if (!place(2 * X::NV, ns > nr ? ns : nr, blk, unit)) return;
+  if (blk < X::NV) {
+    if (unit < ns) state_body<T, T, DK, X::BV, false>(S, s, blk, unit, smem);
+  } else {
+    if (unit < nr) state_body<T, float, DK, X::BV, true>(R, r, blk - X::NV, unit, smem);
+  }
+}
+template <typename T, int DK, int DV, int B>
+__global__ __launch_bounds__(NT, (Wide<T, DK, DV, B>::held)) void wide_gradients_kernel(
+    ChunkArgs q, ChunkArgs k, ChunkArgs v, Span s, Span r) {
+  extern __shared__ __align__(16) unsigned char smem[];
+  using X = Wide<T, DK, DV, B>;
+  const long n = q.chains * s.segs, n8 = (n + 7) / 8 * 8;
+  const int role = (int)(blockIdx.x / n8);
+  const long unit = blockIdx.x % n8;
+  if (unit >= n) return;
+  if (role < X::NK) chunk_body<float, T, T, DV, X::BK, true, true>(k, r, role, unit, smem);
+  else if (role < 2 * X::NK) chunk_body<T, float, T, DV, X::BK, false, true>(q, s, role - X::NK, unit, smem);
+  else chunk_body<T, T, float, DK, X::BV, true, false>(v, r, role - 2 * X::NK, unit, smem);
+}
+template <typename T, int DK, int DV, int B>
+hipError_t wide(const ChunkArgs& S, const ChunkArgs& R, const ChunkArgs& q, const ChunkArgs& k,
+                const ChunkArgs& v, const Span& s, const Span& r, hipStream_t stream) {
+  using X = Wide<T, DK, DV, B>;
+  hipError_t e;
+  const long writes = s.writes > r.writes ? s.writes : r.writes;
+  if (writes > 0) {
+    constexpr size_t bytes = sizeof(LdsState<T, float, DK, X::BV>);
+    auto kernel = wide_states_kernel<T, DK, DV, B>;
+    if ((e = lds_limit(kernel, bytes)) != hipSuccess) return e;
+    hipLaunchKernelGGL(kernel, dim3(grid_of(2 * X::NV, S.chains * writes)), dim3(NT), bytes, stream, S, s, R, r);
+    if ((e = hipGetLastError()) != hipSuccess) return e;
+    if ((e = launch_segments(S.U0, s, R.U0, r, S.chains, (long)DK * DV, stream)) != hipSuccess) return e;
+  }
+  auto kernel = wide_gradients_kernel<T, DK, DV, B>;
+  if ((e = lds_limit(kernel, X::bytes)) != hipSuccess) return e;
+  hipLaunchKernelGGL(kernel, dim3(grid_of(2 * X::NK + X::NV, S.chains * s.segs)), dim3(NT), X::bytes, stream,
+                     q, k, v, s, r);
+  return hipGetLastError();
+}
+
+// f(dk, dv) as constants: both up to 64, or one of them 128
+template <bool WIDE, class F>
+hipError_t with_dims(int dk, int dv, F&& f) {
   auto cols = [&](auto k) {
+    constexpr bool big = decltype(k)::value == 128;
     switch (dv) {
-      case 16: return f(k, std::integral_constant<int, 16>());
-      case 32: return f(k, std::integral_constant<int, 32>());
-      case 64: return f(k, std::integral_constant<int, 64>());
+      case 16: if constexpr (big == WIDE) return f(k, std::integral_constant<int, 16>()); break;
+      case 32: if constexpr (big == WIDE) return f(k, std::integral_constant<int, 32>()); break;
+      case 64: if constexpr (big == WIDE) return f(k, std::integral_constant<int, 64>()); break;
+      case 128: if constexpr (WIDE) return f(k, std::integral_constant<int, 128>()); break;
     }
     return hipErrorInvalidValue;
   };
@@ -397,6 +456,7 @@ hipError_t with_small(int dk, int dv, F&& f) {
     case 16: return cols(std::integral_constant<int, 16>());
     case 32: return cols(std::integral_constant<int, 32>());
     case 64: return cols(std::integral_constant<int, 64>());
+    case 128: if constexpr (WIDE) return cols(std::integral_constant<int, 128>()); break;
   }
   return hipErrorInvalidValue;
 }
@@ -405,7 +465,7 @@ hipError_t with_small(int dk, int dv, F&& f) {
 // and its workspace.
 struct Plan {
   Span s, r;
-  int block_k, block_v;    // columns of a workgroup of dq and dk, and of dv
+  int block;               // columns of a workgroup at most; 0: all
   int blocks;              // of dq's and dk's columns
   long chains, state;
   size_t bytes() const {
@@ -417,10 +477,9 @@ Plan plan_of(const GatedBwdArgs& a) {
   Plan p;
   p.chains = (long)a.batch * a.heads;
   p.state = (long)a.ndv * a.ndk;
-  const bool both = a.ndk <= 64 && a.ndv <= 64;      // dk and dv in one workgroup: all columns
-  p.block_k = both ? a.ndk : rows_of(a.ndk, p.chains, a.seqlen, kWhole);
-  p.block_v = both ? a.ndv : rows_of(a.ndv, p.chains, a.seqlen, kWhole);
-  p.blocks = a.ndk / p.block_k;
+  // up to 64 columns dk and dv are one workgroup's
+  p.block = a.ndk <= 64 && a.ndv <= 64 ? 0 : rows_of(128, p.chains, a.seqlen, kWhole);
+  p.blocks = p.block && p.block < a.ndk ? a.ndk / p.block : 1;
   p.s = cut(p.chains * p.blocks, a.seqlen, 512, kMostChunks, kWhole);
   p.r = p.s;
   // the end's state only where its gradient meets it
@@ -445,24 +504,19 @@ hipError_t run(const GatedBwdArgs& a, Plan p, hipStream_t stream) {
   const ChunkArgs dq{a.v, a.dO, a.k, a.log_a, a.S0, a.dq, nullptr, a.q, r, p.chains, a.seqlen, a.ndk};
   const ChunkArgs dk{a.dO, a.v, a.q, a.log_a, a.dS_L, a.dk, nullptr, a.k, c, p.chains, a.seqlen, a.ndk};
   const ChunkArgs dv{a.q, a.k, a.dO, a.log_a, a.dS_L, a.dv, a.dS0, nullptr, nullptr, p.chains, a.seqlen, a.ndv};
-  if (a.ndk <= 64 && a.ndv <= 64) {
-    e = with_small(a.ndk, a.ndv, [&](auto nk, auto nv) {
+  if (p.block == 0) {
+    e = with_dims<false>(a.ndk, a.ndv, [&](auto nk, auto nv) {
       const KVArgs kv{a.q, a.k, a.v, a.dO, a.log_a, a.dS_L, a.dk, a.dv, a.dS0, c, p.chains, a.seqlen};
       return both<T, decltype(nk)::value, decltype(nv)::value>(S, R, dq, kv, p.s, p.r, stream);
     });
   } else {
-    if ((e = launch_states<T, T, false>(S, a.ndk, p.block_v, p.s, stream)) != hipSuccess) return e;
-    if ((e = launch_states<T, float, true>(R, a.ndk, p.block_v, p.r, stream)) != hipSuccess) return e;
-    e = with_sizes(a.ndv, p.block_k, [&](auto d, auto z) {
-      return go_chunk<T, float, T, decltype(d)::value, decltype(z)::value, false, true>(dq, p.s, stream);
-    });
-    if (e != hipSuccess) return e;
-    e = with_sizes(a.ndv, p.block_k, [&](auto d, auto z) {
-      return go_chunk<float, T, T, decltype(d)::value, decltype(z)::value, true, true>(dk, p.r, stream);
-    });
-    if (e != hipSuccess) return e;
-    e = with_sizes(a.ndk, p.block_v, [&](auto d, auto z) {
-      return go_chunk<T, T, float, decltype(d)::value, decltype(z)::value, true, false>(dv, p.r, stream);
+    e = with_dims<true>(a.ndk, a.ndv, [&](auto nk, auto nv) {
+      constexpr int DK = decltype(nk)::value, DV = decltype(nv)::value;
+      switch (p.block) {
+        case 16: return wide<T, DK, DV, 16>(S, R, dq, dk, dv, p.s, p.r, stream);
+        case 32: return wide<T, DK, DV, 32>(S, R, dq, dk, dv, p.s, p.r, stream);
+        default: return wide<T, DK, DV, 64>(S, R, dq, dk, dv, p.s, p.r, stream);
+      }
     });
   }
   if (e != hipSuccess || !a.dlog_a) return e;
