@@ -478,7 +478,16 @@ Plan plan_of(const GatedBwdArgs& a) {
   p.chains = (long)a.batch * a.heads;
   p.state = (long)a.ndv * a.ndk;
   // up to 64 columns dk and dv are one workgroup's
-  p.block = a.ndk <= 64 && a.ndv <= 64 ? 0 : rows_of(128, p.chains, a.seqlen, kWhole);
+  p.block = 0;
+  if (a.ndk > 64 || a.ndv > 64) {
+    // bf16 with dk >= 64: 32 columns leave room for two workgroups on a compute unit, 64
+    // for one (4x16x2048x128: 318 us against 354, 8x16x1024x128x64: 164 against 212); with
+    // dk 16 and 32 there is room for two of 64 (8x16x1024x16x128: 110 against 130 us of
+    // 32), with float32 inputs for one of either (2x16x2048x128: 310 against 366 us)
+    const int most = a.dtype == 0 && a.ndk >= 64 ? 32 : 64;
+    p.block = rows_of(128, p.chains, a.seqlen, kWhole);
+    if (p.block > most) p.block = most;
+  }
   p.blocks = p.block && p.block < a.ndk ? a.ndk / p.block : 1;
   p.s = cut(p.chains * p.blocks, a.seqlen, 512, kMostChunks, kWhole);
   p.r = p.s;
