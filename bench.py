@@ -19,7 +19,8 @@ Prints one JSON line.  Besides the contract fields it carries
   secondary     the other workloads: Falcon-1A, per-channel Falcon-2, windowed
                 Falcon-3/3A at d = 128, the backward of the headline workload,
                 the decode step (warm, and cold: the state evicted from every
-                cache before each step), a copy kernel for attainable bandwidth,
+                cache before each step), a block's norms around an update and
+                the gated recurrence, a copy kernel for attainable bandwidth,
                 and model-FLOP utilization.
 """
 from __future__ import annotations
@@ -424,6 +425,46 @@ def main():
                                            "cold_total_gbs": nb / sec_gc / 1e9,
                                            "cold_hbm_frac": nb / sec_gc / 1e9 / HBM_PEAK_GBS}}
             del S, qs, ks, vs
+            torch.cuda.empty_cache()
+        if args.only in (None, "block"):
+            # a block's path between two projections at the headline shape: unit q and
+            # k out of a fused projection (norm_in), an update (Falcon-1's chunk form,
+            # or the gated recurrence), the gated norm onto the residual stream
+            # (norm_out); and the gated recurrence's gradients and decode step
+            B, H, L, dk, dv = 8, 12, 2048, 64, 64
+            g = torch.Generator(device=dev).manual_seed(1006)
+            rn = lambda *s: torch.randn(s, generator=g, device=dev)  # noqa: E731
+            p = rn(B, L, 4, H, dk).to(torch.bfloat16)
+            res, w = rn(B, L, H, dv).to(torch.bfloat16), torch.ones(dv, device=dev)
+            log_a = torch.nn.functional.logsigmoid(rn(B, H, L) + 4)
+            q, k, v = fw.norm_in(p[:, :, 0], p[:, :, 1], p[:, :, 2])
+            dO = rn(B, H, L, dv)
+
+            def block(update):
+                q, k, v = fw.norm_in(p[:, :, 0], p[:, :, 1], p[:, :, 2])
+                return fw.norm_out(update(q, k, v), w, p[:, :, 3], residual=res)
+            falcon = lambda q, k, v: fw.fwd_chunk(q, k, v, variant=fw.FALCON_1, beta=0.5,  # noqa: E731
+                                                  lam=0.01, eps=1e-6)
+            gated = lambda q, k, v: fw.gated_fwd_chunk(q, k, v, log_a)  # noqa: E731
+            n = B * H * L
+            leg = {"workload": "block_8x12x2048x64"}
+            for name, fn, nb in (
+                    ("falcon1", lambda: block(falcon), n * (3 * dk * 4 + 3 * dk * 2 + dv * 10)),
+                    ("gated", lambda: block(gated), n * (3 * dk * 4 + 3 * dk * 2 + dv * 10 + 4)),
+                    ("gated_forward", lambda: gated(q, k, v), n * (3 * dk * 2 + dv * 4 + 4)),
+                    ("gated_backward", lambda: fw.gated_bwd_chunk(q, k, v, log_a, dO),
+                     n * (3 * dk * 2 + dv * 4 + 3 * dk * 4 + 8))):
+                sec = time_calls(fn, 20, 5)
+                leg[name] = {"us_per_call": sec * 1e6, "tokens_per_s": B * L / sec,
+                             "algorithmic_gbs": nb / sec / 1e9}
+            S = rn(512, H, dv, dk) * 0.02
+            qd, kd, vd = (x[0, :, :512].transpose(0, 1).contiguous() for x in (q, k, v))
+            la = log_a[0, :, :512].t().contiguous()
+            sec = time_calls(lambda: fw.gated_decode_step(S, qd, kd, vd, la), 100, 10)
+            nb = 512 * H * (8 * dk * dv + 3 * dk * 2 + 4 * dv + 4)
+            leg["gated_decode_512x12"] = {"us_per_step": sec * 1e6, "total_gbs": nb / sec / 1e9}
+            sec_out["block"] = leg
+            del p, res, q, k, v, dO, S
             torch.cuda.empty_cache()
         if args.only in (None, "copy"):
             # attainable bandwidth: device-to-device copy of 1 GiB (also the known-size

@@ -385,7 +385,8 @@ int falcon_bwd_chunk_noalloc(int variant, int window, int flags, float beta, con
  *   q_in, k_in, v_in   token-major, dtype; v_in and v may both be NULL
  *   q, k, v            head-major, dtype, contiguous
  *   eps                finite, >= 0 (eps = 0 with a zero row gives NaN)
- * Sums are float32; each output is rounded once.
+ * Sums are float32 (a row whose sum of squares overflows, entries from about 1e19 on,
+ * gives zeros); each output is rounded once.
  *
  * falcon_norm_in_bwd - its gradient: with r = 1 / sqrt(|x|^2 + eps), y = r x
  *   dx = r (dy - y (y . dy)) for q and k,  dv_in = dv
@@ -399,7 +400,7 @@ int falcon_bwd_chunk_noalloc(int variant, int window, int flags, float beta, con
  *   gate               token-major, dtype, or NULL (act = 1)
  *   gate_kind          FALCON_GATE_SILU (g / (1 + e^-g)) or FALCON_GATE_SIGMOID
  *   residual           token-major, dtype, or NULL; may equal y exactly (in place)
- *   scale              finite
+ *   scale              finite; eps as above
  *   y                  token-major, dtype
  *
  * falcon_norm_out_bwd - its gradients for o, gate and weight (the residual's is
@@ -453,7 +454,7 @@ int falcon_norm_out_bwd(int batch, int heads, int seqlen, int dv, int dtype, con
  *             NULL.  With workspace_bytes >= falcon_gated_fwd_workspace_bytes(...)
  *             a long sequence of few chains is cut into segments that run side by
  *             side; otherwise each chain is walked in order.  Results agree up to
- *             rounding.
+ *             rounding.  A workspace serves one call at a time.
  * Finite inputs (log_a: also -inf) give the recurrence to float32 rounding: products
  * run on bf16 matrix cores with float32 operands in three bf16 parts, decays as
  * differences of float64 sums.  log_a > 0 (growth) is taken as given.  A NaN or an

@@ -171,6 +171,25 @@ def test_another_stream():
         assert all(torch.equal(d[n], grads[n]) for n in grads)
 
 
+def test_default_stream_by_its_handle_and_empty_calls():
+    x = _batch(9, torch.bfloat16, l=20)
+    q_in, k_in, v_in, _ = _views(x["p"])
+    torch.cuda.synchronize()
+    q, k, v = fw.norm_in(q_in, k_in, v_in, stream=0)
+    torch.cuda.synchronize()
+    want = fw.norm_in(q_in, k_in, v_in)
+    assert all(torch.equal(a, b) for a, b in zip((q, k, v), want))
+    # no tokens, no sequences: refused as by the other entry points
+    none = q[:, :, :0].contiguous()
+    for call in (lambda: fw.gated_fwd_chunk(none, none, v[:, :, :0].contiguous()),
+                 lambda: fw.gated_fwd_chunk(q[:0], k[:0], v[:0]),
+                 lambda: fw.norm_in(q_in[:, :0], k_in[:, :0]),
+                 lambda: fw.norm_out(q[:, :, :0].float(), torch.ones(DK, device="cuda")),
+                 lambda: fw.gated_decode_step(x["S0"][:0], q[:0, :, 0], k[:0, :, 0], v[:0, :, 0])):
+        with pytest.raises((fw.FalconError, ValueError)):
+            call()
+
+
 def test_two_calls_at_once():
     """Two streams, two batches, no workspace in common."""
     xs = [_batch(6 + i, torch.bfloat16, l=900) for i in range(2)]

@@ -97,9 +97,9 @@ def norm_in_bwd(q_in, k_in, dq, dk, dv=None, *, eps=1e-6, out=None, stream=None)
     _b._expect(torch, "dv", dv, (B, H, L, ndv), f32, dev)
     with _b._guard(torch, dev, stream):
         if out is None:
-            out = (torch.empty((B, L, H, ndk), device=dev, dtype=dt),
-                   torch.empty((B, L, H, ndk), device=dev, dtype=dt),
-                   None if dv is None else torch.empty((B, L, H, ndv), device=dev, dtype=dt))
+            out = (q_in.new_empty((B, L, H, ndk)),
+                   q_in.new_empty((B, L, H, ndk)),
+                   None if dv is None else q_in.new_empty((B, L, H, ndv)))
         oqp, ldoq = _rows(torch, "out[0]", out[0], (B, L, H, ndk), dt, dev)
         okp, ldok = _rows(torch, "out[1]", out[1], (B, L, H, ndk), dt, dev)
         ovp, ldov = _rows(torch, "out[2]", out[2], (B, L, H, ndv), dt, dev)
@@ -133,7 +133,7 @@ def norm_out(o, weight, gate=None, *, gate_kind="silu", residual=None, scale=1.0
     rp, ldr = _rows(torch, "residual", residual, (B, L, H, dv), dt, dev)
     with _b._guard(torch, dev, stream):
         if out is None:
-            out = torch.empty((B, L, H, dv), device=dev, dtype=dt)
+            out = o.new_empty((B, L, H, dv), dtype=dt)
         dcode = _b._dtype_code(torch, out)
         yp, ldy = _rows(torch, "out", out, (B, L, H, dv), dt, dev)
         status = lib.falcon_norm_out(B, H, L, dv, dcode, _b._address(o), _b._address(weight), gp, ldg, kind,
@@ -163,14 +163,13 @@ def norm_out_bwd(o, weight, dy, gate=None, *, gate_kind="silu", scale=1.0, eps=1
     if gate is None and dgate is not None:
         raise ValueError("dgate without a gate")
     with _b._guard(torch, dev, stream):
-        res = dict(dO=torch.empty((B, H, L, dv), device=dev, dtype=f32),
-                   dweight=torch.empty((dv,), device=dev, dtype=f32))
+        res = dict(dO=o.new_empty((B, H, L, dv)),
+                   dweight=o.new_empty((dv,)))
         if gate is not None:
-            res["dgate"] = dgate if dgate is not None else torch.empty((B, L, H, dv), device=dev,
-                                                                       dtype=dt)
+            res["dgate"] = dgate if dgate is not None else dy.new_empty((B, L, H, dv))
         gop, ldgo = _rows(torch, "dgate", res.get("dgate"), (B, L, H, dv), dt, dev)
         need = int(lib.falcon_norm_out_bwd_workspace_bytes(B, L, dv))
-        ws = torch.empty(max(need, 16), device=dev, dtype=torch.uint8)
+        ws = o.new_empty((max(need, 16) // 4,))
         status = lib.falcon_norm_out_bwd(B, H, L, dv, dcode, _b._address(o), _b._address(weight), gp, ldg,
                                          kind, float(scale), float(eps), dp, ldd,
                                          _b._address(res["dO"]), gop, ldgo, _b._address(res["dweight"]),
