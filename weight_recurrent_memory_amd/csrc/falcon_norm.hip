@@ -11,7 +11,10 @@
 //                dO = r (dn - n mean(n dn))
 //
 // All four are bound by HBM: a few operations per element, each element read
-// and written once.  One row (one token of one head, d elements) lies on
+// and written once.  Measured (bf16), where a copy of 1 GiB moves 5.25 TB/s: norm_in
+// 8x2048x12x64 26.1 us = 5.8 TB/s (the last call's rows are partly in the Infinity Cache),
+// norm_in_bwd 4x1999x16x128 60.8 us = 5.9 TB/s, norm_out 8x2048x12x64 with gate and
+// residual 26.0 us = 4.8 TB/s, norm_out_bwd 2x8192x16x128 97 us = 4.8 TB/s.  One row (one token of one head, d elements) lies on
 // d / V lanes, V elements each (one 16-byte access of the element type; float32
 // rows beside bf16 ones take two), so a row's sums are shuffles inside a lane
 // group.  A workgroup takes a tile of TT consecutive tokens with every head and
@@ -64,6 +67,30 @@ struct Vec<float> {
     *reinterpret_cast<float4*>(p) = float4{x[0], x[1], x[2], x[3]};
   }
 };
+
+// The same stored past the caches, and V float32 values read past them, for
+// norm_in_bwd, whose inputs have their last use there (4x1999x16x128: 60.8 us against 70.5;
+// a block's forward and backward at 8x12x2048x64: 322 us against 328).  The other outputs
+// are the next kernel's inputs: past the caches they cost it more than they save here.
+template <typename T, int V>
+__device__ __forceinline__ void store_once(T* p, const float (&x)[V]) {
+  if constexpr (sizeof(T) == 4) {
+    __builtin_nontemporal_store(floatx4{x[0], x[1], x[2], x[3]}, reinterpret_cast<floatx4*>(p));
+  } else {
+    typedef unsigned int uintx4 __attribute__((ext_vector_type(4)));
+    __builtin_nontemporal_store(uintx4{pack_bf16x2(x[0], x[1]), pack_bf16x2(x[2], x[3]),
+                                       pack_bf16x2(x[4], x[5]), pack_bf16x2(x[6], x[7])},
+                                reinterpret_cast<uintx4*>(p));
+  }
+}
+template <int V>
+__device__ __forceinline__ void load_once(const float* p, float (&x)[V]) {
+#pragma unroll
+  for (int i = 0; i < V; i += 4) {
+    const floatx4 u = __builtin_nontemporal_load(reinterpret_cast<const floatx4*>(p + i));
+    x[i] = u.x; x[i + 1] = u.y; x[i + 2] = u.z; x[i + 3] = u.w;
+  }
+}
 
 // V float32 values (16-byte aligned).
 template <int V>
@@ -157,7 +184,7 @@ __device__ __forceinline__ void norm_in_bwd_rows(const T* x, long ldx, const flo
 #pragma unroll
     for (int i = 0; i < V; ++i) f[i] = g[i] = 0.0f;
     if (w.in) {
-      load_f32<V>(dy + w.head * D + c, g);
+      load_once<V>(dy + w.head * D + c, g);
       if (NORM) Vec<T>::load(x + w.tok * ldx + (long)w.h * D + c, f);
     }
     if (NORM) {
@@ -176,7 +203,7 @@ __device__ __forceinline__ void norm_in_bwd_rows(const T* x, long ldx, const flo
 #pragma unroll
       for (int i = 0; i < V; ++i) g[i] = rs * (g[i] - f[i] * dot);
     }
-    if (w.in) Vec<T>::store(dx + w.tok * ld + (long)w.h * D + c, g);
+    if (w.in) store_once<T, V>(dx + w.tok * ld + (long)w.h * D + c, g);
   }
 }
 
@@ -332,11 +359,12 @@ __global__ __launch_bounds__(1024) void norm_out_dweight_kernel(const float* par
 
 // Tokens of a tile.  norm_in with 8 against 16: 26.1 against 27.1 us (8x2048x12x64 bf16),
 // its gradient 68 against 71 us (4x1999x16x128); norm_out with 16 against 8 and 32: 26.7
-// against 26.8 and 28.5 us (8x2048x12x64 with gate and residual).  Calls of few tokens
-// take 4, for more workgroups.
-constexpr int kTileIn = 8, kTileOut = 16, kTileFew = 4;
+// against 26.8 and 28.5 us (8x2048x12x64 with gate and residual), its gradient with 8 and
+// 2048 workgroups against 16 and 1024: 100 against 105 us (2x8192x16x128).  Calls of few
+// tokens take 4, for more workgroups.
+constexpr int kTileIn = 8, kTileOut = 16, kTileOutBwd = 8, kTileFew = 4;
 constexpr long kFewTokens = 4096;
-constexpr int kBwdGroups = 1024;  // workgroups of norm_out_bwd at most
+constexpr int kBwdGroups = 2048;  // workgroups of norm_out_bwd at most
 
 int tile_of(long N, int tile) { return N < kFewTokens ? kTileFew : tile; }
 long tiles_of(long N, int tile) { return (N + tile_of(N, tile) - 1) / tile_of(N, tile); }
@@ -421,13 +449,13 @@ hipError_t launch_norm_out(const NormOutArgs& a, hipStream_t stream) {
 }
 
 size_t norm_out_bwd_workspace_bytes(int batch, int seqlen, int dv) {
-  const long tiles = tiles_of((long)batch * seqlen, kTileOut);
+  const long tiles = tiles_of((long)batch * seqlen, kTileOutBwd);
   return (size_t)(tiles < kBwdGroups ? tiles : kBwdGroups) * dv * sizeof(float);
 }
 
 hipError_t launch_norm_out_bwd(const NormOutBwdArgs& a, hipStream_t stream) {
   (void)hipGetLastError();
-  const long N = (long)a.batch * a.seqlen, tiles = tiles_of(N, kTileOut);
+  const long N = (long)a.batch * a.seqlen, tiles = tiles_of(N, kTileOutBwd);
   const int groups = (int)(tiles < kBwdGroups ? tiles : kBwdGroups);
   const hipError_t e = with_type(a.dtype, [&](auto t) {
     using T = decltype(t);
@@ -439,7 +467,7 @@ hipError_t launch_norm_out_bwd(const NormOutBwdArgs& a, hipStream_t stream) {
           hipLaunchKernelGGL((norm_out_bwd_kernel<T, d(), tile(), false>), dim3(groups), dim3(NT), 0, stream, a, tiles);
         return hipGetLastError();
       };
-      return tile_of(N, kTileOut) == kTileOut ? go(std::integral_constant<int, kTileOut>())
+      return tile_of(N, kTileOutBwd) == kTileOutBwd ? go(std::integral_constant<int, kTileOutBwd>())
                                  : go(std::integral_constant<int, kTileFew>());
     });
   });
