@@ -12,6 +12,14 @@
 //   dlog_a_t = X + sum_{t'>=t} r_t' - sum_{s>=t} c_s,   X = <R, S> at the segment's end,
 // summed in float64.  Segments are 16 chunks at most, so that an X is never far away; at
 // a reset the sum is 0 and begins anew, so that nothing of one document is left in another.
+//
+// Four launches: both directions' segment writes, their recurrences, the three gradients,
+// the gates.  8x12x2048x64 bf16: 28 + 13 + 108 + 7 us (143 us a call, the kernels partly
+// overlapping); the gradients move 422 MB over the fabric (inputs read by the dk and dv
+// part and again by the dq part, 3.9 TB/s) and issue 540 vector and 86 matrix
+// instructions a chunk and wave on two waves a SIMD: bound by both.  Tried: three parts in
+// place of two (157 us), blocks of 32 columns (180 us), segments of two chunks for this
+// shape (179 us), each part a launch of its own (188 us).
 #include "falcon_gated_chunk.h"
 
 namespace falcon {

@@ -19,6 +19,18 @@
 // these are the 8 k-slots the next product (Z^T P^T) wants, so decays, mask and split
 // happen in registers.  A chunk's x, z and U lie in LDS by rows; products over
 // tokens read x and z transposed; the next chunk's rows are loaded while this one is computed.
+//
+// Bounds.  Forward at 64 columns (8x12x2048, bf16, 768 workgroups): 27.8 us, 142 MB over
+// the fabric = 5.1 TB/s, a large copy's rate; per chunk and wave about 490 vector and 72
+// matrix instructions.  At 128 columns (1x4x32771): 61 us of issue, two workgroups on a
+// compute unit (72 KB of LDS, 246 registers); blocks of 32 z rows in place of 64 make it
+// 103 us a call against 92, the scores being formed twice as often.
+// What the layout is for: rows as they come from memory and ds_read_b64_tr_b16 for the
+// products over tokens, in place of a second, transposed copy: 40 KB in place of 57 at 64
+// columns, three workgroups on a compute unit in place of two (a call 63 -> 56 us); reads
+// through buffers that end with the sequence, in place of bounds arithmetic (56 -> 53 us at
+// 64 columns, 120 -> 103 at 128).  Tried without gain: two chunks ahead in state_kernel;
+// the recurrence over segments inside chunk_kernel's first steps (58 us against 54.6).
 #pragma once
 #include <type_traits>
 
@@ -267,13 +279,11 @@ __device__ __forceinline__ floatx4 values4(const uint16_t* p, int stride) {
   return x;
 }
 
-// Workgroups on a compute unit that the registers are held to: three with bf16 operands
-// up to 64 columns, two up to 64 columns and at 128 with bf16 operands, else one.
-template <typename TX, typename TY, typename TZ, int DX>
-constexpr int groups() {
-  constexpr int n = planes<TX>() + planes<TY>() + planes<TZ>();
-  return n == 3 && DX <= 64 ? 3 : n < 9 || DX <= 64 ? 2 : 1;
-}
+// Workgroups on a compute unit that chunk_kernel's registers are held to: with bf16
+// operands three up to 64 columns and two at 128, with float32 two and one.  (Three at 128
+// columns or two there with float32 spill a hundred registers and more.)
+template <typename T, int DX>
+constexpr int held() { return planes<T>() == 1 ? (DX <= 64 ? 3 : 2) : (DX <= 64 ? 2 : 1); }
 
 // GRAD: U is kept transposed in memory ([x][z], a state's own layout for dq and dk), and
 // dots are written.
@@ -437,7 +447,7 @@ __device__ __forceinline__ void chunk_body(const ChunkArgs& a, const Span& sp, i
   if (a.U_out && step == sp.segs - 1) st.store(a.U_out + chain * state + U_blk, U_sz, U_sx);
 }
 template <typename TX, typename TY, typename TZ, int DX, int DZ, bool REV, bool GRAD>
-__global__ __launch_bounds__(NT, (groups<TX, TY, TZ, DX>())) void chunk_kernel(ChunkArgs a, Span sp) {
+__global__ __launch_bounds__(NT, (held<TX, DX>())) void chunk_kernel(ChunkArgs a, Span sp) {
   extern __shared__ __align__(16) unsigned char smem[];
   int blk;
   long unit;
