@@ -443,7 +443,8 @@ int falcon_norm_out_bwd(int batch, int heads, int seqlen, int dv, int dtype, con
  * per (batch, head, token) in place of the decay 1 - eta lambda, and the same
  * step's key:
  *   S_t = a_t S_{t-1} + v_t k_t^T,   a_t = exp(log_a_t),   o_t = S_t q_t
- *   log_a    [batch, heads, L] float32, or NULL (a = 1).  A log decay below
+ *   log_a    [batch, heads, L] float32 (4-byte aligned, the other pointers 16), or
+ *            NULL (a = 1).  A log decay below
  *            -1000 counts as -1000 (e^-1000 is 0 in float32), so -inf resets the
  *            state: a new sequence starts at that token.
  *

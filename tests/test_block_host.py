@@ -107,7 +107,7 @@ def test_norm_out_bwd_workspace(lib):
 
 @pytest.mark.parametrize("over,status", SIZES + [
     (dict(nseq=0), INVALID), (dict(dk=24), UNSUPPORTED), (dict(S=None), INVALID),
-    (dict(o=None), INVALID), (dict(q=P[1] + 2), INVALID), (dict(log_a=P[4] + 4), INVALID),
+    (dict(o=None), INVALID), (dict(q=P[1] + 2), INVALID), (dict(log_a=P[4] + 2), INVALID),
     (dict(o=P[0] + 64), INVALID), (dict(o=P[4]), INVALID), (dict(S=P[2]), INVALID),
     (dict(nseq=1 << 18, heads=16, S=1 << 44, q=1 << 40, k=2 << 40, v=3 << 40, log_a=4 << 40,
           o=5 << 40), UNSUPPORTED),
@@ -133,6 +133,12 @@ def test_binding_refuses_host_tensors_and_odd_layouts():
                 ok[:, :, :1].expand(2, 5, 3, 16), ok[:1].expand(2, 5, 3, 16)):
         with pytest.raises(ValueError):
             rows(torch, "x", bad, tuple(bad.shape), torch.float32, bad.device)
+    # a projection with one more column a head behind it: rows 3 elements off 16 bytes
+    odd = torch.zeros(2, 5, 99)[..., :48].view(2, 5, 3, 16)
+    shifted = torch.zeros(2 * 5 * 48 + 1)[1:].view(2, 5, 3, 16)
+    for bad in (odd, shifted):
+        with pytest.raises(ValueError, match="16"):
+            rows(torch, "x", bad, (2, 5, 3, 16), torch.float32, bad.device)
     with pytest.raises(ValueError):
         fw.norms._gate_kind("relu")
 
@@ -147,7 +153,7 @@ BWD = dict(batch=2, heads=3, seqlen=8, dk=64, dv=64, dtype=0, q=P[0], k=P[1], v=
 @pytest.mark.parametrize("over,status", SIZES + [
     (dict(batch=0), INVALID), (dict(seqlen=0), INVALID), (dict(batch=1 << 16, seqlen=1 << 15), INVALID),
     (dict(dk=24), UNSUPPORTED), (dict(q=None), INVALID), (dict(o=None), INVALID),
-    (dict(k=P[1] + 8), INVALID), (dict(log_a=P[3] + 4), INVALID), (dict(ws=P[7] + 8), INVALID),
+    (dict(k=P[1] + 8), INVALID), (dict(log_a=P[3] + 2), INVALID), (dict(ws=P[7] + 8), INVALID),
     (dict(o=P[0]), INVALID), (dict(o=P[3]), INVALID), (dict(S_out=P[2]), INVALID),
     (dict(S_out=P[4] + 64), INVALID),                # the start's state only exactly in place
     (dict(o=P[4]), INVALID), (dict(S_out=P[5]), INVALID),
@@ -164,7 +170,7 @@ def test_gated_fwd_chunk(lib, over, status):
     (dict(dO=None), INVALID), (dict(dq=None), INVALID), (dict(ws=None), INVALID),
     (dict(wsb=100), INVALID), (dict(ws=P[12] + 8), INVALID), (dict(log_a=None), INVALID),
     (dict(dO=P[5] + 4), INVALID), (dict(dq=P[0]), INVALID), (dict(dk_=P[7]), INVALID),
-    (dict(dS0=P[4]), INVALID), (dict(dS0=P[6]), INVALID), (dict(dlog_a=P[3]), INVALID),
+    (dict(dS0=P[4]), INVALID), (dict(dS0=P[6]), INVALID), (dict(dlog_a=P[10] + 2), INVALID), (dict(dlog_a=P[3]), INVALID),
     (dict(ws=P[9] + 64), INVALID),
     (dict(heads=512, batch=64, seqlen=1 << 17, q=1 << 45, k=2 << 45, v=3 << 45, log_a=4 << 45,
           S0=5 << 45, dO=6 << 45, dS_L=7 << 45, dq=8 << 45, dk_=9 << 45, dv_=10 << 45,

@@ -247,6 +247,26 @@ def test_captured_with_large_lds(dtype, d):
         assert all(torch.equal(a, b) for a, b in zip(outs, want[rep])), rep
 
 
+def test_log_decays_of_any_alignment():
+    """A step's log decays as a slice of all steps' (4-byte aligned), three heads."""
+    x = _inputs(46, 1, 3, 70, 32, 16, torch.bfloat16)
+    buf = torch.zeros(3 * 70 + 8, device="cuda")
+    dO = _up(np.random.default_rng(47).standard_normal((1, 3, 70, 16)))
+    run = lambda la: [fw.gated_fwd_chunk(x["q"], x["k"], x["v"], la, S0=x["S0"])] + list(  # noqa: E731
+        fw.gated_bwd_chunk(x["q"], x["k"], x["v"], la, dO).values())
+    want = run(x["log_a"])
+    for at in (1, 2, 3):
+        la = buf[at:at + 210].view(1, 3, 70)
+        la.copy_(x["log_a"])
+        assert all(torch.equal(a, b) for a, b in zip(run(la), want))
+    steps = -torch.rand(4, 1, 3, device="cuda")
+    for t in range(4):
+        S, S2 = x["S0"].clone(), x["S0"].clone()
+        one = [x[n][:, :, t].contiguous() for n in ("q", "k", "v")]
+        o = fw.gated_decode_step(S, *one, steps[t])
+        assert torch.equal(o, fw.gated_decode_step(S2, *one, steps[t].clone())) and torch.equal(S, S2)
+
+
 def test_growing_state():
     """log_a > 0: gates above one, the state grows by e^(0.05 L)."""
     x = _inputs(43, 1, 2, 200, 32, 64, torch.bfloat16)
@@ -301,3 +321,27 @@ def test_backward_against_differences():
             return np.sum(o * _np(dO)) + np.sum(S * _np(dS))
         want, have = (f(1e-5) - f(-1e-5)) / 2e-5, np.sum(_np(d[n]) * u)
         assert abs(want - have) <= 1e-6 + 1e-5 * np.sum(np.abs(_np(d[n]) * u)), n
+
+
+@pytest.mark.parametrize("seed", range(60))
+def test_random_configurations(seed):
+    """Sizes, types, gates and starts drawn at random: every block size, cut and whole
+    sequences, forward, gradients and a decode step behind the sequence."""
+    r = np.random.default_rng(1000 + seed)
+    dk, dv = (int(r.choice([16, 32, 64, 128])) for _ in range(2))
+    L = int(np.exp(r.uniform(0, np.log(1500))))
+    B, H = int(r.integers(1, 4)), int(r.integers(1, 7))
+    if L * B * H * max(dk, dv) > 400_000:
+        B, H = 1, min(H, 2)
+    dtype = TYPES[int(r.integers(2))]
+    x = _inputs(seed, B, H, L, dk, dv, dtype, gate=str(r.choice(["mixed", "strong", "resets", "none"])),
+                start=bool(r.integers(2)))
+    _, S = _check_forward(x)
+    _check_backward(x, seed + 500, end=bool(r.integers(2)))
+    q, k, v = (x[n][:, :, -1].contiguous() for n in ("q", "k", "v"))
+    la = None if x["log_a"] is None else x["log_a"][:, :, -1].contiguous()
+    one = fw.gated_fwd_chunk(*(t[:, :, None] for t in (q, k, v)), None if la is None else la[:, :, None],
+                             S0=S, return_state=True)
+    o = fw.gated_decode_step(S, q, k, v, la)
+    for a, b in ((o, one[0][:, :, 0]), (S, one[1])):
+        assert float((a - b).norm()) <= 1e-6 * float(b.norm()) + 1e-30

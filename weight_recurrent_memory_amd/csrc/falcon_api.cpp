@@ -619,6 +619,9 @@ bool all_aligned16(const void* const (&ptrs)[N]) {
   return true;
 }
 
+// Log decays are read and written one by one.
+bool aligned4(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 3u) == 0; }
+
 }  // namespace
 
 FALCON_EXPORT int falcon_norm_in(int batch, int heads, int seqlen, int dk, int dv, int dtype,
@@ -757,8 +760,8 @@ FALCON_EXPORT int falcon_gated_decode_step(int nseq, int heads, int dk, int dv, 
   int st = check_sizes(nseq, heads, 1, dk, dv, dtype, &N, &es);
   if (st != FALCON_OK) return st;
   if (!S || !q || !k || !v || !o) return FALCON_ERR_INVALID_ARG;
-  const void* ptrs[] = {S, q, k, v, log_a, o};
-  if (!all_aligned16(ptrs)) return FALCON_ERR_INVALID_ARG;
+  const void* ptrs[] = {S, q, k, v, o};
+  if (!all_aligned16(ptrs) || !aligned4(log_a)) return FALCON_ERR_INVALID_ARG;
   const size_t NH = N * heads;
   const Range outs[] = {{S, NH * dv * dk * 4}, {o, NH * dv * 4}};
   const Range ins[] = {{q, NH * dk * es}, {k, NH * dk * es}, {v, NH * dv * es}, {log_a, NH * 4}};
@@ -798,8 +801,8 @@ FALCON_EXPORT int falcon_gated_fwd_chunk(int batch, int heads, int seqlen, int d
   int st = check_sizes(batch, heads, seqlen, dk, dv, dtype, &N, &es);
   if (st != FALCON_OK) return st;
   if (!q || !k || !v || !o) return FALCON_ERR_INVALID_ARG;
-  const void* ptrs[] = {q, k, v, log_a, S0, o, S_out, workspace};
-  if (!all_aligned16(ptrs)) return FALCON_ERR_INVALID_ARG;
+  const void* ptrs[] = {q, k, v, S0, o, S_out, workspace};
+  if (!all_aligned16(ptrs) || !aligned4(log_a)) return FALCON_ERR_INVALID_ARG;
   if (!supported_dim(dk) || !supported_dim(dv)) return FALCON_ERR_UNSUPPORTED;
   if (!gated_chains(batch, heads, dv)) return FALCON_ERR_UNSUPPORTED;
   const size_t NH = N * heads, state = (size_t)batch * heads * dv * dk * 4;
@@ -854,8 +857,8 @@ FALCON_EXPORT int falcon_gated_bwd_chunk(int batch, int heads, int seqlen, int d
   if (st != FALCON_OK) return st;
   if (!q || !k || !v || !dO || !dq || !dk_out || !dv_out || !workspace || (dlog_a && !log_a))
     return FALCON_ERR_INVALID_ARG;
-  const void* ptrs[] = {q, k, v, log_a, S0, dO, dS_L, dq, dk_out, dv_out, dlog_a, dS0, workspace};
-  if (!all_aligned16(ptrs)) return FALCON_ERR_INVALID_ARG;
+  const void* ptrs[] = {q, k, v, S0, dO, dS_L, dq, dk_out, dv_out, dS0, workspace};
+  if (!all_aligned16(ptrs) || !aligned4(log_a) || !aligned4(dlog_a)) return FALCON_ERR_INVALID_ARG;
   if (!supported_dim(dk) || !supported_dim(dv)) return FALCON_ERR_UNSUPPORTED;
   if (!gated_bwd_sizes(batch, heads, seqlen, dk, dv)) return FALCON_ERR_UNSUPPORTED;
   const size_t need = gated_bwd_need(batch, heads, seqlen, dk, dv, dtype);

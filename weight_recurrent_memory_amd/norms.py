@@ -28,7 +28,11 @@ def _rows(torch, name, t, shape, dtype, device):
     if s3 != 1 or (H > 1 and s2 != d) or ld < H * d or (B > 1 and s0 != L * ld):
         raise ValueError("%s: strides %s of %s are not rows of %d elements at one distance"
                          % (name, t.stride(), shape, H * d))
-    return t.data_ptr(), ld
+    at = t.data_ptr()
+    if at % 16 or ld * t.element_size() % 16:
+        raise ValueError("%s: rows must start 16-byte aligned and lie a multiple of 16 bytes "
+                         "apart (%d elements of %s)" % (name, ld, dtype))
+    return at, ld
 
 
 def _token_major(torch, name, t):
