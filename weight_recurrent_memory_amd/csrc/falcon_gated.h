@@ -293,9 +293,9 @@ struct Span {
 // which is what is aimed at; most: chunks of a segment at most; whole: sequences of fewer
 // chunks are not cut (the extra launches would cost more).  Segments have two chunks at
 // least.  Measured, us: 1x4x32771x128 forward 92 with 512 workgroups (what the GPU holds
-// of that kernel) against 104 with 768; 1x8xLx64 forward cut and whole: L 320 21 and 15,
-// L 512 21 and 22, L 1024 21 and 40; backward 1x8x256x64 29 and 27, 2x8x512x64 31 and 41;
-// two chunks against four: backward 1x5x4099x128x64 84 and 108.
+// of that kernel) against 104 with 768; forward cut and whole, 1x8xLx64: L 512 20.5 and
+// 15, L 768 21.5 and 21, L 1000 21.5 and 27, 8x12x512x64 27.5 and 20.5; two chunks against
+// four: backward 1x5x4099x128x64 84 and 108.
 inline Span cut(long units, long seqlen, long slots, long most, long whole) {
   const long chunks = (seqlen + C - 1) / C;
   long n = units < slots && chunks >= whole ? slots / units : 1;

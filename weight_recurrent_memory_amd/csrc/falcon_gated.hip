@@ -61,7 +61,7 @@ namespace {
 
 // One workgroup's walk takes any number of chunks.  256 compute units hold two or three
 // workgroups of the chunk kernel each, one with float32 inputs at 128 columns.
-constexpr long kWhole = 8;
+constexpr long kWhole = 13;
 int block_of(const GatedArgs& a) { return rows_of(a.dv, (long)a.batch * a.heads, a.seqlen, kWhole); }
 Span cut_of(const GatedArgs& a) {
   const long blocks = a.dv / block_of(a);

@@ -27,7 +27,10 @@ namespace gated {
 namespace {
 
 constexpr int kMostChunks = 16;            // of a segment: 1024 tokens
-constexpr long kWhole = 5;                 // chunks from which a sequence is cut
+// Chunks from which a sequence is cut: where few workgroups would walk it whole (us cut and
+// whole: 1x8x512x64 29 and 48), at 128 columns (1x3x320x128: 37 and 28), and where 192
+// and more do (8x12x512x64 58 and 49, 2x8x512x128 52 and 43).
+constexpr long kWholeFew = 5, kWholeWide = 8, kWholeMany = 13, kMany = 192;
 
 struct GateArgs {
   const float* log_a;
@@ -486,18 +489,25 @@ Plan plan_of(const GatedBwdArgs& a) {
   p.chains = (long)a.batch * a.heads;
   p.state = (long)a.ndv * a.ndk;
   // up to 64 columns dk and dv are one workgroup's
-  p.block = 0;
-  if (a.ndk > 64 || a.ndv > 64) {
-    // bf16 with dk >= 64: 32 columns leave room for two workgroups on a compute unit, 64
-    // for one (4x16x2048x128: 318 us against 354, 8x16x1024x128x64: 164 against 212); with
-    // dk 16 and 32 there is room for two of 64 (8x16x1024x16x128: 110 against 130 us of
-    // 32), with float32 inputs for one of either (2x16x2048x128: 310 against 366 us)
-    const int most = a.dtype == 0 && a.ndk >= 64 ? 32 : 64;
-    p.block = rows_of(128, p.chains, a.seqlen, kWhole);
-    if (p.block > most) p.block = most;
+  const bool is_wide = a.ndk > 64 || a.ndv > 64;
+  // bf16 with dk >= 64: 32 columns leave room for two workgroups on a compute unit, 64 for
+  // one (4x16x2048x128: 318 us against 354, 8x16x1024x128x64: 164 against 212); with dk 16
+  // and 32 there is room for two of 64 (8x16x1024x16x128: 110 against 130 us of 32), with
+  // float32 inputs for one of either (2x16x2048x128: 310 against 366 us)
+  const int most = a.dtype == 0 && a.ndk >= 64 ? 32 : 64;
+  auto block_for = [&](long whole) {
+    const int rows = rows_of(128, p.chains, a.seqlen, whole);
+    return rows < most ? rows : most;
+  };
+  long whole = is_wide ? kWholeWide : kWholeFew, walks = 2 * p.chains;
+  if (is_wide) {
+    const int b = block_for(1l << 40);
+    walks = p.chains * (2 * ((a.ndk + b - 1) / b) + (a.ndv + b - 1) / b);
   }
+  if (walks >= kMany) whole = kWholeMany;
+  p.block = is_wide ? block_for(whole) : 0;
   p.blocks = p.block && p.block < a.ndk ? a.ndk / p.block : 1;
-  p.s = cut(p.chains * p.blocks, a.seqlen, 512, kMostChunks, kWhole);
+  p.s = cut(p.chains * p.blocks, a.seqlen, 512, kMostChunks, whole);
   p.r = p.s;
   // the end's state only where its gradient meets it
   p.s.writes = a.dS_L && a.dlog_a ? p.s.segs : p.s.segs - 1;
