@@ -217,9 +217,10 @@ def test_backward_in_segments(dtype, dk, dv, L):
     assert all(torch.equal(got[n], again[n]) for n in got)
 
 
-def test_backward_of_many_chains():
-    """Segments of 1024 tokens whatever the number of chains."""
-    _check_backward(_inputs(25, 30, 40, 1100, 16, 16, torch.bfloat16, gate="resets"), 26)
+@pytest.mark.parametrize("L", [900, 1100])
+def test_backward_of_many_chains(L):
+    """Segments of 1024 tokens at most, whatever the number of chains: one and two."""
+    _check_backward(_inputs(25, 30, 40, L, 16, 16, torch.bfloat16, gate="resets"), 26)
 
 
 @pytest.mark.parametrize("dtype,d", [(torch.bfloat16, 128), (torch.float32, 64), (torch.float32, 128)])

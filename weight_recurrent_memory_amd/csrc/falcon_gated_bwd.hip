@@ -28,9 +28,10 @@ namespace {
 
 constexpr int kMostChunks = 16;            // of a segment: 1024 tokens
 // Chunks from which a sequence is cut: where few workgroups would walk it whole (us cut and
-// whole: 1x8x512x64 29 and 48), at 128 columns (1x3x320x128: 37 and 28), and where 192
-// and more do (8x12x512x64 58 and 49, 2x8x512x128 52 and 43).
-constexpr long kWholeFew = 5, kWholeWide = 8, kWholeMany = 13, kMany = 192;
+// whole: 1x8x512x64 29 and 48), at 128 columns (1x3x320x128: 37 and 28), where 192 do
+// (8x12x512x64 58 and 49, 2x8x512x128 52 and 43) and where 320 do (16x12x1000x64: 142 and
+// 107; a whole segment's chunks).
+constexpr long kWholeFew = 5, kWholeWide = 8, kWholeMany = 13, kMany = 192, kMost = 320;
 
 struct GateArgs {
   const float* log_a;
@@ -504,7 +505,7 @@ Plan plan_of(const GatedBwdArgs& a) {
     const int b = block_for(1l << 40);
     walks = p.chains * (2 * ((a.ndk + b - 1) / b) + (a.ndv + b - 1) / b);
   }
-  if (walks >= kMany) whole = kWholeMany;
+  if (walks >= kMany) whole = walks >= kMost ? kMostChunks + 1 : kWholeMany;
   p.block = is_wide ? block_for(whole) : 0;
   p.blocks = p.block && p.block < a.ndk ? a.ndk / p.block : 1;
   p.s = cut(p.chains * p.blocks, a.seqlen, 512, kMostChunks, whole);
