@@ -1,0 +1,102 @@
+"""norm_in, norm_out and their gradients where they can go wrong: eps = 0, workgroups that
+walk several tiles, gates far from zero, rows that are not finite.
+
+Tolerances as derived in test_gpu_norms.py: u = 2^-24, h = half a step of the output type.
+"""
+import numpy as np
+import pytest
+
+from oracle import block_oracle as bo
+
+pytestmark = pytest.mark.gpu
+
+torch = pytest.importorskip("torch")
+import weight_recurrent_memory_amd as fw  # noqa: E402
+
+U = 2.0 ** -24
+HALF = {torch.bfloat16: 2.0 ** -8, torch.float32: U}
+TYPES = [torch.bfloat16, torch.float32]
+
+
+@pytest.fixture(scope="module", autouse=True)
+def _gpu():
+    if not torch.cuda.is_available():
+        pytest.skip("no GPU")
+    fw.load_library()
+
+
+def _np(t):
+    return t.detach().double().cpu().numpy()
+
+
+def _rand(seed, *shape, dtype=torch.float32, std=1.0):
+    r = np.random.default_rng(seed)
+    return torch.from_numpy((std * r.standard_normal(shape)).astype(np.float32)).cuda().to(dtype)
+
+
+def _meets(got, ref, tol):
+    got, tol = _np(got), np.broadcast_to(tol, np.shape(ref))
+    assert got.shape == np.shape(ref)
+    bad = ~(np.abs(got - ref) <= tol)
+    assert not bad.any(), "%d off, worst %g times the tolerance" % (
+        bad.sum(), np.nanmax(np.abs(got - ref)[bad] / np.maximum(tol[bad], 1e-300)))
+
+
+def _heads_first(x):
+    return np.swapaxes(x, 1, 2)
+
+
+def _check_norm_out_bwd(o, w, dy, gate, kind, eps, adds=256):
+    """adds: additions that a term of dweight passes."""
+    dv, dtype = o.shape[-1], dy.dtype
+    d = fw.norm_out_bwd(o, w, dy, gate, gate_kind=kind or "silu", scale=0.5, eps=eps)
+    ref = bo.norm_out_backward(_np(o), _np(w), _np(dy), None if gate is None else _np(gate),
+                               kind or "silu", 0.5, eps)
+    on = _heads_first(_np(o))
+    r = 1 / np.sqrt(np.mean(on * on, -1, keepdims=True) + eps)
+    n, dz = np.abs(r * on), np.abs(0.5 * _np(dy))
+    if gate is not None:
+        g = _np(gate)
+        sg = bo.activation("sigmoid", g)[0]
+        slope = sg * (1 + np.abs(g)) if kind == "silu" else sg
+        _meets(d["dgate"], ref["dgate"], HALF[dtype] * np.abs(ref["dgate"])
+               + (dv / 2 + 32) * U * dz * np.abs(_np(w)) * n * slope)
+        dz = dz * np.abs(bo.activation(kind, g)[0])
+    _meets(d["dweight"], ref["dweight"], (adds + dv / 2 + 32) * U * np.sum(dz * n, axis=(0, 1, 2)))
+    dn = dz * np.abs(_np(w))
+    size = r * (dn + n * np.mean(n * dn, -1, keepdims=True))
+    _meets(d["dO"], ref["dO"], _heads_first((3 * dv + 64) * U * size))
+
+
+# tokens and heads that do not fill a tile or a workgroup's lane groups, and one that does
+EPS0 = [(512, 1, 12, 64), (2, 17, 12, 16), (1, 1, 1, 128), (1, 4099, 3, 32), (1, 4096, 16, 64)]
+
+
+@pytest.mark.parametrize("dtype", TYPES)
+@pytest.mark.parametrize("B,L,H,d", EPS0)
+@pytest.mark.parametrize("kind", ["silu", "sigmoid", None])
+def test_eps_zero_norm_out_bwd(B, L, H, d, dtype, kind):
+    o, w, dy = _rand(1, B, H, L, d, std=0.5), 1 + _rand(2, d, std=0.1), _rand(3, B, L, H, d, dtype=dtype)
+    gate = _rand(4, B, L, H, d, dtype=dtype) if kind else None
+    _check_norm_out_bwd(o, w, dy, gate, kind, 0.0)
+
+
+@pytest.mark.parametrize("dtype", TYPES)
+@pytest.mark.parametrize("B,L,H,d", EPS0)
+def test_eps_zero_forward_and_norm_in(B, L, H, d, dtype):
+    x, k = _rand(5, B, L, H, d, dtype=dtype), _rand(6, B, L, H, d, dtype=dtype)
+    q, kk, _ = fw.norm_in(x, k, eps=0.0)
+    for got, y in ((q, x), (kk, k)):
+        ref = bo.unit_rows(_heads_first(_np(y)), 0.0)
+        _meets(got, ref, (HALF[dtype] + (d / 2 + 6) * U) * np.abs(ref))
+    g = _rand(7, B, H, L, d)
+    for got, y in zip(fw.norm_in_bwd(x, k, g, g, eps=0.0), (x, k)):
+        y, gg = _np(y), _heads_first(_np(g))
+        r = 1 / np.sqrt(np.sum(y * y, -1, keepdims=True))
+        ref, n = bo.unit_rows_backward(y, gg, 0.0), np.abs(r * y)
+        size = r * (np.abs(gg) + n * np.sum(n * np.abs(gg), -1, keepdims=True))
+        _meets(got, ref, HALF[dtype] * np.abs(ref) + (3 * d + 24) * U * size)
+    o, w = _rand(8, B, H, L, d, std=0.5), 1 + _rand(9, d, std=0.1)
+    y = fw.norm_out(o, w, x, scale=0.5, eps=0.0)
+    ref = bo.norm_out(_np(o), _np(w), _np(x), "silu", None, 0.5, 0.0)
+    _meets(y, ref, (HALF[dtype] + (d / 2 + 25) * U) * np.abs(ref))

@@ -298,7 +298,8 @@ __global__ __launch_bounds__(NT) void norm_out_bwd_kernel(NormOutBwdArgs a, long
 #pragma unroll
       for (int i = 0; i < V; ++i) s += o[i] * o[i];
       s = group_sum<VPR>(s);
-      const float rs = rsqrtf(s * (1.0f / D) + a.eps);
+      // (a lane group without a row adds 0 to dw also where eps = 0 makes its rsqrt infinite)
+      const float rs = w.in ? rsqrtf(s * (1.0f / D) + a.eps) : 0.0f;
       float dot = 0.0f;
 #pragma unroll
       for (int i = 0; i < V; ++i) {
