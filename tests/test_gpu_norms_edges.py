@@ -100,3 +100,22 @@ def test_eps_zero_forward_and_norm_in(B, L, H, d, dtype):
     y = fw.norm_out(o, w, x, scale=0.5, eps=0.0)
     ref = bo.norm_out(_np(o), _np(w), _np(x), "silu", None, 0.5, 0.0)
     _meets(y, ref, (HALF[dtype] + (d / 2 + 25) * U) * np.abs(ref))
+
+
+@pytest.mark.parametrize("dtype", TYPES)
+@pytest.mark.parametrize("kind", ["silu", "sigmoid"])
+def test_gates_far_from_zero(kind, dtype):
+    """A saturated gate's slope to float32 rounding of itself (a sigmoid's is e^-|g|):
+    16u of s and 1 - s each beside the row's (d / 2 + 6) u; silu's 1 + g (1 - s) has terms
+    of both signs, which count by their sizes."""
+    L, d = 640, 64
+    g = torch.linspace(-80, 80, L * d, device="cuda").view(1, L, 1, d).to(dtype)
+    o, w, dy = _rand(10, 1, 1, L, d), 1 + _rand(11, d, std=0.1), _rand(12, 1, L, 1, d, dtype=dtype)
+    got = fw.norm_out_bwd(o, w, dy, g, gate_kind=kind)["dgate"]
+    on = _heads_first(_np(o))
+    z = _np(dy) * _np(w) * on / np.sqrt(np.mean(on * on, -1, keepdims=True) + 1e-6)
+    e = np.exp(-np.abs(_np(g)))
+    s, rest = np.where(_np(g) >= 0, 1, e) / (1 + e), np.where(_np(g) >= 0, e, 1) / (1 + e)
+    slope = s * rest if kind == "sigmoid" else s * (1 + _np(g) * rest)
+    size = s * rest if kind == "sigmoid" else s * (1 + np.abs(_np(g)) * rest)
+    _meets(got, z * slope, HALF[dtype] * np.abs(z * slope) + (d / 2 + 38) * U * np.abs(z) * size + 2.0 ** -126)

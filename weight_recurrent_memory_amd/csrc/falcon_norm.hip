@@ -221,7 +221,7 @@ __global__ __launch_bounds__(NT) void norm_in_bwd_kernel(NormInBwdArgs a) {
 
 // --------------------------------------------------------------- norm_out
 
-// act(g) and act'(g); s = 1 / (1 + e^-g) goes to 0 and 1 at the ends without a NaN
+// s = 1 / (1 + e^-g) goes to 0 and 1 at the ends without a NaN
 // (e^-g = inf gives 0; g s at g = -inf is kept out by the caller's finite gates).
 __device__ __forceinline__ float sigmoid(float g) { return 1.0f / (1.0f + expf(-g)); }
 
@@ -306,9 +306,11 @@ __global__ __launch_bounds__(NT) void norm_out_bwd_kernel(NormOutBwdArgs a, long
         o[i] *= rs;                         // n
         d[i] *= a.scale;
         if (GATE) {
-          const float sg = sigmoid(g[i]);
+          const float e = expf(-g[i]), sg = 1.0f / (1.0f + e);
+          // 1 - sg: as a difference it keeps ever fewer bits from g = 5 on and is 0 from 17 on
+          const float rest = g[i] > 0.0f ? e * sg : 1.0f - sg;
           const float act = a.gate_kind == 0 ? g[i] * sg : sg;
-          const float slope = a.gate_kind == 0 ? sg * (1.0f + g[i] * (1.0f - sg)) : sg * (1.0f - sg);
+          const float slope = a.gate_kind == 0 ? sg * (1.0f + g[i] * rest) : sg * rest;
           g[i] = d[i] * wv[i] * o[i] * slope;
           d[i] *= act;                      // dz
         }
