@@ -619,6 +619,9 @@ bool all_aligned16(const void* const (&ptrs)[N]) {
   return true;
 }
 
+// Heads of the norms: a workgroup's rows, up to 16 tokens of every head, are counted in 32 bits.
+bool norm_heads(int heads) { return heads < (1 << 27); }
+
 // Log decays are read and written one by one.
 bool aligned4(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 3u) == 0; }
 
@@ -643,7 +646,7 @@ FALCON_EXPORT int falcon_norm_in(int batch, int heads, int seqlen, int dk, int d
   const Range outs[] = {{q, N * heads * dk * es}, {k, N * heads * dk * es}, {v, N * heads * dv * es}};
   const Range ins[] = {hull(rq), hull(rk), hull(rv)};
   if (any_overlap(outs, ins)) return FALCON_ERR_INVALID_ARG;
-  if (!supported_dim(dk) || !supported_dim(dv)) return FALCON_ERR_UNSUPPORTED;
+  if (!supported_dim(dk) || !supported_dim(dv) || !norm_heads(heads)) return FALCON_ERR_UNSUPPORTED;
   const falcon::NormInArgs a{batch, heads, seqlen, dk, dv, dtype, q_in, (long)ld_q, k_in, (long)ld_k,
                              v_in, (long)ld_v, eps, q, k, v};
   return finish_launch(falcon::launch_norm_in(a, (hipStream_t)stream));
@@ -676,7 +679,7 @@ FALCON_EXPORT int falcon_norm_in_bwd(int batch, int heads, int seqlen, int dk, i
     for (const Range& r : ins)
       if (overlap(hull(outs[i]), r)) return FALCON_ERR_INVALID_ARG;
   }
-  if (!supported_dim(dk) || !supported_dim(dv)) return FALCON_ERR_UNSUPPORTED;
+  if (!supported_dim(dk) || !supported_dim(dv) || !norm_heads(heads)) return FALCON_ERR_UNSUPPORTED;
   const falcon::NormInBwdArgs a{batch, heads, seqlen, dk, dv, dtype, q_in, (long)ld_q, k_in,
                                 (long)ld_k, eps, dq, dk_, dv_, dq_in, (long)ld_dq, dk_in,
                                 (long)ld_dk, dv_in, (long)ld_dv};
@@ -707,7 +710,7 @@ FALCON_EXPORT int falcon_norm_out(int batch, int heads, int seqlen, int dv, int 
     return FALCON_ERR_INVALID_ARG;
   // in place: each element of the residual is read before y's is written there
   if (!(residual == y && ld_res == ld_y) && overlap(ry, rr)) return FALCON_ERR_INVALID_ARG;
-  if (!supported_dim(dv)) return FALCON_ERR_UNSUPPORTED;
+  if (!supported_dim(dv) || !norm_heads(heads)) return FALCON_ERR_UNSUPPORTED;
   const falcon::NormOutArgs a{batch, heads, seqlen, dv, dtype, o, weight, gate, (long)ld_gate,
                               gate_kind, residual, (long)ld_res, scale, eps, y, (long)ld_y};
   return finish_launch(falcon::launch_norm_out(a, (hipStream_t)stream));
@@ -739,7 +742,7 @@ FALCON_EXPORT int falcon_norm_out_bwd(int batch, int heads, int seqlen, int dv, 
   if (check_rows(gate, ld_gate, heads, dv, N, es, &rg) || check_rows(dy, ld_dy, heads, dv, N, es, &rd) ||
       check_rows(dgate, ld_dgate, heads, dv, N, es, &og))
     return FALCON_ERR_INVALID_ARG;
-  if (!supported_dim(dv)) return FALCON_ERR_UNSUPPORTED;
+  if (!supported_dim(dv) || !norm_heads(heads)) return FALCON_ERR_UNSUPPORTED;
   const size_t need = falcon::norm_out_bwd_workspace_bytes(batch, seqlen, dv);
   if (workspace_bytes < need) return FALCON_ERR_INVALID_ARG;
   const Range outs[] = {{dO, N * heads * dv * 4}, {dweight, (size_t)dv * 4}, {workspace, need}};
