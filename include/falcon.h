@@ -445,9 +445,9 @@ int falcon_norm_out_bwd(int batch, int heads, int seqlen, int dv, int dtype, con
  * step's key:
  *   S_t = a_t S_{t-1} + v_t k_t^T,   a_t = exp(log_a_t),   o_t = S_t q_t
  *   log_a    [batch, heads, L] float32 (4-byte aligned, the other pointers 16), or
- *            NULL (a = 1).  A log decay below
- *            -1000 counts as -1000 (e^-1000 is 0 in float32), so -inf resets the
- *            state: a new sequence starts at that token.
+ *            NULL (a = 1).  A log decay below -1000 counts as -1000.  A token whose
+ *            decay is 0 in float32 (-inf, and any log decay below about -104) is a
+ *            reset: a new sequence starts at it.
  *
  * falcon_gated_fwd_chunk - a sequence, in chunks of 64 tokens
  *   q, k, v, S0, o, S_out   as falcon_fwd_chunk (S0, S_out may be NULL; S_out may
@@ -470,7 +470,10 @@ int falcon_norm_out_bwd(int batch, int heads, int seqlen, int dv, int dtype, con
  *   dO        [batch, heads, L, dv] float32
  *   dS_L      [batch, heads, dv, dk] float32, or NULL
  *   dq, dk_out, dv_out   [batch, heads, L, dk / dk / dv] float32
- *   dlog_a    [batch, heads, L] float32, or NULL; needs log_a.  0 at a reset.
+ *   dlog_a    [batch, heads, L] float32, or NULL; needs log_a.  0 at a reset, and
+ *             before one nothing of what lies behind it.  A difference of sums: its
+ *             error is float32 rounding of q . dq and k . dk of the tokens from it up
+ *             to the next reset (1024 at most), not of itself
  *   dS0       [batch, heads, dv, dk] float32, or NULL (with S0 NULL: the gradient of
  *             the zero state)
  *   workspace falcon_gated_bwd_workspace_bytes(...) bytes, 16-byte aligned

@@ -258,6 +258,8 @@ __device__ __forceinline__ double wave_scan(double x) {
   return x;
 }
 __device__ __forceinline__ float exp2_of(double x) { return __builtin_amdgcn_exp2f((float)x); }
+// A token whose decay is 0: nothing passes from before it.
+__device__ __forceinline__ bool is_reset(float g) { return exp2_of(log2_decay(g)) == 0.0f; }
 
 // A sum of log2 decays as two floats, and the decay 2^(t - s): the difference of the first
 // parts is exact where they are near each other and else good to 2^-24 of an exponent

@@ -11,7 +11,8 @@
 // leave its rounding behind; then inside a segment
 //   dlog_a_t = X + sum_{t'>=t} r_t' - sum_{s>=t} c_s,   X = <R, S> at the segment's end,
 // summed in float64.  Segments are 16 chunks at most, so that an X is never far away; at
-// a reset the sum is 0 and begins anew, so that nothing of one document is left in another.
+// a reset, any token whose float32 decay is 0, the sum is 0 and begins anew: no product
+// passes it, and the rounding left by one document's sums stays out of another's.
 //
 // Four launches: both directions' segment writes, their recurrences, the three gradients,
 // the gates.  8x12x2048x64 bf16: 28 + 13 + 108 + 7 us (143 us a call, the kernels partly
@@ -86,7 +87,7 @@ __global__ __launch_bounds__(NT) void gate_kernel(GateArgs a, Span s, Span r) {
         rr += a.r[(b * a.chains + chain) * len + t];
         cc += a.c[(b * a.chains + chain) * len + t];
       }
-      reset[j] = a.log_a[chain * len + t] < -1000.0f;
+      reset[j] = is_reset(a.log_a[chain * len + t]);
     }
     mine += rr - cc;
     sum[j] = mine;
