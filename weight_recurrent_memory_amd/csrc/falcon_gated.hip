@@ -96,7 +96,7 @@ hipError_t launch_gated(const GatedArgs& a, void* ws, size_t ws_bytes, hipStream
     float* p = static_cast<float*>(ws);
     gated::place_span(sp, (long)a.batch * a.heads, (long)a.dv * a.dk, p);
   } else {
-    sp = gated::Span{1, (a.seqlen + gated::C - 1) / gated::C, 0, nullptr, nullptr};
+    sp = gated::Span{1, (int)(((long)a.seqlen + gated::C - 1) / gated::C), 0, nullptr, nullptr};
   }
   return a.dtype == 0 ? gated::run<uint16_t>(a, sp, stream) : gated::run<float>(a, sp, stream);
 }
