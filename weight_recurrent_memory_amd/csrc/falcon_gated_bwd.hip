@@ -346,10 +346,8 @@ __device__ __forceinline__ void kv_body(const KVArgs& a, const Span& sp, long un
   if (a.dS0 && step == sp.segs - 1) st.store(a.dS0 + chain * state, DK, 1);
 }
 
-// Both directions' states, and all three gradients, in one launch each: one launch's
-// last workgroups leave no part of the GPU idle.  (Up to 64 columns; at 128
-// the largest of the LDS needs, dk's 104 KB, would hold the others to one workgroup a
-// compute unit.)
+// Up to 64 columns: both directions' states, and all three gradients, in one launch each:
+// one launch's last workgroups leave no part of the GPU idle.
 template <typename T, int DK, int DV>
 __global__ __launch_bounds__(NT) void both_states_kernel(ChunkArgs S, Span s, ChunkArgs R, Span r) {
   extern __shared__ __align__(16) unsigned char smem[];
@@ -474,6 +472,14 @@ hipError_t with_dims(int dk, int dv, F&& f) {
   return hipErrorInvalidValue;
 }
 
+// Columns of a block at most with a size of 128.  bf16 with dk >= 64: 32 columns leave room
+// for two workgroups on a compute unit, 64 for one (4x16x2048x128: 318 us against 354,
+// 8x16x1024x128x64: 164 against 212); with dk 16 and 32 there is room for two of 64
+// (8x16x1024x16x128: 110 against 130 us of 32), with float32 inputs for one of either
+// (2x16x2048x128: 310 against 366 us).
+template <typename T>
+constexpr int most_columns(int dk) { return sizeof(T) == 2 && dk >= 64 ? 32 : 64; }
+
 // The two spans of a call (states first token first, their gradients last token first)
 // and its workspace.
 struct Plan {
@@ -492,11 +498,7 @@ Plan plan_of(const GatedBwdArgs& a) {
   p.state = (long)a.ndv * a.ndk;
   // up to 64 columns dk and dv are one workgroup's
   const bool is_wide = a.ndk > 64 || a.ndv > 64;
-  // bf16 with dk >= 64: 32 columns leave room for two workgroups on a compute unit, 64 for
-  // one (4x16x2048x128: 318 us against 354, 8x16x1024x128x64: 164 against 212); with dk 16
-  // and 32 there is room for two of 64 (8x16x1024x16x128: 110 against 130 us of 32), with
-  // float32 inputs for one of either (2x16x2048x128: 310 against 366 us)
-  const int most = a.dtype == 0 && a.ndk >= 64 ? 32 : 64;
+  const int most = a.dtype == 0 ? most_columns<uint16_t>(a.ndk) : most_columns<float>(a.ndk);
   auto block_for = [&](long whole) {
     const int rows = rows_of(128, p.chains, a.seqlen, whole);
     return rows < most ? rows : most;
@@ -544,8 +546,10 @@ hipError_t run(const GatedBwdArgs& a, Plan p, hipStream_t stream) {
       switch (p.block) {
         case 16: return wide<T, DK, DV, 16>(S, R, dq, dk, dv, p.s, p.r, stream);
         case 32: return wide<T, DK, DV, 32>(S, R, dq, dk, dv, p.s, p.r, stream);
-        default: return wide<T, DK, DV, 64>(S, R, dq, dk, dv, p.s, p.r, stream);
+        case 64:
+          if constexpr (most_columns<T>(DK) == 64) return wide<T, DK, DV, 64>(S, R, dq, dk, dv, p.s, p.r, stream);
       }
+      return hipErrorInvalidValue;
     });
   }
   if (e != hipSuccess || !a.dlog_a) return e;
