@@ -119,3 +119,12 @@ def test_gates_far_from_zero(kind, dtype):
     slope = s * rest if kind == "sigmoid" else s * (1 + _np(g) * rest)
     size = s * rest if kind == "sigmoid" else s * (1 + np.abs(_np(g)) * rest)
     _meets(got, z * slope, HALF[dtype] * np.abs(z * slope) + (d / 2 + 38) * U * np.abs(z) * size + 2.0 ** -126)
+
+
+@pytest.mark.parametrize("B,L,H,d", [(3, 8195, 1, 16), (2, 20001, 2, 64)])
+def test_workgroups_of_several_tiles(B, L, H, d):
+    """dweight over more tiles than norm_out_bwd has workgroups (16384 tokens of 8): a term
+    passes a lane's rows (under 16), 128 lane groups and 2048 workgroups' parts 32 at a time."""
+    o, w = _rand(13, B, H, L, d, std=0.5), 1 + _rand(14, d, std=0.1)
+    dy, gate = _rand(15, B, L, H, d, dtype=torch.bfloat16), _rand(16, B, L, H, d, dtype=torch.bfloat16)
+    _check_norm_out_bwd(o, w, dy, gate, "silu", 1e-6)
