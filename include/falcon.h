@@ -459,10 +459,14 @@ int falcon_norm_out_bwd(int batch, int heads, int seqlen, int dv, int dtype, con
  *             rounding.  A workspace serves one call at a time.
  * Finite inputs (log_a: also -inf) give the recurrence to float32 rounding: products
  * run on bf16 matrix cores with float32 operands in three bf16 parts, decays as
- * differences of float64 sums.  log_a > 0 (growth) is taken as given.  A NaN or an
- * infinity in a token reaches every output of its 64-token chunk, also of earlier
- * tokens: rows of padding have to be finite (whatever they hold, no earlier token
- * reads them).
+ * differences of float64 sums.  log_a > 0 (growth) is taken as given; a growth that
+ * float32 does not hold (log decays that add up to 88 over some stretch) gives
+ * infinities and NaN, also of a state of zeros.  A NaN or an infinity reaches the
+ * outputs that read it, o of its token and of later ones and S_out, and no others:
+ * rows of padding behind a sequence may hold anything.  (A reset does not clear it:
+ * 0 * NaN.  float32 inputs and states beyond bf16's 3.39e38 count as infinite.
+ * The segments that hold one, or start from one, are walked again token by token, at
+ * some hundred times their time.)
  * batch * heads * dv < 2^27 (FALCON_ERR_UNSUPPORTED from there on).
  *
  * falcon_gated_bwd_chunk - gradients of sum <dO, o> + <dS_L, S_L>
@@ -477,6 +481,9 @@ int falcon_norm_out_bwd(int batch, int heads, int seqlen, int dv, int dtype, con
  *   dS0       [batch, heads, dv, dk] float32, or NULL (with S0 NULL: the gradient of
  *             the zero state)
  *   workspace falcon_gated_bwd_workspace_bytes(...) bytes, 16-byte aligned
+ * Here a NaN or an infinity in a token also reaches gradients that do not depend on it:
+ * dq, dk_out and dv_out of its 64-token chunk, and dlog_a of the tokens before it, 1024
+ * at most, not past the last reset.  Rows of padding have to be finite.
  * Outputs and workspace overlap no other argument.  FALCON_ERR_UNSUPPORTED from
  * batch * heads * max(dk, dv) * (L + 1023) / 1024 = 2^26 and from
  * batch * heads * dk * dv = 2^32 on.

@@ -78,7 +78,7 @@ hipError_t run(const GatedArgs& a, const Span& sp, hipStream_t stream) {
   const hipError_t e = launch_states<T, T, false>(c, a.dk, block_of(a), sp, stream);
   if (e != hipSuccess) return e;
   return with_sizes(a.dk, block_of(a), [&](auto d, auto r) {
-    return go_chunk<T, T, T, decltype(d)::value, decltype(r)::value, false, false>(c, sp, stream);
+    return go_chunk<T, decltype(d)::value, decltype(r)::value>(c, sp, stream);
   });
 }
 

@@ -73,6 +73,7 @@ struct LdsState {
   alignas(16) float e[C];
   alignas(16) float w[C];
   float d;
+  alignas(4) unsigned char bad[4];                  // a wave's state is not finite
 };
 template <typename TX, typename TZ, int DX, int DZ>
 struct Lds : LdsState<TX, TZ, DX, DZ> {
@@ -114,6 +115,14 @@ struct State {
         for (int i = 0; i < 4; ++i) p[i * sx] = t[j][i];
       }
     }
+  }
+  // (by a sum: one that overflows counts as an entry that does)
+  __device__ __forceinline__ bool finite() const {
+    float s = 0.0f;
+#pragma unroll
+    for (int j = 0; j < NK; ++j)
+      if (has(j)) s += (t[j].x + t[j].y) + (t[j].z + t[j].w);
+    return __builtin_isfinite(s);
   }
   template <int W>
   __device__ __forceinline__ void to_planes(uint16_t* s, int stride) const {
@@ -286,9 +295,10 @@ template <typename T, int DX>
 constexpr int held() { return planes<T>() == 1 ? (DX <= 64 ? 3 : 2) : (DX <= 64 ? 2 : 1); }
 
 // GRAD: U is kept transposed in memory ([x][z], a state's own layout for dq and dk), and
-// dots are written.
+// dots are written.  Returns true (the forward only), and leaves U_out, where walk_again has
+// to follow.
 template <typename TX, typename TY, typename TZ, int DX, int DZ, bool REV, bool GRAD>
-__device__ __forceinline__ void chunk_body(const ChunkArgs& a, const Span& sp, int blk, long unit,
+__device__ __forceinline__ bool chunk_body(const ChunkArgs& a, const Span& sp, int blk, long unit,
                                            unsigned char* smem) {
   using L = Lds<TX, TZ, DX, DZ>;
   constexpr int NPX = L::NPX, NPY = planes<TY>(), NPZ = L::NPZ;
@@ -444,15 +454,87 @@ __device__ __forceinline__ void chunk_body(const ChunkArgs& a, const Span& sp, i
     }
     st.update(lds);
   }
+  if (!REV && !GRAD) {
+    // a barrier and a sum of the state, once a segment: 0-1.3% of a call (1x4x32771x128 89.9
+    // and 91.2 us, 8x12x2048x64 within noise)
+    const bool bad = __any(!st.finite());
+    if (lane == 0) lds.bad[wave] = bad;
+    __syncthreads();
+    if (__builtin_expect(*reinterpret_cast<const unsigned*>(lds.bad) != 0, 0)) return true;
+  }
   if (a.U_out && step == sp.segs - 1) st.store(a.U_out + chain * state + U_blk, U_sz, U_sx);
+  return false;
 }
-template <typename TX, typename TY, typename TZ, int DX, int DZ, bool REV, bool GRAD>
-__global__ __launch_bounds__(NT, (held<TX, DX>())) void chunk_kernel(ChunkArgs a, Span sp) {
+
+// The forward's outputs that are not finite formed anew, by the recurrence itself, one token
+// at a time.  The products over a chunk's tokens multiply the tokens that a mask leaves out
+// with 0, and 0 * NaN is NaN: a NaN or an infinity in v would reach every output of its chunk,
+// also of earlier tokens.  The walk's state behind it is not finite either, up to the walk's
+// end, which is where it is looked for.  A row of the state lies on 256 / DZ lanes.  About a
+// hundred times a walk's time, and only where inputs, or a state that has overflowed, leave
+// no finite state.
+template <typename T, int DX, int DZ>
+__device__ __forceinline__ void walk_again(const ChunkArgs& a, const Span& sp, int blk, long unit) {
+  constexpr int TPR = NT / DZ, N = DX / TPR;           // 4 to 16 lanes a row, of 1 to 32 columns
+  const long chain = unit / sp.segs, len = a.seqlen, state = (long)a.nz * DX;
+  const int step = (int)(unit % sp.segs);
+  const Walk<false> walk(sp, step, len);
+  const long end = walk.t0 + (long)walk.n * C < len ? walk.t0 + (long)walk.n * C : len;
+  const int row = blk * DZ + (int)threadIdx.x / TPR, c0 = ((int)threadIdx.x % TPR) * N;
+  const long at = (long)row * DX + c0;
+  const T* k = static_cast<const T*>(a.x) + chain * len * DX + c0;
+  const T* q = static_cast<const T*>(a.y) + chain * len * DX + c0;
+  const T* v = static_cast<const T*>(a.z) + chain * len * a.nz + row;
+  const float* la = a.log_a ? a.log_a + chain * len : nullptr;
+  float* out = a.out + chain * len * a.nz + row;
+  const float* S0 = sp.segs > 1 ? sp.states + (chain * (sp.writes + 1) + step) * state
+                                : a.U0 ? a.U0 + chain * state : nullptr;
+  float S[N];
+#pragma unroll
+  for (int j = 0; j < N; ++j) S[j] = S0 ? S0[at + j] : 0.0f;
+  for (long t = walk.t0; t < end; ++t) {
+    const float d = la ? exp2_of(log2_decay(la[t])) : 1.0f, vt = ld_in(v, t * a.nz);
+    float o = 0.0f;
+#pragma unroll
+    for (int j = 0; j < N; ++j) {
+      S[j] = d * S[j] + vt * ld_in(k, t * DX + j);
+      o += S[j] * ld_in(q, t * DX + j);
+    }
+    o = group_sum<TPR>(o);
+    if (c0 == 0 && !__builtin_isfinite(out[t * a.nz])) out[t * a.nz] = o;
+  }
+  if (a.U_out && step == sp.segs - 1) {
+#pragma unroll
+    for (int j = 0; j < N; ++j) a.U_out[chain * state + at + j] = S[j];
+  }
+}
+
+struct ChunkCall {
+  ChunkArgs a;
+  Span sp;
+};
+// The running kernel's arguments read anew: what only a rare path needs is not held in
+// registers up to it (held, it spilled scalar registers: 2-4% of a call).
+__device__ __forceinline__ ChunkCall call_again() {
+  unsigned long at = (unsigned long)__builtin_amdgcn_kernarg_segment_ptr();
+  asm volatile("" : "+s"(at));
+  struct { unsigned w[sizeof(ChunkCall) / 4]; } words;
+#pragma unroll
+  for (unsigned i = 0; i < sizeof(ChunkCall) / 4; ++i)
+    words.w[i] = ((const __attribute__((address_space(4))) unsigned*)at)[i];
+  return __builtin_bit_cast(ChunkCall, words);
+}
+template <typename T, int DX, int DZ>
+__global__ __launch_bounds__(NT, (held<T, DX>())) void chunk_kernel(ChunkCall call) {
   extern __shared__ __align__(16) unsigned char smem[];
   int blk;
   long unit;
-  if (place(a.nz / DZ, a.chains * sp.segs, blk, unit))
-    chunk_body<TX, TY, TZ, DX, DZ, REV, GRAD>(a, sp, blk, unit, smem);
+  if (!place(call.a.nz / DZ, call.a.chains * call.sp.segs, blk, unit)) return;
+  if (chunk_body<T, T, T, DX, DZ, false, false>(call.a, call.sp, blk, unit, smem)) {
+    const ChunkCall c = call_again();
+    place(c.a.nz / DZ, c.a.chains * c.sp.segs, blk, unit);
+    walk_again<T, DX, DZ>(c.a, c.sp, blk, unit);
+  }
 }
 
 // A kernel with more than 64 KB of LDS has to be told so (about a microsecond a call;
@@ -473,13 +555,14 @@ hipError_t go_state(const ChunkArgs& a, const Span& sp, hipStream_t stream) {
   hipLaunchKernelGGL(kernel, dim3(grid_of(a.nz / DZ, a.chains * sp.writes)), dim3(NT), bytes, stream, a, sp);
   return hipGetLastError();
 }
-template <typename TX, typename TY, typename TZ, int DX, int DZ, bool REV, bool GRAD>
+template <typename T, int DX, int DZ>
 hipError_t go_chunk(const ChunkArgs& a, const Span& sp, hipStream_t stream) {
-  constexpr size_t bytes = sizeof(Lds<TX, TZ, DX, DZ>);
-  auto kernel = chunk_kernel<TX, TY, TZ, DX, DZ, REV, GRAD>;
+  constexpr size_t bytes = sizeof(Lds<T, T, DX, DZ>);
+  auto kernel = chunk_kernel<T, DX, DZ>;
   const hipError_t e = lds_limit(kernel, bytes);
   if (e != hipSuccess) return e;
-  hipLaunchKernelGGL(kernel, dim3(grid_of(a.nz / DZ, a.chains * sp.segs)), dim3(NT), bytes, stream, a, sp);
+  hipLaunchKernelGGL(kernel, dim3(grid_of(a.nz / DZ, a.chains * sp.segs)), dim3(NT), bytes, stream,
+                     ChunkCall{a, sp});
   return hipGetLastError();
 }
 
