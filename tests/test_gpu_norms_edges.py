@@ -128,3 +128,39 @@ def test_workgroups_of_several_tiles(B, L, H, d):
     o, w = _rand(13, B, H, L, d, std=0.5), 1 + _rand(14, d, std=0.1)
     dy, gate = _rand(15, B, L, H, d, dtype=torch.bfloat16), _rand(16, B, L, H, d, dtype=torch.bfloat16)
     _check_norm_out_bwd(o, w, dy, gate, "silu", 1e-6)
+
+
+@pytest.mark.parametrize("dtype", TYPES)
+@pytest.mark.parametrize("value", [float("nan"), float("inf")])
+@pytest.mark.parametrize("B,L,H,d", [(2, 17, 12, 16), (1, 4100, 3, 128)])
+def test_a_row_that_is_not_finite_stays_by_itself(B, L, H, d, value, dtype):
+    """Every other row keeps its bits; only dweight, the sum over all rows, has it too."""
+    b, t, h = B - 1, L // 2, H - 1
+    def calls(row):
+        """Outputs and the place of the row in each, for a row of an input set to `value`."""
+        q, k, v = (_rand(20 + i, B, L, H, d, dtype=dtype) for i in range(3))
+        o, w, g = _rand(23, B, H, L, d), 1 + _rand(24, d, std=0.1), _rand(25, B, H, L, d)
+        for n, x in (("q", q), ("v", v)):
+            if row == n:
+                x[b, t, h, 3] = value
+        for n, x in (("o", o), ("g", g)):
+            if row == n:
+                x[b, h, t, 3] = value
+        yield from zip("qkv", fw.norm_in(q, k, v))
+        yield from zip(("dq", "dk", "dv"), fw.norm_in_bwd(q, k, g, g, g))
+        yield "y", fw.norm_out(o, w, q, residual=v)
+        for n, x in fw.norm_out_bwd(o, w, v, q).items():
+            yield n, x
+    clean = {n: x.clone() for n, x in calls(None)}
+    for row in "qvog":
+        touched = 0
+        for n, x in calls(row):
+            if n == "dweight":
+                continue
+            ref = clean[n]
+            head_major = n in ("q", "k", "v", "dO")
+            x, ref = ((y if head_major else y.transpose(1, 2)).clone() for y in (x, ref))
+            touched += not bool(x[b, h, t].isfinite().all())
+            x[b, h, t] = ref[b, h, t] = 0
+            assert torch.equal(x, ref), (row, n)
+        assert touched

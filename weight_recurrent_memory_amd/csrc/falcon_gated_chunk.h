@@ -470,9 +470,9 @@ __device__ __forceinline__ bool chunk_body(const ChunkArgs& a, const Span& sp, i
 // at a time.  The products over a chunk's tokens multiply the tokens that a mask leaves out
 // with 0, and 0 * NaN is NaN: a NaN or an infinity in v would reach every output of its chunk,
 // also of earlier tokens.  The walk's state behind it is not finite either, up to the walk's
-// end, which is where it is looked for.  A row of the state lies on 256 / DZ lanes.  About a
-// hundred times a walk's time, and only where inputs, or a state that has overflowed, leave
-// no finite state.
+// end, which is where it is looked for.  A row of the state lies on 256 / DZ lanes.  Only where
+// inputs, or a state that has overflowed, leave no finite state: a call with a NaN in every
+// chain takes 396 us in place of 56 (8x12x2048x64), 1039 in place of 94 (1x4x32771x128).
 template <typename T, int DX, int DZ>
 __device__ __forceinline__ void walk_again(const ChunkArgs& a, const Span& sp, int blk, long unit) {
   constexpr int TPR = NT / DZ, N = DX / TPR;           // 4 to 16 lanes a row, of 1 to 32 columns
