@@ -3,9 +3,9 @@
 // by the chunk kernel of falcon_gated_chunk.h.  A long sequence of few chains is cut into
 // segments until some 768 workgroups run: a first kernel forms each segment's own write to
 // the state from zero (k and v only), a second runs the short recurrence over segments,
-// and the main kernel starts each segment from its state.  8x12x2048x64 bf16: 14 + 8 + 28 us
-// in three kernels, 47-52 us a call (walked whole, on 96 workgroups, 77 us); 1x4x32771x128:
-// 27 + 9 + 61 us, 86-92 us a call (walked whole 1666 us).
+// and the main kernel starts each segment from its state.  8x12x2048x64 bf16: 14 + 8 + 30 us
+// in three kernels, 46-52 us a call (walked whole, on 96 workgroups, 77 us); 1x4x32771x128:
+// 26 + 9 + 60 us, 84-91 us a call (walked whole 1664 us).
 #include "falcon_gated_chunk.h"
 
 namespace falcon {

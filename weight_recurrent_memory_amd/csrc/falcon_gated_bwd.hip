@@ -15,10 +15,10 @@
 // passes it, and the rounding left by one document's sums stays out of another's.
 //
 // Four launches: both directions' segment writes, their recurrences, the three gradients,
-// the gates.  8x12x2048x64 bf16: 28 + 13 + 108 + 7 us (143 us a call, the kernels partly
-// overlapping); the gradients move 422 MB over the fabric (inputs read by the dk and dv
-// part and again by the dq part, 3.9 TB/s) and issue 540 vector and 86 matrix
-// instructions a chunk and wave on two waves a SIMD: bound by both.  Tried: three parts in
+// the gates.  8x12x2048x64 bf16: 30 + 13 + 109 + 8 us (131-152 us a call from GPU to GPU, the
+// kernels partly overlapping); the gradients move 422 MB over the fabric (inputs read by
+// the dk and dv part and again by the dq part, 3.9 TB/s) and issue 540 vector and 86
+// matrix instructions a chunk and wave on two waves a SIMD: bound by both.  Tried: three parts in
 // place of two (157 us), blocks of 32 columns (180 us), segments of two chunks for this
 // shape (179 us), each part a launch of its own (188 us).
 #include "falcon_gated_chunk.h"

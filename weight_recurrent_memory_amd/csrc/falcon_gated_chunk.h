@@ -20,10 +20,10 @@
 // happen in registers.  A chunk's x, z and U lie in LDS by rows; products over
 // tokens read x and z transposed; the next chunk's rows are loaded while this one is computed.
 //
-// Bounds.  Forward at 64 columns (8x12x2048, bf16, 768 workgroups): 27.8 us, 142 MB over
-// the fabric = 5.1 TB/s, a large copy's rate; per chunk and wave about 490 vector and 72
-// matrix instructions.  At 128 columns (1x4x32771): 61 us of issue, two workgroups on a
-// compute unit (72 KB of LDS, 246 registers); blocks of 32 z rows in place of 64 make it
+// Bounds.  Forward at 64 columns (8x12x2048, bf16, 768 workgroups): 30 us, 141 MB over
+// the fabric = 4.7 TB/s, nearly a large copy's rate; per chunk and wave about 490 vector and
+// 72 matrix instructions.  At 128 columns (1x4x32771): 60 us of issue, two workgroups on a
+// compute unit (72 KB of LDS, 250 registers); blocks of 32 z rows in place of 64 make it
 // 103 us a call against 92, the scores being formed twice as often.
 // What the layout is for: rows as they come from memory and ds_read_b64_tr_b16 for the
 // products over tokens, in place of a second, transposed copy: 40 KB in place of 57 at 64

@@ -13,11 +13,11 @@
 // All four are bound by HBM: a few operations per element, each element read
 // and written once.  Measured (bf16), where a copy of 1 GiB moves 5.25 TB/s: norm_in
 // 8x2048x12x64 26.1 us = 5.8 TB/s (the last call's rows are partly in the Infinity Cache),
-// norm_in_bwd 4x1999x16x128 60.8 us = 5.9 TB/s, norm_out 8x2048x12x64 with gate and
-// residual 26.0 us = 4.8 TB/s, norm_out_bwd 2x8192x16x128 97 us = 4.8 TB/s.  One row (one token of one head, d elements) lies on
-// d / V lanes, V elements each (one 16-byte access of the element type; float32
-// rows beside bf16 ones take two), so a row's sums are shuffles inside a lane
-// group.  A workgroup takes a tile of TT consecutive tokens with every head and
+// norm_in_bwd 4x1999x16x128 60.0 us = 6.0 TB/s, norm_out 8x2048x12x64 with gate and
+// residual 26.0 us = 4.8 TB/s, norm_out_bwd 2x8192x16x128 100 us = 4.7 TB/s.
+// One row (one token of one head, d elements) lies on d / V lanes, V elements each (one
+// 16-byte access of the element type; float32 rows beside bf16 ones take two), so a
+// row's sums are shuffles inside a lane group.  A workgroup takes a tile of TT consecutive tokens with every head and
 // walks it head by head: the head-major side is then read or written in runs of
 // TT rows, and the token-major side of a tile is one workgroup's, so that lines
 // shared by two heads (d = 16: 32-byte rows) meet in one L2.
