@@ -416,8 +416,9 @@ int falcon_bwd_chunk_noalloc(int variant, int window, int flags, float beta, con
  *
  * dk, dv in {16, 32, 64, 128}, bf16 or fp32; batch * L < 2^31; heads < 2^27 (more:
  * FALCON_ERR_UNSUPPORTED).  Rows are independent: a NaN or an infinity stays in its
- * row (and in dweight).  Outputs overlap no other argument, except that token-major outputs may interleave (views of one
- * fused buffer with one ld) and y as above.  Errors as elsewhere.
+ * row (and in dweight).  Outputs overlap no other argument, except that token-major
+ * outputs may interleave (views of one fused buffer with one ld) and y as above.
+ * Errors as elsewhere.
  */
 #define FALCON_GATE_SILU 0
 #define FALCON_GATE_SIGMOID 1
