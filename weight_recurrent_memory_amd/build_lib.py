@@ -1,11 +1,11 @@
-"""Build libfalcon.so in-tree with hipcc for gfx950.
+"""Build libfalcon.so and libfalcon_block.so in-tree with hipcc for gfx950.
 
     python -m weight_recurrent_memory_amd.build_lib      (or __graft_entry__.build())
 
 Every HIP source is compiled with packed-fp32 instruction selection disabled
-(the compiler then never emits v_pk_{add,mul,fma}_f32) and linked into one
-shared library whose only exported symbols are the C entry points of
-include/falcon.h.
+(the compiler then never emits v_pk_{add,mul,fma}_f32) and linked into two
+shared libraries whose only exported symbols are C entry points: libfalcon.so
+(include/falcon.h) and libfalcon_block.so (include/falcon_block.h).
 """
 from __future__ import annotations
 
@@ -20,6 +20,7 @@ ROOT = os.path.dirname(HERE)
 CSRC = os.path.join(HERE, "csrc")
 INCLUDE = os.path.join(ROOT, "include")
 OUT = os.path.join(HERE, "libfalcon.so")
+BLOCK_OUT = os.path.join(HERE, "libfalcon_block.so")
 BUILD = os.path.join(ROOT, "_build")
 
 SOURCES = ["falcon_api.cpp", "falcon_recurrent.hip", "falcon_decode.hip", "falcon_chunk.hip",
@@ -27,6 +28,8 @@ SOURCES = ["falcon_api.cpp", "falcon_recurrent.hip", "falcon_decode.hip", "falco
            "falcon_chunk_ip.hip", "falcon_backward.hip", "falcon_masked.hip",
            "falcon_norm.hip", "falcon_gated.hip",
            "falcon_gated_bwd.hip", "falcon_gated_decode.hip"]
+BLOCK_SOURCES = ["falcon_block_api.cpp", "falcon_delta.hip", "falcon_delta_solve.hip",
+                 "falcon_delta_decode.hip", "falcon_rotary.hip"]
 ARCH = os.environ.get("FALCON_OFFLOAD_ARCH", "gfx950")
 
 
@@ -52,7 +55,8 @@ def _stale(src: str, obj: str) -> bool:
 
 
 def _compile(src: str, incremental: bool = False) -> str:
-    obj = os.path.join(BUILD, os.path.basename(src) + ".o")
+    folder = os.path.join(BUILD, "block") if src in BLOCK_SOURCES else BUILD
+    obj = os.path.join(folder, os.path.basename(src) + ".o")
     if incremental and not _stale(src, obj):
         return obj
     lang = ["-x", "hip"] if src.endswith(".cpp") else []
@@ -63,19 +67,25 @@ def _compile(src: str, incremental: bool = False) -> str:
     return obj
 
 
-def build(verbose: bool = False, incremental: bool = False) -> str:
-    """Compile every source (only the stale ones with incremental=True) and link."""
-    os.makedirs(BUILD, exist_ok=True)
-    with ThreadPoolExecutor(max_workers=min(8, len(SOURCES), os.cpu_count() or 1)) as ex:
-        objs = list(ex.map(lambda src: _compile(src, incremental), SOURCES))
-    tmp = OUT + ".tmp"
+def _link(objs, out: str) -> None:
+    tmp = out + ".tmp"
     cmd = [hipcc(), "-shared", "-fPIC", "--offload-arch=" + ARCH, "-o", tmp] + objs
     res = subprocess.run(cmd, capture_output=True, text=True)
     if res.returncode != 0:
         raise RuntimeError("link failed: %s\n%s" % (res.stdout, res.stderr))
-    os.replace(tmp, OUT)
+    os.replace(tmp, out)
+
+
+def build(verbose: bool = False, incremental: bool = False) -> str:
+    """Compile every source (only the stale ones with incremental=True) and link."""
+    os.makedirs(os.path.join(BUILD, "block"), exist_ok=True)
+    every = SOURCES + BLOCK_SOURCES
+    with ThreadPoolExecutor(max_workers=min(8, len(every), os.cpu_count() or 1)) as ex:
+        objs = list(ex.map(lambda src: _compile(src, incremental), every))
+    _link(objs[:len(SOURCES)], OUT)
+    _link(objs[len(SOURCES):], BLOCK_OUT)
     if verbose:
-        print("built", OUT)
+        print("built", OUT, BLOCK_OUT)
     return OUT
 
 

@@ -1,0 +1,454 @@
+// falcon_delta.hip - forward of the gated delta rule over a sequence (falcon_delta.h).
+#include "falcon_delta.h"
+
+namespace falcon {
+namespace delta {
+namespace {
+
+struct WalkArgs {
+  const void* q;
+  const void* k;
+  const void* v;
+  const float* beta;
+  const float* log_a;      // or null
+  const uint4* T;
+  const float* S0;         // or null
+  float* o;
+  float* S_out;            // or null; may be S0
+  float* starts;           // [chain][segs][dv][dk]: slot j + 1 first segment j's own write,
+                           // then the state that segment j + 1 starts from (slot 0 unused)
+  float* moves;            // [chain][segs - 1][dk][dk]: what a segment multiplies its start's
+                           // rows with, transposed
+  long chains;
+  int seqlen, nv;
+  int segs, per;           // segments of a chain, chunks of one
+};
+
+template <typename T, int DK, int ND>
+struct WalkLds {
+  static constexpr int NP = planes<T>(), NQ = (DK + 31) / 32;
+  alignas(16) uint16_t k[2][NP][C * DK];
+  alignas(16) uint4 s[2][ND][NQ][3][64];     // S at the chunk's start, as operands
+  alignas(16) uint4 u[2][ND][2][3][64];
+  Gates gate[2];
+  alignas(16) unsigned char bad[4];
+};
+
+// S^T: 16 value rows, columns of keys in tiles of 16.
+template <int DK>
+struct StateT {
+  static constexpr int NK = DK / 16, NQ = (DK + 31) / 32;
+  floatx4 t[NK];
+  __device__ __forceinline__ void load(const float* S) {       // rows of the 16, or null
+    const int m = threadIdx.x & 15, g = (threadIdx.x & 63) >> 4;
+#pragma unroll
+    for (int j = 0; j < NK; ++j)
+      t[j] = S ? *reinterpret_cast<const floatx4*>(S + m * DK + 16 * j + 4 * g) : floatx4{0.f, 0.f, 0.f, 0.f};
+  }
+  __device__ __forceinline__ void unit(int row0) {             // rows of the unit matrix
+    const int m = threadIdx.x & 15, g = (threadIdx.x & 63) >> 4;
+#pragma unroll
+    for (int j = 0; j < NK; ++j)
+#pragma unroll
+      for (int r = 0; r < 4; ++r) t[j][r] = row0 + m == 16 * j + 4 * g + r ? 1.0f : 0.0f;
+  }
+  __device__ __forceinline__ void store(float* S) const {
+    const int m = threadIdx.x & 15, g = (threadIdx.x & 63) >> 4;
+#pragma unroll
+    for (int j = 0; j < NK; ++j) *reinterpret_cast<floatx4*>(S + m * DK + 16 * j + 4 * g) = t[j];
+  }
+  __device__ __forceinline__ void store_transposed(float* S, int row0) const {
+    const int m = threadIdx.x & 15, g = (threadIdx.x & 63) >> 4;
+#pragma unroll
+    for (int j = 0; j < NK; ++j)
+#pragma unroll
+      for (int r = 0; r < 4; ++r) S[(16 * j + 4 * g + r) * DK + row0 + m] = t[j][r];
+  }
+  __device__ __forceinline__ void frag(int i, bf16x8 (&f)[3]) const {
+    const floatx4 zero = {0.f, 0.f, 0.f, 0.f};
+    if constexpr (DK == 16) frag_pair(t[0], zero, f);
+    else frag_pair(t[2 * i], t[2 * i + 1], f);
+  }
+  __device__ __forceinline__ bool finite() const {
+    float s = 0.0f;
+#pragma unroll
+    for (int j = 0; j < NK; ++j) s += (t[j].x + t[j].y) + (t[j].z + t[j].w);
+    return __builtin_isfinite(s);
+  }
+};
+
+// The wave that owns 16 value rows: S through the chunks of a segment.
+template <typename T, int DK>
+struct Walker {
+  static constexpr int NP = planes<T>(), NQ = (DK + 31) / 32, NK = DK / 16;
+  StateT<DK> S;
+  bf16x8 T_[kFrags][3];
+  float v[16];
+
+  __device__ __forceinline__ void load_T(const uint4* p) {
+    const int lane = threadIdx.x & 63;
+#pragma unroll
+    for (int f = 0; f < kFrags; ++f)
+#pragma unroll
+      for (int n = 0; n < 3; ++n) T_[f][n] = __builtin_bit_cast(bf16x8, p[(f * 3 + n) * 64 + lane]);
+  }
+  // v: the sequence's rows from the chunk's first token on; col: of the 16 rows' first
+  __device__ __forceinline__ void load_v(const T* p, long rows, int nv, int col) {
+    const int m = threadIdx.x & 15, g = (threadIdx.x & 63) >> 4;
+    const Window w(p, rows, nv, 0);
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+#pragma unroll
+      for (int r = 0; r < 4; ++r) v[4 * i + r] = load_one(w, (16 * i + 4 * g + r) * nv + col + m, T());
+  }
+
+  // One chunk; store(which, index, plane, fragment) gets S's and U's operands.
+  template <class Next, class Store>
+  __device__ __forceinline__ void chunk(const uint16_t* k, const Gates& gt, Next&& next, Store&& store) {
+    const int g = (threadIdx.x & 63) >> 4;
+    const floatx4 zero = {0.f, 0.f, 0.f, 0.f};
+    floatx4 x[4] = {zero, zero, zero, zero};
+    // K S^T
+#pragma unroll
+    for (int n = 0; n < NQ; ++n) {
+      bf16x8 s[3];
+      S.frag(n, s);
+#pragma unroll
+      for (int p = 0; p < 3; ++p) store(0, n, p, s[p]);
+      bf16x8 kf[4][NP];
+#pragma unroll
+      for (int i = 0; i < 4; ++i) pair_frag<NP, DK>(k, 16 * i + (threadIdx.x & 15), n, kf[i]);
+#pragma unroll
+      for (int p = 0; p < NP; ++p)
+#pragma unroll
+        for (int r = 0; p + r < 3; ++r)
+#pragma unroll
+          for (int i = 0; i < 4; ++i) x[i] = mfma16(kf[i][p], s[r], x[i]);
+    }
+    // X = b v - b e K S^T, then U = T X
+    bf16x8 xf[2][3];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const floatx4 b = *reinterpret_cast<const floatx4*>(gt.b + 16 * i + 4 * g);
+      const floatx4 be = *reinterpret_cast<const floatx4*>(gt.be + 16 * i + 4 * g);
+#pragma unroll
+      for (int r = 0; r < 4; ++r) x[i][r] = b[r] * v[4 * i + r] - be[r] * x[i][r];
+    }
+    frag_pair(x[0], x[1], xf[0]);
+    frag_pair(x[2], x[3], xf[1]);
+    floatx4 u[4] = {zero, zero, zero, zero};
+#pragma unroll
+    for (int j = 0; j < 2; ++j)
+#pragma unroll
+      for (int p = 0; p < 3; ++p)
+#pragma unroll
+        for (int r = 0; p + r < 3; ++r)
+#pragma unroll
+          for (int i = 2 * j; i < 4; ++i) u[i] = mfma16(T_[frag_of(i, j)][p], xf[j][r], u[i]);
+    next();
+    bf16x8 f[3];
+#pragma unroll
+    for (int j = 0; j < 2; ++j) {
+      frag_pair(u[2 * j], u[2 * j + 1], f);
+#pragma unroll
+      for (int p = 0; p < 3; ++p) store(1, j, p, f[p]);
+    }
+    // S <- d S + (w U)^T K
+#pragma unroll
+    for (int i = 0; i < 4; ++i) u[i] *= *reinterpret_cast<const floatx4*>(gt.w + 16 * i + 4 * g);
+    const float d = gt.d;
+#pragma unroll
+    for (int j = 0; j < NK; ++j) S.t[j] *= d;
+#pragma unroll
+    for (int n = 0; n < 2; ++n) {
+      frag_pair(u[2 * n], u[2 * n + 1], f);
+      constexpr int J = NK < 4 ? NK : 4;
+#pragma unroll
+      for (int j0 = 0; j0 < NK; j0 += J) {
+        bf16x8 kt[J][NP];
+#pragma unroll
+        for (int j = 0; j < J; ++j) pair_frag_t<NP, DK>(k, n, j0 + j, kt[j]);
+#pragma unroll
+        for (int p = 0; p < NP; ++p)
+#pragma unroll
+          for (int r = 0; p + r < 3; ++r)
+#pragma unroll
+            for (int j = 0; j < J; ++j) S.t[j0 + j] = mfma16(kt[j][p], f[r], S.t[j0 + j]);
+      }
+    }
+  }
+};
+
+// K rows of a chunk on their way to LDS, by N waves.
+template <typename T, int DK, int NTH>
+struct StageK {
+  static constexpr int NP = planes<T>(), G = DK / 8, UNITS = C * G, N = (UNITS + NTH - 1) / NTH;
+  Raw<T> r[N];
+  __device__ __forceinline__ void load(const Window& w, int t) {
+#pragma unroll
+    for (int i = 0; i < N; ++i) {
+      const int u = t + i * NTH;
+      r[i].load(w, UNITS % NTH == 0 || u < UNITS ? 8 * u * (int)sizeof(T) : kNowhere);
+    }
+  }
+  __device__ __forceinline__ void store(uint16_t* k, int t) const {
+#pragma unroll
+    for (int i = 0; i < N; ++i) {
+      const int u = t + i * NTH;
+      if (UNITS % NTH != 0 && u >= UNITS) continue;
+      uint4 a[NP];
+      r[i].split(a);
+#pragma unroll
+      for (int p = 0; p < NP; ++p) *reinterpret_cast<uint4*>(k + p * C * DK + at<DK>(u / G, 8 * (u % G))) = a[p];
+    }
+  }
+};
+
+// The token tiles of output wave w of ND.
+template <int ND>
+__device__ __forceinline__ int tile_of(int w, int n) {
+  return ND == 1 ? n : n == 0 ? w : 3 - w;
+}
+
+// OUT: the main walk; else a segment's own write (blocks of value rows) and the matrix it
+// multiplies its start's rows with (blocks of unit rows behind them).
+template <typename T, int DK, int ND, bool OUT>
+__global__ __launch_bounds__(128 * ND) void walk_kernel(WalkArgs a) {
+  extern __shared__ __align__(16) unsigned char smem[];
+  using L = WalkLds<T, DK, ND>;
+  constexpr int NP = planes<T>(), NQ = (DK + 31) / 32, DZ = 16 * ND, NTO = 64 * ND, NT_ = 4 / ND;
+  L& lds = *reinterpret_cast<L*>(smem);
+  const int vblocks = a.nv / DZ, blocks = OUT ? vblocks : vblocks + (DK + DZ - 1) / DZ;
+  const int steps = OUT ? a.segs : a.segs - 1;
+  int blk;
+  long unit;
+  if (!place(blocks, a.chains * steps, blk, unit)) return;
+  const long chain = unit / steps;
+  const int seg = (int)(unit % steps);
+  const long len = a.seqlen, chunks = (len + C - 1) / C, c0 = (long)seg * a.per;
+  const int n = (int)(chunks - c0 < a.per ? chunks - c0 : a.per);
+  const int wave = threadIdx.x >> 6, lane = threadIdx.x & 63, m = lane & 15, g = lane >> 4;
+  const T* k = static_cast<const T*>(a.k) + (chain * len + c0 * C) * DK;
+  const long left = len - c0 * C;            // tokens from the segment's start on
+  const bool unit_rows = !OUT && blk >= vblocks;
+  const int row0 = (unit_rows ? blk - vblocks : blk) * DZ;
+
+  if (wave < ND) {
+    const int row = row0 + 16 * wave;
+    const bool idle = unit_rows && row >= DK;
+    Walker<T, DK> w;
+    const T* v = static_cast<const T*>(a.v) + (chain * len + c0 * C) * a.nv;
+    const uint4* Tp = a.T + (chain * chunks + c0) * kT;
+    const long state = (long)a.nv * DK;
+    if (unit_rows) w.S.unit(row);
+    else if (!OUT) w.S.load(nullptr);
+    else if (seg > 0) w.S.load(a.starts + (chain * a.segs + seg) * state + (long)row * DK);
+    else w.S.load(a.S0 ? a.S0 + chain * state + (long)row * DK : nullptr);
+    w.load_T(Tp);
+#pragma unroll
+    for (int i = 0; i < 16; ++i) w.v[i] = 0.0f;
+    if (!unit_rows) w.load_v(v, left, a.nv, row);
+    for (int c = 0; c <= n; ++c) {
+      __syncthreads();
+      if (c == n || idle) continue;
+      w.chunk(lds.k[c & 1][0], lds.gate[c & 1],
+              [&] {
+                if (c + 1 >= n) return;
+                w.load_T(Tp + (long)(c + 1) * kT);
+                if (!unit_rows) w.load_v(v + (long)(c + 1) * C * a.nv, left - (long)(c + 1) * C, a.nv, row);
+              },
+              [&](int which, int i, int p, const bf16x8& f) {
+                if (!OUT) return;
+                uint4* to = which == 0 ? lds.s[c & 1][wave][i][p] : lds.u[c & 1][wave][i][p];
+                to[lane] = __builtin_bit_cast(uint4, f);
+              });
+    }
+    if (OUT) {
+      if (a.S_out && seg == a.segs - 1) w.S.store(a.S_out + chain * state + (long)row * DK);
+    } else if (unit_rows) {
+      if (!idle) w.S.store_transposed(a.moves + (chain * steps + seg) * DK * DK, row);
+    } else {
+      w.S.store(a.starts + (chain * a.segs + seg + 1) * state + (long)row * DK);
+    }
+    return;
+  }
+
+  // the other waves: K and gates of the next chunk, and the outputs of the one before
+  const int ow = wave - ND, ot = threadIdx.x - 64 * ND;
+  const float* la = a.log_a ? a.log_a + chain * len + c0 * C : nullptr;
+  const float* be = a.beta + chain * len + c0 * C;
+  const T* q = static_cast<const T*>(a.q) + (chain * len + c0 * C) * DK;
+  float* o = a.o + (chain * len + c0 * C) * a.nv + row0;
+  StageK<T, DK, NTO> sk;
+  GateLoad gl;
+  sk.load(Window(k, left, DK, 0), ot);
+  gl.load(la, be, 0, left);
+  sk.store(lds.k[0][0], ot);
+  if (ow == 0) gl.store(lds.gate[0]);
+  bf16x8 qf[NT_][NQ][NP], pf[NT_][2][3];
+  float ev[NT_];
+  for (int c = 0; c <= n; ++c) {
+    __syncthreads();
+    PairRow<T, DK> qr[NT_];
+    if (c + 1 < n) {
+      sk.load(Window(k + (long)(c + 1) * C * DK, left - (long)(c + 1) * C, DK, 0), ot);
+      gl.load(la, be, (long)(c + 1) * C, left);
+    }
+    if (OUT) {
+      if (c < n) {
+        const Window wq(q + (long)c * C * DK, left - (long)c * C, DK, 0);
+#pragma unroll
+        for (int j = 0; j < NT_; ++j) qr[j].load(wq, 16 * tile_of<ND>(ow, j) + m);
+      }
+      if (c > 0) {
+        const int b = (c - 1) & 1;
+#pragma unroll
+        for (int z = 0; z < ND; ++z) {
+          floatx4 acc[NT_];
+#pragma unroll
+          for (int j = 0; j < NT_; ++j) acc[j] = floatx4{0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+          for (int i = 0; i < NQ; ++i) {
+            bf16x8 s[3];
+#pragma unroll
+            for (int p = 0; p < 3; ++p) s[p] = __builtin_bit_cast(bf16x8, lds.s[b][z][i][p][lane]);
+#pragma unroll
+            for (int p = 0; p < 3; ++p)
+#pragma unroll
+              for (int r = 0; r < NP; ++r)
+                if (p + r < 3) {
+#pragma unroll
+                  for (int j = 0; j < NT_; ++j) acc[j] = mfma16(s[p], qf[j][i][r], acc[j]);
+                }
+          }
+#pragma unroll
+          for (int j = 0; j < NT_; ++j) acc[j] *= ev[j];
+#pragma unroll
+          for (int i = 0; i < 2; ++i) {
+            bf16x8 u[3];
+#pragma unroll
+            for (int p = 0; p < 3; ++p) u[p] = __builtin_bit_cast(bf16x8, lds.u[b][z][i][p][lane]);
+#pragma unroll
+            for (int p = 0; p < 3; ++p)
+#pragma unroll
+              for (int r = 0; p + r < 3; ++r)
+#pragma unroll
+                for (int j = 0; j < NT_; ++j)
+                  if (i == 0 || tile_of<ND>(ow, j) >= 2) acc[j] = mfma16(u[p], pf[j][i][r], acc[j]);
+          }
+#pragma unroll
+          for (int j = 0; j < NT_; ++j) {
+            const long t = (long)(c - 1) * C + 16 * tile_of<ND>(ow, j) + m;
+            if (t < left)
+              __builtin_nontemporal_store(acc[j], reinterpret_cast<floatx4*>(o + t * a.nv + 16 * z + 4 * g));
+          }
+        }
+      }
+      if (c < n) {
+        // this chunk's scores, decayed: operands with rows t and slots s
+        const uint16_t* kl = lds.k[c & 1][0];
+        const Gates& gt = lds.gate[c & 1];
+#pragma unroll
+        for (int j = 0; j < NT_; ++j) {
+          const int ti = tile_of<ND>(ow, j);
+#pragma unroll
+          for (int i = 0; i < NQ; ++i) qr[j].frag(i, qf[j][i]);
+          ev[j] = gt.e[16 * ti + m];
+          const float2 Gt = gt.g[16 * ti + m];
+#pragma unroll
+          for (int h = 0; h < 2; ++h) {
+            if (2 * h > ti) continue;
+            floatx4 p[2];
+#pragma unroll
+            for (int z = 0; z < 2; ++z) {
+              const int si = 2 * h + z;
+              p[z] = floatx4{0.f, 0.f, 0.f, 0.f};
+              if (si > ti) continue;
+#pragma unroll
+              for (int i = 0; i < NQ; ++i) {
+                bf16x8 kf[NP];
+                pair_frag<NP, DK>(kl, 16 * si + m, i, kf);
+                mma<NP, NP>(kf, qf[j][i], p[z]);
+              }
+#pragma unroll
+              for (int r = 0; r < 4; ++r) {
+                const float x = p[z][r] * decay(Gt, gt.g[16 * si + 4 * g + r]);
+                p[z][r] = (si < ti || 4 * g + r <= m) ? x : 0.0f;
+              }
+            }
+            frag_pair(p[0], p[1], pf[j][h]);
+          }
+        }
+      }
+    }
+    if (c + 1 < n) {
+      sk.store(lds.k[(c + 1) & 1][0], ot);
+      if (ow == 0) gl.store(lds.gate[(c + 1) & 1]);
+    }
+  }
+}
+
+// ------------------------------------------------------------------- plans
+
+struct Plan {
+  int nd, segs, per;
+  long chains;
+  size_t T_bytes, starts, moves;      // bytes
+  size_t bytes() const { return T_bytes + starts + moves; }
+};
+Plan plan_of(const DeltaArgs& a) {
+  Plan p;
+  p.chains = (long)a.batch * a.heads;
+  const long chunks = ((long)a.seqlen + C - 1) / C;
+  p.nd = a.dv >= 32 ? 2 : 1;
+  if (a.dtype != 0 && a.dk == 128) p.nd = 1;
+  p.segs = 1;
+  p.per = (int)chunks;
+  p.T_bytes = (size_t)p.chains * chunks * kT * 16;
+  p.starts = p.segs > 1 ? (size_t)p.chains * p.segs * a.dv * a.dk * 4 : 0;
+  p.moves = p.segs > 1 ? (size_t)p.chains * (p.segs - 1) * a.dk * a.dk * 4 : 0;
+  return p;
+}
+
+template <typename T, int DK, int ND, bool OUT>
+hipError_t go(const WalkArgs& a, hipStream_t stream) {
+  constexpr size_t bytes = sizeof(WalkLds<T, DK, ND>);
+  static_assert(bytes <= 163840, "LDS of a workgroup");
+  auto kernel = walk_kernel<T, DK, ND, OUT>;
+  const hipError_t e = lds_limit(kernel, bytes);
+  if (e != hipSuccess) return e;
+  constexpr int DZ = 16 * ND;
+  const int blocks = OUT ? a.nv / DZ : a.nv / DZ + (DK + DZ - 1) / DZ;
+  hipLaunchKernelGGL(kernel, dim3(grid_of(blocks, a.chains * (OUT ? a.segs : a.segs - 1))), dim3(128 * ND), bytes,
+                     stream, a);
+  return hipGetLastError();
+}
+
+template <typename T>
+hipError_t run(const DeltaArgs& a, const Plan& p, hipStream_t stream) {
+  WalkArgs w{a.q, a.k, a.v, a.beta, a.log_a, static_cast<const uint4*>(a.workspace), a.S0, a.o, a.S_out,
+             nullptr, nullptr, p.chains, a.seqlen, a.dv, p.segs, p.per};
+  const SolveArgs s{a.k, a.beta, a.log_a, static_cast<uint4*>(a.workspace), nullptr, p.chains, a.seqlen};
+  const hipError_t e = launch_solve(s, a.dk, a.dtype, stream);
+  if (e != hipSuccess) return e;
+  return with_dim(a.dk, [&](auto d) {
+    constexpr int DK = decltype(d)::value;
+    if constexpr (!(sizeof(T) == 4 && DK == 128)) {
+      if (p.nd == 2) return go<T, DK, 2, true>(w, stream);
+    }
+    return go<T, DK, 1, true>(w, stream);
+  });
+}
+
+}  // namespace
+}  // namespace delta
+
+size_t delta_workspace_bytes(const DeltaArgs& a) { return delta::plan_of(a).bytes(); }
+
+hipError_t launch_delta(const DeltaArgs& a, hipStream_t stream) {
+  (void)hipGetLastError();
+  const delta::Plan p = delta::plan_of(a);
+  return a.dtype == 0 ? delta::run<uint16_t>(a, p, stream) : delta::run<float>(a, p, stream);
+}
+
+}  // namespace falcon
