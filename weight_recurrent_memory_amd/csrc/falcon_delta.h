@@ -33,6 +33,9 @@ __device__ __forceinline__ void wave_order() {
   __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "wavefront");
 }
 
+// The wave of a workgroup, as a scalar: what goes by it needs no lane masks.
+__device__ __forceinline__ int wave_id() { return __builtin_amdgcn_readfirstlane((int)threadIdx.x >> 6); }
+
 // T as operands of rows t, in paired order of s: of row tile i the 32-token steps 0..i/2.
 constexpr int kFrags = 6;
 __host__ __device__ constexpr int frag_of(int i, int j) { return i < 2 ? i : 2 * i - 2 + j; }

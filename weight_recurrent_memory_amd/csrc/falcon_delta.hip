@@ -16,7 +16,7 @@ struct WalkArgs {
   float* o;
   float* S_out;            // or null; may be S0
   float* starts;           // [chain][segs][dv][dk]: slot j + 1 first segment j's own write,
-                           // then the state that segment j + 1 starts from (slot 0 unused)
+                           // then slot j the state that segment j starts from
   float* moves;            // [chain][segs - 1][dk][dk]: what a segment multiplies its start's
                            // rows with, transposed
   long chains;
@@ -24,14 +24,22 @@ struct WalkArgs {
   int segs, per;           // segments of a chain, chunks of one
 };
 
-template <typename T, int DK, int ND>
-struct WalkLds {
-  static constexpr int NP = planes<T>(), NQ = (DK + 31) / 32;
-  alignas(16) uint16_t k[2][NP][C * DK];
-  alignas(16) uint4 s[2][ND][NQ][3][64];     // S at the chunk's start, as operands
-  alignas(16) uint4 u[2][ND][2][3][64];
-  Gates gate[2];
+// Chunks that K and gates are in LDS before they are used.  bf16: two, so that a chunk's
+// first operands are read behind the one before it.
+template <typename T>
+constexpr int ahead() { return planes<T>() == 1 ? 2 : 1; }
+
+template <typename T, int DK>
+struct StateLds {
+  static constexpr int NP = planes<T>(), NQ = (DK + 31) / 32, R = ahead<T>() + 1;
+  alignas(16) uint16_t k[R][NP][C * DK];
+  Gates gate[R];
   alignas(16) unsigned char bad[4];
+};
+template <typename T, int DK, int ND>
+struct WalkLds : StateLds<T, DK> {
+  alignas(16) uint4 s[2][ND][StateLds<T, DK>::NQ][3][64];     // S at the chunk's start, as operands
+  alignas(16) uint4 u[2][ND][2][3][64];
 };
 
 // S^T: 16 value rows, columns of keys in tiles of 16.
@@ -102,66 +110,71 @@ struct Walker {
       for (int r = 0; r < 4; ++r) v[4 * i + r] = load_one(w, (16 * i + 4 * g + r) * nv + col + m, T());
   }
 
-  // One chunk; store(which, index, plane, fragment) gets S's and U's operands.
-  template <class Next, class Store>
-  __device__ __forceinline__ void chunk(const uint16_t* k, const Gates& gt, Next&& next, Store&& store) {
+  bf16x8 kf[4][NQ][NP];      // K's rows
+
+  __device__ __forceinline__ void load_k(const uint16_t* k) {
+#pragma unroll
+    for (int n = 0; n < NQ; ++n)
+#pragma unroll
+      for (int i = 0; i < 4; ++i) pair_frag<NP, DK>(k, 16 * i + (threadIdx.x & 15), n, kf[i][n]);
+  }
+
+  // One chunk; store(which, index, plane, fragment) gets S's and U's operands.  load() is
+  // called once v and T are used, last() behind everything.
+  template <class Load, class Last, class Store>
+  __device__ __forceinline__ void chunk(const uint16_t* k, const Gates& gt, Load&& load, Last&& last, Store&& store) {
     const int g = (threadIdx.x & 63) >> 4;
     const floatx4 zero = {0.f, 0.f, 0.f, 0.f};
-    floatx4 x[4] = {zero, zero, zero, zero};
+    if (ahead<T>() == 1) load_k(k);
     // K S^T
+    floatx4 x[4] = {zero, zero, zero, zero}, b[4], be[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      b[i] = *reinterpret_cast<const floatx4*>(gt.b + 16 * i + 4 * g);
+      be[i] = *reinterpret_cast<const floatx4*>(gt.be + 16 * i + 4 * g);
+    }
 #pragma unroll
     for (int n = 0; n < NQ; ++n) {
       bf16x8 s[3];
       S.frag(n, s);
 #pragma unroll
       for (int p = 0; p < 3; ++p) store(0, n, p, s[p]);
-      bf16x8 kf[4][NP];
-#pragma unroll
-      for (int i = 0; i < 4; ++i) pair_frag<NP, DK>(k, 16 * i + (threadIdx.x & 15), n, kf[i]);
 #pragma unroll
       for (int p = 0; p < NP; ++p)
 #pragma unroll
         for (int r = 0; p + r < 3; ++r)
 #pragma unroll
-          for (int i = 0; i < 4; ++i) x[i] = mfma16(kf[i][p], s[r], x[i]);
+          for (int i = 0; i < 4; ++i) x[i] = mfma16(kf[i][n][p], s[r], x[i]);
     }
     // X = b v - b e K S^T, then U = T X
-    bf16x8 xf[2][3];
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      const floatx4 b = *reinterpret_cast<const floatx4*>(gt.b + 16 * i + 4 * g);
-      const floatx4 be = *reinterpret_cast<const floatx4*>(gt.be + 16 * i + 4 * g);
-#pragma unroll
-      for (int r = 0; r < 4; ++r) x[i][r] = b[r] * v[4 * i + r] - be[r] * x[i][r];
-    }
-    frag_pair(x[0], x[1], xf[0]);
-    frag_pair(x[2], x[3], xf[1]);
+    bf16x8 xf[3];
     floatx4 u[4] = {zero, zero, zero, zero};
 #pragma unroll
-    for (int j = 0; j < 2; ++j)
+    for (int j = 0; j < 2; ++j) {
+#pragma unroll
+      for (int i = 2 * j; i < 2 * j + 2; ++i)
+#pragma unroll
+        for (int r = 0; r < 4; ++r) x[i][r] = b[i][r] * v[4 * i + r] - be[i][r] * x[i][r];
+      frag_pair(x[2 * j], x[2 * j + 1], xf);
 #pragma unroll
       for (int p = 0; p < 3; ++p)
 #pragma unroll
         for (int r = 0; p + r < 3; ++r)
 #pragma unroll
-          for (int i = 2 * j; i < 4; ++i) u[i] = mfma16(T_[frag_of(i, j)][p], xf[j][r], u[i]);
-    next();
-    bf16x8 f[3];
-#pragma unroll
-    for (int j = 0; j < 2; ++j) {
-      frag_pair(u[2 * j], u[2 * j + 1], f);
-#pragma unroll
-      for (int p = 0; p < 3; ++p) store(1, j, p, f[p]);
+          for (int i = 2 * j; i < 4; ++i) u[i] = mfma16(T_[frag_of(i, j)][p], xf[r], u[i]);
     }
+    load();
     // S <- d S + (w U)^T K
+    bf16x8 f[3];
+    floatx4 w[4];
 #pragma unroll
-    for (int i = 0; i < 4; ++i) u[i] *= *reinterpret_cast<const floatx4*>(gt.w + 16 * i + 4 * g);
+    for (int i = 0; i < 4; ++i) w[i] = *reinterpret_cast<const floatx4*>(gt.w + 16 * i + 4 * g);
     const float d = gt.d;
 #pragma unroll
     for (int j = 0; j < NK; ++j) S.t[j] *= d;
 #pragma unroll
     for (int n = 0; n < 2; ++n) {
-      frag_pair(u[2 * n], u[2 * n + 1], f);
+      frag_pair(u[2 * n] * w[2 * n], u[2 * n + 1] * w[2 * n + 1], f);
       constexpr int J = NK < 4 ? NK : 4;
 #pragma unroll
       for (int j0 = 0; j0 < NK; j0 += J) {
@@ -175,7 +188,11 @@ struct Walker {
 #pragma unroll
             for (int j = 0; j < J; ++j) S.t[j0 + j] = mfma16(kt[j][p], f[r], S.t[j0 + j]);
       }
+      frag_pair(u[2 * n], u[2 * n + 1], f);
+#pragma unroll
+      for (int p = 0; p < 3; ++p) store(1, n, p, f[p]);
     }
+    last();
   }
 };
 
@@ -204,102 +221,55 @@ struct StageK {
   }
 };
 
-// The token tiles of output wave w of ND.
+// The token tiles of output wave w of ND: as many scores each.
 template <int ND>
-__device__ __forceinline__ int tile_of(int w, int n) {
+__device__ __forceinline__ constexpr int tile_of(int w, int n) {
   return ND == 1 ? n : n == 0 ? w : 3 - w;
 }
 
-// OUT: the main walk; else a segment's own write (blocks of value rows) and the matrix it
-// multiplies its start's rows with (blocks of unit rows behind them).
-template <typename T, int DK, int ND, bool OUT>
-__global__ __launch_bounds__(128 * ND) void walk_kernel(WalkArgs a) {
-  extern __shared__ __align__(16) unsigned char smem[];
-  using L = WalkLds<T, DK, ND>;
-  constexpr int NP = planes<T>(), NQ = (DK + 31) / 32, DZ = 16 * ND, NTO = 64 * ND, NT_ = 4 / ND;
-  L& lds = *reinterpret_cast<L*>(smem);
-  const int vblocks = a.nv / DZ, blocks = OUT ? vblocks : vblocks + (DK + DZ - 1) / DZ;
-  const int steps = OUT ? a.segs : a.segs - 1;
-  int blk;
-  long unit;
-  if (!place(blocks, a.chains * steps, blk, unit)) return;
-  const long chain = unit / steps;
-  const int seg = (int)(unit % steps);
-  const long len = a.seqlen, chunks = (len + C - 1) / C, c0 = (long)seg * a.per;
-  const int n = (int)(chunks - c0 < a.per ? chunks - c0 : a.per);
-  const int wave = threadIdx.x >> 6, lane = threadIdx.x & 63, m = lane & 15, g = lane >> 4;
+// The other waves: K and gates of the next chunk, and the outputs of the one before.
+template <typename T, int DK, int ND, bool OUT, int ow>
+__device__ __forceinline__ void helper(const WalkArgs& a, WalkLds<T, DK, ND>& lds, long chain, long c0, int n,
+                                       int row0) {
+  constexpr int NP = planes<T>(), NQ = (DK + 31) / 32, NTO = 64 * ND, NT_ = 4 / ND;
+  const int lane = threadIdx.x & 63, m = lane & 15, g = lane >> 4;
+  const long len = a.seqlen, left = len - c0 * C;
   const T* k = static_cast<const T*>(a.k) + (chain * len + c0 * C) * DK;
-  const long left = len - c0 * C;            // tokens from the segment's start on
-  const bool unit_rows = !OUT && blk >= vblocks;
-  const int row0 = (unit_rows ? blk - vblocks : blk) * DZ;
-
-  if (wave < ND) {
-    const int row = row0 + 16 * wave;
-    const bool idle = unit_rows && row >= DK;
-    Walker<T, DK> w;
-    const T* v = static_cast<const T*>(a.v) + (chain * len + c0 * C) * a.nv;
-    const uint4* Tp = a.T + (chain * chunks + c0) * kT;
-    const long state = (long)a.nv * DK;
-    if (unit_rows) w.S.unit(row);
-    else if (!OUT) w.S.load(nullptr);
-    else if (seg > 0) w.S.load(a.starts + (chain * a.segs + seg) * state + (long)row * DK);
-    else w.S.load(a.S0 ? a.S0 + chain * state + (long)row * DK : nullptr);
-    w.load_T(Tp);
-#pragma unroll
-    for (int i = 0; i < 16; ++i) w.v[i] = 0.0f;
-    if (!unit_rows) w.load_v(v, left, a.nv, row);
-    for (int c = 0; c <= n; ++c) {
-      __syncthreads();
-      if (c == n || idle) continue;
-      w.chunk(lds.k[c & 1][0], lds.gate[c & 1],
-              [&] {
-                if (c + 1 >= n) return;
-                w.load_T(Tp + (long)(c + 1) * kT);
-                if (!unit_rows) w.load_v(v + (long)(c + 1) * C * a.nv, left - (long)(c + 1) * C, a.nv, row);
-              },
-              [&](int which, int i, int p, const bf16x8& f) {
-                if (!OUT) return;
-                uint4* to = which == 0 ? lds.s[c & 1][wave][i][p] : lds.u[c & 1][wave][i][p];
-                to[lane] = __builtin_bit_cast(uint4, f);
-              });
-    }
-    if (OUT) {
-      if (a.S_out && seg == a.segs - 1) w.S.store(a.S_out + chain * state + (long)row * DK);
-    } else if (unit_rows) {
-      if (!idle) w.S.store_transposed(a.moves + (chain * steps + seg) * DK * DK, row);
-    } else {
-      w.S.store(a.starts + (chain * a.segs + seg + 1) * state + (long)row * DK);
-    }
-    return;
-  }
-
-  // the other waves: K and gates of the next chunk, and the outputs of the one before
-  const int ow = wave - ND, ot = threadIdx.x - 64 * ND;
+  const int ot = threadIdx.x - 64 * ND;
   const float* la = a.log_a ? a.log_a + chain * len + c0 * C : nullptr;
   const float* be = a.beta + chain * len + c0 * C;
   const T* q = static_cast<const T*>(a.q) + (chain * len + c0 * C) * DK;
   float* o = a.o + (chain * len + c0 * C) * a.nv + row0;
+  constexpr int D = ahead<T>(), R = D + 1;
   StageK<T, DK, NTO> sk;
   GateLoad gl;
-  sk.load(Window(k, left, DK, 0), ot);
-  gl.load(la, be, 0, left);
-  sk.store(lds.k[0][0], ot);
-  if (ow == 0) gl.store(lds.gate[0]);
+  auto load = [&](int c) {
+    sk.load(Window(k + (long)c * C * DK, left - (long)c * C, DK, 0), ot);
+    gl.load(la, be, (long)c * C, left);
+  };
+  auto store = [&](int c) {
+    sk.store(lds.k[c % R][0], ot);
+    if (ow == 0) gl.store(lds.gate[c % R]);
+  };
+#pragma unroll
+  for (int c = 0; c < D; ++c) {
+    if (c >= n) break;
+    load(c);
+    store(c);
+  }
   bf16x8 qf[NT_][NQ][NP], pf[NT_][2][3];
   float ev[NT_];
+  PairRow<T, DK> qr[NT_];
+  auto load_q = [&](int c) {
+    const Window wq(q + (long)c * C * DK, left - (long)c * C, DK, 0);
+#pragma unroll
+    for (int j = 0; j < NT_; ++j) qr[j].load(wq, 16 * tile_of<ND>(ow, j) + m);
+  };
+  if (OUT) load_q(0);
   for (int c = 0; c <= n; ++c) {
     __syncthreads();
-    PairRow<T, DK> qr[NT_];
-    if (c + 1 < n) {
-      sk.load(Window(k + (long)(c + 1) * C * DK, left - (long)(c + 1) * C, DK, 0), ot);
-      gl.load(la, be, (long)(c + 1) * C, left);
-    }
+    if (c + D < n) load(c + D);
     if (OUT) {
-      if (c < n) {
-        const Window wq(q + (long)c * C * DK, left - (long)c * C, DK, 0);
-#pragma unroll
-        for (int j = 0; j < NT_; ++j) qr[j].load(wq, 16 * tile_of<ND>(ow, j) + m);
-      }
       if (c > 0) {
         const int b = (c - 1) & 1;
 #pragma unroll
@@ -346,8 +316,8 @@ __global__ __launch_bounds__(128 * ND) void walk_kernel(WalkArgs a) {
       }
       if (c < n) {
         // this chunk's scores, decayed: operands with rows t and slots s
-        const uint16_t* kl = lds.k[c & 1][0];
-        const Gates& gt = lds.gate[c & 1];
+        const uint16_t* kl = lds.k[c % R][0];
+        const Gates& gt = lds.gate[c % R];
 #pragma unroll
         for (int j = 0; j < NT_; ++j) {
           const int ti = tile_of<ND>(ow, j);
@@ -379,12 +349,210 @@ __global__ __launch_bounds__(128 * ND) void walk_kernel(WalkArgs a) {
             frag_pair(p[0], p[1], pf[j][h]);
           }
         }
+        if (c + 1 < n) load_q(c + 1);
       }
     }
-    if (c + 1 < n) {
-      sk.store(lds.k[(c + 1) & 1][0], ot);
-      if (ow == 0) gl.store(lds.gate[(c + 1) & 1]);
+    if (c + D < n) store(c + D);
+  }
+}
+
+// The segment's outputs that are not finite formed anew, by the recurrence itself, one token
+// at a time: a product over a chunk's tokens multiplies those that a mask leaves out with 0,
+// and 0 * NaN is NaN, so that a NaN in v would reach every output of its chunk, also of
+// earlier tokens.  The state behind the segment is not finite either, which is where it is
+// looked for.  A row of the state lies on 8 lanes.
+template <typename T, int DK, int ND>
+__device__ __forceinline__ void walk_again(const WalkArgs& a, long chain, int seg, int row0) {
+  constexpr int TPR = 8, N = DK / TPR;
+  const long len = a.seqlen, state = (long)a.nv * DK, first = (long)seg * a.per * C;
+  const long end = first + (long)a.per * C < len ? first + (long)a.per * C : len;
+  const int row = row0 + (int)threadIdx.x / TPR, c0 = ((int)threadIdx.x % TPR) * N;
+  const T* k = static_cast<const T*>(a.k) + chain * len * DK + c0;
+  const T* q = static_cast<const T*>(a.q) + chain * len * DK + c0;
+  const T* v = static_cast<const T*>(a.v) + chain * len * a.nv + row;
+  const float* la = a.log_a ? a.log_a + chain * len : nullptr;
+  const float* be = a.beta + chain * len;
+  float* out = a.o + chain * len * a.nv + row;
+  const float* S0 = a.segs > 1 ? a.starts + (chain * a.segs + seg) * state : a.S0 ? a.S0 + chain * state : nullptr;
+  const long at = (long)row * DK + c0;
+  float S[N];
+#pragma unroll
+  for (int j = 0; j < N; ++j) S[j] = S0 ? S0[at + j] : 0.0f;
+  for (long t = first; t < end; ++t) {
+    const float d = la ? exp2_of(log2_decay(la[t])) : 1.0f, b = be[t], vt = ld_in(v, t * a.nv);
+    float r = 0.0f, o = 0.0f;
+#pragma unroll
+    for (int j = 0; j < N; ++j) {
+      S[j] *= d;
+      r += S[j] * ld_in(k, t * DK + j);
     }
+    const float u = b * (vt - group_sum<TPR>(r));
+#pragma unroll
+    for (int j = 0; j < N; ++j) {
+      S[j] += u * ld_in(k, t * DK + j);
+      o += S[j] * ld_in(q, t * DK + j);
+    }
+    o = group_sum<TPR>(o);
+    if (c0 == 0 && !__builtin_isfinite(out[t * a.nv])) out[t * a.nv] = o;
+  }
+  if (a.S_out && seg == a.segs - 1) {
+#pragma unroll
+    for (int j = 0; j < N; ++j) a.S_out[chain * state + at + j] = S[j];
+  }
+}
+
+// The running kernel's arguments read anew: what only a rare path needs is not held in
+// registers up to it.
+__device__ __forceinline__ WalkArgs args_again() {
+  unsigned long at = (unsigned long)__builtin_amdgcn_kernarg_segment_ptr();
+  asm volatile("" : "+s"(at));
+  struct { unsigned w[sizeof(WalkArgs) / 4]; } words;
+#pragma unroll
+  for (unsigned i = 0; i < sizeof(WalkArgs) / 4; ++i)
+    words.w[i] = ((const __attribute__((address_space(4))) unsigned*)at)[i];
+  return __builtin_bit_cast(WalkArgs, words);
+}
+
+// OUT: the main walk; else a segment's own write (blocks of value rows) and the matrix it
+// multiplies its start's rows with (blocks of unit rows behind them).
+template <typename T, int DK, int ND, bool OUT>
+__global__ __launch_bounds__(128 * ND, (OUT ? 2 : 1)) void walk_kernel(WalkArgs a) {
+  extern __shared__ __align__(16) unsigned char smem[];
+  using L = WalkLds<T, DK, ND>;
+  constexpr int DZ = 16 * ND;
+  L& lds = *reinterpret_cast<L*>(smem);
+  const int vblocks = a.nv / DZ, blocks = OUT ? vblocks : vblocks + (DK + DZ - 1) / DZ;
+  const int steps = OUT ? a.segs : a.segs - 1;
+  int blk;
+  long unit;
+  if (!place(blocks, a.chains * steps, blk, unit)) return;
+  const long chain = unit / steps;
+  const int seg = (int)(unit % steps);
+  const long len = a.seqlen, chunks = (len + C - 1) / C, c0 = (long)seg * a.per;
+  const int n = (int)(chunks - c0 < a.per ? chunks - c0 : a.per);
+  const int wave = wave_id(), lane = threadIdx.x & 63;
+  const long left = len - c0 * C;            // tokens from the segment's start on
+  const bool unit_rows = !OUT && blk >= vblocks;
+  const int row0 = (unit_rows ? blk - vblocks : blk) * DZ;
+
+  if (wave < ND) {
+    const int row = row0 + 16 * wave;
+    const bool idle = unit_rows && row >= DK;
+    Walker<T, DK> w;
+    const T* v = static_cast<const T*>(a.v) + (chain * len + c0 * C) * a.nv;
+    const uint4* Tp = a.T + (chain * chunks + c0) * kT;
+    const long state = (long)a.nv * DK;
+    if (unit_rows) w.S.unit(row);
+    else if (!OUT) w.S.load(nullptr);
+    else if (a.segs > 1) w.S.load(a.starts + (chain * a.segs + seg) * state + (long)row * DK);
+    else w.S.load(a.S0 ? a.S0 + chain * state + (long)row * DK : nullptr);
+    w.load_T(Tp);
+#pragma unroll
+    for (int i = 0; i < 16; ++i) w.v[i] = 0.0f;
+    if (!unit_rows) w.load_v(v, left, a.nv, row);
+    for (int c = 0; c <= n; ++c) {
+      __syncthreads();
+      if (c == n || idle) continue;
+      if (ahead<T>() > 1 && c == 0) w.load_k(lds.k[0][0]);
+      w.chunk(lds.k[c % L::R][0], lds.gate[c % L::R],
+              [&] {
+                if (c + 1 >= n) return;
+                // (loads come back in order: the one needed first is issued first)
+                if (!unit_rows) w.load_v(v + (long)(c + 1) * C * a.nv, left - (long)(c + 1) * C, a.nv, row);
+                w.load_T(Tp + (long)(c + 1) * kT);
+              },
+              [&] {
+                if (ahead<T>() > 1) w.load_k(lds.k[(c + 1) % L::R][0]);
+              },
+              [&](int which, int i, int p, const bf16x8& f) {
+                if (!OUT) return;
+                uint4* to = which == 0 ? lds.s[c & 1][wave][i][p] : lds.u[c & 1][wave][i][p];
+                to[lane] = __builtin_bit_cast(uint4, f);
+              });
+    }
+    if (OUT) {
+      const bool bad = __any(!w.S.finite());
+      if (lane == 0) lds.bad[wave] = bad;
+      if (!bad && a.S_out && seg == a.segs - 1) w.S.store(a.S_out + chain * state + (long)row * DK);
+      __syncthreads();
+    } else if (unit_rows) {
+      if (!idle) w.S.store_transposed(a.moves + (chain * steps + seg) * DK * DK, row);
+    } else {
+      w.S.store(a.starts + (chain * a.segs + seg + 1) * state + (long)row * DK);
+    }
+  } else {
+    if (ND == 1 || wave == ND) helper<T, DK, ND, OUT, 0>(a, lds, chain, c0, n, row0);
+    else helper<T, DK, ND, OUT, 1>(a, lds, chain, c0, n, row0);
+    if (OUT) __syncthreads();
+  }
+  if (OUT) {
+    bool bad = false;
+#pragma unroll
+    for (int i = 0; i < ND; ++i) bad |= lds.bad[i] != 0;
+    // (of 16 rows each, so that rows whose result replaced their start stay as they are)
+    if (__builtin_expect(bad, 0) && lds.bad[wave / 2]) {
+      const WalkArgs again = args_again();
+      place(again.nv / DZ, again.chains * again.segs, blk, unit);
+      walk_again<T, DK, ND>(again, unit / again.segs, (int)(unit % again.segs), blk * DZ);
+    }
+  }
+}
+
+
+// The states that segments start from: start of j + 1 = (start of j) M_j + write of j, in
+// place.  A workgroup takes 16 value rows of a chain, a wave 16 columns of the result.
+template <int DK>
+__global__ __launch_bounds__(4 * DK) void join_kernel(WalkArgs a) {
+  constexpr int NQ = (DK + 31) / 32;
+  __shared__ __align__(16) uint2 s[2][NQ][3][64][2];
+  const int wave = wave_id(), lane = threadIdx.x & 63, m = lane & 15, g = lane >> 4;
+  const int blocks = a.nv / 16;
+  const long chain = blockIdx.x / blocks, state = (long)a.nv * DK;
+  const long row = (blockIdx.x % blocks) * 16 + m;
+  const long at = row * DK + 16 * wave + 4 * g;
+  float* starts = a.starts + chain * a.segs * state + at;
+  const float* moves = a.moves + chain * (a.segs - 1) * DK * DK + (16 * wave + m) * DK + 4 * g;
+  const floatx4 zero = {0.f, 0.f, 0.f, 0.f};
+  floatx4 x = a.S0 ? *reinterpret_cast<const floatx4*>(a.S0 + chain * state + at) : zero;
+  *reinterpret_cast<floatx4*>(starts) = x;
+  if (DK == 16) {
+    for (int i = threadIdx.x; i < 2 * 3 * 64; i += 64) (&s[0][0][0][0][0])[2 * i + 1] = uint2{0u, 0u};
+  }
+  floatx4 lo[NQ], hi[NQ], w;
+  auto fetch = [&](int j) {
+    w = *reinterpret_cast<const floatx4*>(starts + (j + 1) * state);
+#pragma unroll
+    for (int i = 0; i < NQ; ++i) {
+      lo[i] = *reinterpret_cast<const floatx4*>(moves + (long)j * DK * DK + 32 * i);
+      hi[i] = DK > 16 ? *reinterpret_cast<const floatx4*>(moves + (long)j * DK * DK + 32 * i + 16) : zero;
+    }
+  };
+  fetch(0);
+  for (int j = 0; j < a.segs - 1; ++j) {
+    uint2 h, mi, l;
+    split3(x.x, x.y, h.x, mi.x, l.x);
+    split3(x.z, x.w, h.y, mi.y, l.y);
+    uint2 (*to)[64][2] = s[j & 1][wave / 2];
+    to[0][lane][wave & 1] = h;
+    to[1][lane][wave & 1] = mi;
+    to[2][lane][wave & 1] = l;
+    bf16x8 f[NQ][3];
+#pragma unroll
+    for (int i = 0; i < NQ; ++i) frag_pair(lo[i], hi[i], f[i]);
+    x = w;
+    __syncthreads();
+    if (j + 2 < a.segs) fetch(j + 1);
+    floatx4 y = zero;
+#pragma unroll
+    for (int i = 0; i < NQ; ++i) {
+      bf16x8 b[3];
+#pragma unroll
+      for (int p = 0; p < 3; ++p) b[p] = __builtin_bit_cast(bf16x8, *reinterpret_cast<const uint4*>(s[j & 1][i][p][lane]));
+      if (i & 1) mma<3, 3>(f[i], b, y);
+      else mma<3, 3>(f[i], b, x);
+    }
+    x += y;
+    *reinterpret_cast<floatx4*>(starts + (j + 1) * state) = x;
   }
 }
 
@@ -396,6 +564,7 @@ struct Plan {
   size_t T_bytes, starts, moves;      // bytes
   size_t bytes() const { return T_bytes + starts + moves; }
 };
+constexpr long kWhole = 16, kSlots = 512;
 Plan plan_of(const DeltaArgs& a) {
   Plan p;
   p.chains = (long)a.batch * a.heads;
@@ -404,6 +573,14 @@ Plan plan_of(const DeltaArgs& a) {
   if (a.dtype != 0 && a.dk == 128) p.nd = 1;
   p.segs = 1;
   p.per = (int)chunks;
+  // segments: walked twice, and the first time with dk unit rows more
+  const long units = p.chains * ((a.dv + a.dk) / (16 * p.nd));
+  if (chunks >= kWhole && units <= kSlots / 4) {
+    long n = kSlots / units;
+    if (n > chunks / 4) n = chunks / 4;
+    p.per = (int)((chunks + n - 1) / n);
+    p.segs = (int)((chunks + p.per - 1) / p.per);
+  }
   p.T_bytes = (size_t)p.chains * chunks * kT * 16;
   p.starts = p.segs > 1 ? (size_t)p.chains * p.segs * a.dv * a.dk * 4 : 0;
   p.moves = p.segs > 1 ? (size_t)p.chains * (p.segs - 1) * a.dk * a.dk * 4 : 0;
@@ -412,7 +589,7 @@ Plan plan_of(const DeltaArgs& a) {
 
 template <typename T, int DK, int ND, bool OUT>
 hipError_t go(const WalkArgs& a, hipStream_t stream) {
-  constexpr size_t bytes = sizeof(WalkLds<T, DK, ND>);
+  constexpr size_t bytes = OUT ? sizeof(WalkLds<T, DK, ND>) : sizeof(StateLds<T, DK>);
   static_assert(bytes <= 163840, "LDS of a workgroup");
   auto kernel = walk_kernel<T, DK, ND, OUT>;
   const hipError_t e = lds_limit(kernel, bytes);
@@ -426,17 +603,28 @@ hipError_t go(const WalkArgs& a, hipStream_t stream) {
 
 template <typename T>
 hipError_t run(const DeltaArgs& a, const Plan& p, hipStream_t stream) {
-  WalkArgs w{a.q, a.k, a.v, a.beta, a.log_a, static_cast<const uint4*>(a.workspace), a.S0, a.o, a.S_out,
-             nullptr, nullptr, p.chains, a.seqlen, a.dv, p.segs, p.per};
+  char* ws = static_cast<char*>(a.workspace);
+  WalkArgs w{a.q, a.k, a.v, a.beta, a.log_a, reinterpret_cast<const uint4*>(ws), a.S0, a.o, a.S_out,
+             reinterpret_cast<float*>(ws + p.T_bytes), reinterpret_cast<float*>(ws + p.T_bytes + p.starts), p.chains, a.seqlen, a.dv, p.segs, p.per};
   const SolveArgs s{a.k, a.beta, a.log_a, static_cast<uint4*>(a.workspace), nullptr, p.chains, a.seqlen};
   const hipError_t e = launch_solve(s, a.dk, a.dtype, stream);
   if (e != hipSuccess) return e;
   return with_dim(a.dk, [&](auto d) {
     constexpr int DK = decltype(d)::value;
+    auto walk = [&](auto nd) {
+      constexpr int ND = decltype(nd)::value;
+      if (p.segs > 1) {
+        hipError_t e = go<T, DK, ND, false>(w, stream);
+        if (e != hipSuccess) return e;
+        hipLaunchKernelGGL((join_kernel<DK>), dim3((unsigned)(p.chains * (a.dv / 16))), dim3(4 * DK), 0, stream, w);
+        if ((e = hipGetLastError()) != hipSuccess) return e;
+      }
+      return go<T, DK, ND, true>(w, stream);
+    };
     if constexpr (!(sizeof(T) == 4 && DK == 128)) {
-      if (p.nd == 2) return go<T, DK, 2, true>(w, stream);
+      if (p.nd == 2) return walk(std::integral_constant<int, 2>());
     }
-    return go<T, DK, 1, true>(w, stream);
+    return walk(std::integral_constant<int, 1>());
   });
 }
 

@@ -52,8 +52,8 @@ template <typename T, int DK>
 __global__ __launch_bounds__(64 * kWaves) void solve_kernel(SolveArgs a, int chunks) {
   constexpr int NP = planes<T>(), NQ = (DK + 31) / 32;
   __shared__ SolveLds all[kWaves];
-  SolveLds& lds = all[threadIdx.x >> 6];
-  const long unit = (long)blockIdx.x * kWaves + (threadIdx.x >> 6);
+  SolveLds& lds = all[wave_id()];
+  const long unit = (long)blockIdx.x * kWaves + wave_id();
   if (unit >= a.chains * chunks) return;
   const long chain = unit / chunks, t0 = (unit % chunks) * C, len = a.seqlen;
   const int lane = threadIdx.x & 63, m = lane & 15, g = lane >> 4;
