@@ -24,14 +24,14 @@ struct WalkArgs {
   int segs, per;           // segments of a chain, chunks of one
 };
 
-// Chunks that K and gates are in LDS before they are used.  bf16: two, so that a chunk's
-// first operands are read behind the one before it.
-template <typename T>
-constexpr int ahead() { return planes<T>() == 1 ? 2 : 1; }
+// Chunks that K and gates are in LDS before they are used.  Two where there are registers for
+// a chunk's first operands behind the chunk before it.
+template <typename T, int DK>
+constexpr int ahead() { return planes<T>() == 1 && DK <= 64 ? 2 : 1; }
 
 template <typename T, int DK>
 struct StateLds {
-  static constexpr int NP = planes<T>(), NQ = (DK + 31) / 32, R = ahead<T>() + 1;
+  static constexpr int NP = planes<T>(), NQ = (DK + 31) / 32, R = ahead<T, DK>() + 1;
   alignas(16) uint16_t k[R][NP][C * DK];
   Gates gate[R];
   alignas(16) unsigned char bad[4];
@@ -110,13 +110,18 @@ struct Walker {
       for (int r = 0; r < 4; ++r) v[4 * i + r] = load_one(w, (16 * i + 4 * g + r) * nv + col + m, T());
   }
 
-  bf16x8 kf[4][NQ][NP];      // K's rows
+  static constexpr bool kAhead = ahead<T, DK>() > 1;
+  bf16x8 kf[kAhead ? NQ : 1][4][NP];      // K's rows
 
+  __device__ __forceinline__ void load_k_step(const uint16_t* k, int n, bf16x8 (&f)[4][NP]) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) pair_frag<NP, DK>(k, 16 * i + (threadIdx.x & 15), n, f[i]);
+  }
   __device__ __forceinline__ void load_k(const uint16_t* k) {
+    if constexpr (kAhead) {
 #pragma unroll
-    for (int n = 0; n < NQ; ++n)
-#pragma unroll
-      for (int i = 0; i < 4; ++i) pair_frag<NP, DK>(k, 16 * i + (threadIdx.x & 15), n, kf[i][n]);
+      for (int n = 0; n < NQ; ++n) load_k_step(k, n, kf[n]);
+    }
   }
 
   // One chunk; store(which, index, plane, fragment) gets S's and U's operands.  load() is
@@ -125,7 +130,6 @@ struct Walker {
   __device__ __forceinline__ void chunk(const uint16_t* k, const Gates& gt, Load&& load, Last&& last, Store&& store) {
     const int g = (threadIdx.x & 63) >> 4;
     const floatx4 zero = {0.f, 0.f, 0.f, 0.f};
-    if (ahead<T>() == 1) load_k(k);
     // K S^T
     floatx4 x[4] = {zero, zero, zero, zero}, b[4], be[4];
 #pragma unroll
@@ -139,12 +143,14 @@ struct Walker {
       S.frag(n, s);
 #pragma unroll
       for (int p = 0; p < 3; ++p) store(0, n, p, s[p]);
+      bf16x8(&kn)[4][NP] = kf[kAhead ? n : 0];
+      if (!kAhead) load_k_step(k, n, kn);
 #pragma unroll
       for (int p = 0; p < NP; ++p)
 #pragma unroll
         for (int r = 0; p + r < 3; ++r)
 #pragma unroll
-          for (int i = 0; i < 4; ++i) x[i] = mfma16(kf[i][n][p], s[r], x[i]);
+          for (int i = 0; i < 4; ++i) x[i] = mfma16(kn[i][p], s[r], x[i]);
     }
     // X = b v - b e K S^T, then U = T X
     bf16x8 xf[3];
@@ -221,17 +227,20 @@ struct StageK {
   }
 };
 
-// The token tiles of output wave w of ND: as many scores each.
+// Output waves of a workgroup of ND state waves (ND = 4: no outputs, two that read K), and the token tiles of output wave w.  (Waves
+// go to the compute unit's four SIMDs in turn: with ND = 2 the tiles of most scores get the
+// SIMDs without a state wave.)
+constexpr int out_waves(int nd) { return nd < 4 ? 2 * nd : 2; }
 template <int ND>
 __device__ __forceinline__ constexpr int tile_of(int w, int n) {
-  return ND == 1 ? n : n == 0 ? w : 3 - w;
+  return ND == 1 ? (n == 0 ? w : 3 - w) : w < 2 ? 3 - w : w - 2;
 }
 
 // The other waves: K and gates of the next chunk, and the outputs of the one before.
 template <typename T, int DK, int ND, bool OUT, int ow>
 __device__ __forceinline__ void helper(const WalkArgs& a, WalkLds<T, DK, ND>& lds, long chain, long c0, int n,
                                        int row0) {
-  constexpr int NP = planes<T>(), NQ = (DK + 31) / 32, NTO = 64 * ND, NT_ = 4 / ND;
+  constexpr int NP = planes<T>(), NQ = (DK + 31) / 32, NTO = 64 * out_waves(ND), NT_ = 4 / out_waves(ND);
   const int lane = threadIdx.x & 63, m = lane & 15, g = lane >> 4;
   const long len = a.seqlen, left = len - c0 * C;
   const T* k = static_cast<const T*>(a.k) + (chain * len + c0 * C) * DK;
@@ -240,7 +249,7 @@ __device__ __forceinline__ void helper(const WalkArgs& a, WalkLds<T, DK, ND>& ld
   const float* be = a.beta + chain * len + c0 * C;
   const T* q = static_cast<const T*>(a.q) + (chain * len + c0 * C) * DK;
   float* o = a.o + (chain * len + c0 * C) * a.nv + row0;
-  constexpr int D = ahead<T>(), R = D + 1;
+  constexpr int D = ahead<T, DK>(), R = D + 1;
   StageK<T, DK, NTO> sk;
   GateLoad gl;
   auto load = [&](int c) {
@@ -413,10 +422,15 @@ __device__ __forceinline__ WalkArgs args_again() {
   return __builtin_bit_cast(WalkArgs, words);
 }
 
+constexpr int threads_of(int nd) { return 64 * (nd + out_waves(nd)); }
+// Waves a SIMD that registers are held to: two, but where that spills.
+template <typename T, int DK, int ND, bool OUT>
+constexpr int waves_of() { return OUT && planes<T>() == 3 && DK == 128 ? 1 : 2; }
+
 // OUT: the main walk; else a segment's own write (blocks of value rows) and the matrix it
 // multiplies its start's rows with (blocks of unit rows behind them).
 template <typename T, int DK, int ND, bool OUT>
-__global__ __launch_bounds__(128 * ND, (OUT ? 2 : 1)) void walk_kernel(WalkArgs a) {
+__global__ __launch_bounds__(threads_of(ND), (waves_of<T, DK, ND, OUT>())) void walk_kernel(WalkArgs a) {
   extern __shared__ __align__(16) unsigned char smem[];
   using L = WalkLds<T, DK, ND>;
   constexpr int DZ = 16 * ND;
@@ -436,8 +450,7 @@ __global__ __launch_bounds__(128 * ND, (OUT ? 2 : 1)) void walk_kernel(WalkArgs 
   const int row0 = (unit_rows ? blk - vblocks : blk) * DZ;
 
   if (wave < ND) {
-    const int row = row0 + 16 * wave;
-    const bool idle = unit_rows && row >= DK;
+    const int row = row0 + 16 * wave;          // (unit rows behind the last one are zeros)
     Walker<T, DK> w;
     const T* v = static_cast<const T*>(a.v) + (chain * len + c0 * C) * a.nv;
     const uint4* Tp = a.T + (chain * chunks + c0) * kT;
@@ -447,42 +460,45 @@ __global__ __launch_bounds__(128 * ND, (OUT ? 2 : 1)) void walk_kernel(WalkArgs 
     else if (a.segs > 1) w.S.load(a.starts + (chain * a.segs + seg) * state + (long)row * DK);
     else w.S.load(a.S0 ? a.S0 + chain * state + (long)row * DK : nullptr);
     w.load_T(Tp);
-#pragma unroll
-    for (int i = 0; i < 16; ++i) w.v[i] = 0.0f;
-    if (!unit_rows) w.load_v(v, left, a.nv, row);
-    for (int c = 0; c <= n; ++c) {
+    // (unit rows have no v: a window of no rows reads 0)
+    auto load_v = [&](int c) {
+      w.load_v(v + (long)c * C * a.nv, unit_rows ? 0 : left - (long)c * C, a.nv, row);
+    };
+    load_v(0);
+    for (int c = 0; c < n; ++c) {
       __syncthreads();
-      if (c == n || idle) continue;
-      if (ahead<T>() > 1 && c == 0) w.load_k(lds.k[0][0]);
+      if (c == 0) w.load_k(lds.k[0][0]);
+      // (what is behind the last chunk is loaded in its own place: no branch holds registers)
+      const int next = c + 1 < n ? c + 1 : c;
       w.chunk(lds.k[c % L::R][0], lds.gate[c % L::R],
               [&] {
-                if (c + 1 >= n) return;
                 // (loads come back in order: the one needed first is issued first)
-                if (!unit_rows) w.load_v(v + (long)(c + 1) * C * a.nv, left - (long)(c + 1) * C, a.nv, row);
-                w.load_T(Tp + (long)(c + 1) * kT);
+                load_v(next);
+                w.load_T(Tp + (long)next * kT);
               },
-              [&] {
-                if (ahead<T>() > 1) w.load_k(lds.k[(c + 1) % L::R][0]);
-              },
+              [&] { w.load_k(lds.k[next % L::R][0]); },
               [&](int which, int i, int p, const bf16x8& f) {
                 if (!OUT) return;
                 uint4* to = which == 0 ? lds.s[c & 1][wave][i][p] : lds.u[c & 1][wave][i][p];
                 to[lane] = __builtin_bit_cast(uint4, f);
               });
     }
+    __syncthreads();
     if (OUT) {
       const bool bad = __any(!w.S.finite());
       if (lane == 0) lds.bad[wave] = bad;
       if (!bad && a.S_out && seg == a.segs - 1) w.S.store(a.S_out + chain * state + (long)row * DK);
       __syncthreads();
     } else if (unit_rows) {
-      if (!idle) w.S.store_transposed(a.moves + (chain * steps + seg) * DK * DK, row);
+      if (row < DK) w.S.store_transposed(a.moves + (chain * steps + seg) * DK * DK, row);
     } else {
       w.S.store(a.starts + (chain * a.segs + seg + 1) * state + (long)row * DK);
     }
   } else {
-    if (ND == 1 || wave == ND) helper<T, DK, ND, OUT, 0>(a, lds, chain, c0, n, row0);
-    else helper<T, DK, ND, OUT, 1>(a, lds, chain, c0, n, row0);
+    if (wave == ND) helper<T, DK, ND, OUT, 0>(a, lds, chain, c0, n, row0);
+    else if (wave == ND + 1) helper<T, DK, ND, OUT, 1>(a, lds, chain, c0, n, row0);
+    else if (wave == ND + 2) helper<T, DK, ND, OUT, 2>(a, lds, chain, c0, n, row0);
+    else helper<T, DK, ND, OUT, 3>(a, lds, chain, c0, n, row0);
     if (OUT) __syncthreads();
   }
   if (OUT) {
@@ -490,7 +506,7 @@ __global__ __launch_bounds__(128 * ND, (OUT ? 2 : 1)) void walk_kernel(WalkArgs 
 #pragma unroll
     for (int i = 0; i < ND; ++i) bad |= lds.bad[i] != 0;
     // (of 16 rows each, so that rows whose result replaced their start stay as they are)
-    if (__builtin_expect(bad, 0) && lds.bad[wave / 2]) {
+    if (__builtin_expect(bad, 0) && threadIdx.x < 128 * ND && lds.bad[wave / 2]) {
       const WalkArgs again = args_again();
       place(again.nv / DZ, again.chains * again.segs, blk, unit);
       walk_again<T, DK, ND>(again, unit / again.segs, (int)(unit % again.segs), blk * DZ);
@@ -564,7 +580,7 @@ struct Plan {
   size_t T_bytes, starts, moves;      // bytes
   size_t bytes() const { return T_bytes + starts + moves; }
 };
-constexpr long kWhole = 16, kSlots = 512;
+constexpr long kWhole = 16, kSlots = 256;
 Plan plan_of(const DeltaArgs& a) {
   Plan p;
   p.chains = (long)a.batch * a.heads;
@@ -574,7 +590,7 @@ Plan plan_of(const DeltaArgs& a) {
   p.segs = 1;
   p.per = (int)chunks;
   // segments: walked twice, and the first time with dk unit rows more
-  const long units = p.chains * ((a.dv + a.dk) / (16 * p.nd));
+  const long units = p.chains * ((a.dv + a.dk + 63) / 64);
   if (chunks >= kWhole && units <= kSlots / 4) {
     long n = kSlots / units;
     if (n > chunks / 4) n = chunks / 4;
@@ -596,7 +612,7 @@ hipError_t go(const WalkArgs& a, hipStream_t stream) {
   if (e != hipSuccess) return e;
   constexpr int DZ = 16 * ND;
   const int blocks = OUT ? a.nv / DZ : a.nv / DZ + (DK + DZ - 1) / DZ;
-  hipLaunchKernelGGL(kernel, dim3(grid_of(blocks, a.chains * (OUT ? a.segs : a.segs - 1))), dim3(128 * ND), bytes,
+  hipLaunchKernelGGL(kernel, dim3(grid_of(blocks, a.chains * (OUT ? a.segs : a.segs - 1))), dim3(threads_of(ND)), bytes,
                      stream, a);
   return hipGetLastError();
 }
@@ -614,7 +630,8 @@ hipError_t run(const DeltaArgs& a, const Plan& p, hipStream_t stream) {
     auto walk = [&](auto nd) {
       constexpr int ND = decltype(nd)::value;
       if (p.segs > 1) {
-        hipError_t e = go<T, DK, ND, false>(w, stream);
+        // (a state wave for each SIMD of a compute unit)
+        hipError_t e = a.dv >= 64 ? go<T, DK, 4, false>(w, stream) : go<T, DK, ND, false>(w, stream);
         if (e != hipSuccess) return e;
         hipLaunchKernelGGL((join_kernel<DK>), dim3((unsigned)(p.chains * (a.dv / 16))), dim3(4 * DK), 0, stream, w);
         if ((e = hipGetLastError()) != hipSuccess) return e;
