@@ -42,6 +42,23 @@ extern "C" {
  * from one, are walked again token by token, which takes many times as long.)
  * batch * heads * max(dk, dv) * (L + 63) / 64 < 2^31 (FALCON_ERR_UNSUPPORTED from there on).
  *
+ * falcon_gated_delta_bwd_chunk - gradients of sum <dO, o> + <dS_L, S_L>
+ *   q, k, v, beta, log_a, S0, dtype   as the forward's
+ *   dO       [batch, heads, L, dv] float32
+ *   dS_L     [batch, heads, dv, dk] float32, or NULL
+ *   dq, dk_out, dv_out   [batch, heads, L, dk / dk / dv] float32
+ *   dbeta    [batch, heads, L] float32
+ *   dlog_a   [batch, heads, L] float32, or NULL; needs log_a.  0 at a reset, and before one
+ *            nothing of what lies behind it.  A difference of sums: its error is float32
+ *            rounding of q . dq and v . dv of the tokens from it to its 64-token chunk's end,
+ *            not of itself
+ *   dS0      [batch, heads, dv, dk] float32, or NULL (with S0 NULL: the gradient of the
+ *            zero state)
+ *   workspace  falcon_gated_delta_bwd_workspace_bytes(...) bytes, 16-byte aligned
+ * Here a NaN or an infinity in a token also reaches gradients that do not depend on it, of its
+ * 64-token chunk.  Rows of padding have to be finite.  Outputs and workspace overlap no other
+ * argument.  Sizes as the forward's.
+ *
  * falcon_gated_delta_decode_step - one token for serving: S [nseq, heads, dv, dk]
  * float32 updated in place, q, k [nseq, heads, dk], v [nseq, heads, dv], beta and log_a
  * [nseq, heads] (log_a or NULL), o [nseq, heads, dv] float32.  No argument may overlap
@@ -53,6 +70,14 @@ int falcon_gated_delta_fwd_chunk(int batch, int heads, int seqlen, int dk, int d
                                  const void* q, const void* k, const void* v, const float* beta,
                                  const float* log_a, const float* S0, float* o, float* S_out,
                                  void* workspace, unsigned long long workspace_bytes, void* stream);
+unsigned long long falcon_gated_delta_bwd_workspace_bytes(int batch, int heads, int seqlen, int dk,
+                                                          int dv, int dtype);
+int falcon_gated_delta_bwd_chunk(int batch, int heads, int seqlen, int dk, int dv, int dtype,
+                                 const void* q, const void* k, const void* v, const float* beta,
+                                 const float* log_a, const float* S0, const float* dO,
+                                 const float* dS_L, float* dq, float* dk_out, float* dv_out,
+                                 float* dbeta, float* dlog_a, float* dS0, void* workspace,
+                                 unsigned long long workspace_bytes, void* stream);
 int falcon_gated_delta_decode_step(int nseq, int heads, int dk, int dv, int dtype, float* S,
                                    const void* q, const void* k, const void* v, const float* beta,
                                    const float* log_a, float* o, void* stream);

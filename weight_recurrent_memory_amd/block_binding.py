@@ -28,6 +28,10 @@ def load_library():
     lib.falcon_gated_delta_fwd_workspace_bytes.argtypes = [i] * 6
     lib.falcon_gated_delta_fwd_chunk.restype = i
     lib.falcon_gated_delta_fwd_chunk.argtypes = [i] * 6 + [vp] * 9 + [ull, vp]
+    lib.falcon_gated_delta_bwd_workspace_bytes.restype = ull
+    lib.falcon_gated_delta_bwd_workspace_bytes.argtypes = [i] * 6
+    lib.falcon_gated_delta_bwd_chunk.restype = i
+    lib.falcon_gated_delta_bwd_chunk.argtypes = [i] * 6 + [vp] * 15 + [ull, vp]
     lib.falcon_gated_delta_decode_step.restype = i
     lib.falcon_gated_delta_decode_step.argtypes = [i] * 5 + [vp] * 8
     lib.falcon_rotary_in.restype = i

@@ -28,8 +28,8 @@ SOURCES = ["falcon_api.cpp", "falcon_recurrent.hip", "falcon_decode.hip", "falco
            "falcon_chunk_ip.hip", "falcon_backward.hip", "falcon_masked.hip",
            "falcon_norm.hip", "falcon_gated.hip",
            "falcon_gated_bwd.hip", "falcon_gated_decode.hip"]
-BLOCK_SOURCES = ["falcon_block_api.cpp", "falcon_delta.hip", "falcon_delta_solve.hip",
-                 "falcon_delta_decode.hip", "falcon_rotary.hip"]
+BLOCK_SOURCES = ["falcon_block_api.cpp", "falcon_delta.hip", "falcon_delta_bwd.hip",
+                 "falcon_delta_solve.hip", "falcon_delta_decode.hip", "falcon_rotary.hip"]
 ARCH = os.environ.get("FALCON_OFFLOAD_ARCH", "gfx950")
 
 

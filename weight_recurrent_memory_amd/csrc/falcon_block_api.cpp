@@ -51,6 +51,46 @@ FALCON_EXPORT int falcon_gated_delta_fwd_chunk(int batch, int heads, int seqlen,
   return finish_launch(falcon::launch_delta(a, (hipStream_t)stream));
 }
 
+FALCON_EXPORT unsigned long long falcon_gated_delta_bwd_workspace_bytes(int batch, int heads, int seqlen,
+                                                                        int dk, int dv, int dtype) {
+  size_t N, es;
+  if (check_sizes(batch, heads, seqlen, dk, dv, dtype, &N, &es) != FALCON_OK || !supported_dim(dk) ||
+      !supported_dim(dv) || !delta_sizes(batch, heads, seqlen, dk, dv))
+    return 0;
+  falcon::DeltaBwdArgs a{batch, heads, seqlen, dk, dv, dtype};
+  return (unsigned long long)falcon::delta_bwd_workspace_bytes(a);
+}
+
+FALCON_EXPORT int falcon_gated_delta_bwd_chunk(int batch, int heads, int seqlen, int dk, int dv, int dtype,
+                                               const void* q, const void* k, const void* v,
+                                               const float* beta, const float* log_a, const float* S0,
+                                               const float* dO, const float* dS_L, float* dq, float* dk_out,
+                                               float* dv_out, float* dbeta, float* dlog_a, float* dS0,
+                                               void* workspace, unsigned long long workspace_bytes,
+                                               void* stream) {
+  size_t N, es;
+  int st = check_sizes(batch, heads, seqlen, dk, dv, dtype, &N, &es);
+  if (st != FALCON_OK) return st;
+  if (!q || !k || !v || !beta || !dO || !dq || !dk_out || !dv_out || !dbeta || !workspace || (dlog_a && !log_a))
+    return FALCON_ERR_INVALID_ARG;
+  const void* ptrs[] = {q, k, v, S0, dO, dS_L, dq, dk_out, dv_out, dS0, workspace};
+  if (!all_aligned16(ptrs) || !aligned4(beta) || !aligned4(log_a) || !aligned4(dbeta) || !aligned4(dlog_a))
+    return FALCON_ERR_INVALID_ARG;
+  if (!supported_dim(dk) || !supported_dim(dv) || !delta_sizes(batch, heads, seqlen, dk, dv))
+    return FALCON_ERR_UNSUPPORTED;
+  const falcon::DeltaBwdArgs a{batch, heads, seqlen, dk, dv, dtype, q, k, v, beta, log_a, S0, dO, dS_L,
+                               dq, dk_out, dv_out, dbeta, dlog_a, dS0, workspace};
+  const size_t need = falcon::delta_bwd_workspace_bytes(a);
+  if (workspace_bytes < need) return FALCON_ERR_INVALID_ARG;
+  const size_t NH = N * heads, state = (size_t)batch * heads * dv * dk * 4;
+  const Range outs[] = {{dq, NH * dk * 4}, {dk_out, NH * dk * 4}, {dv_out, NH * dv * 4}, {dbeta, NH * 4},
+                        {dlog_a, NH * 4}, {dS0, state}, {workspace, need}};
+  const Range ins[] = {{q, NH * dk * es}, {k, NH * dk * es}, {v, NH * dv * es}, {beta, NH * 4}, {log_a, NH * 4},
+                       {S0, state}, {dO, NH * dv * 4}, {dS_L, state}};
+  if (any_overlap(outs, ins)) return FALCON_ERR_INVALID_ARG;
+  return finish_launch(falcon::launch_delta_bwd(a, (hipStream_t)stream));
+}
+
 FALCON_EXPORT int falcon_gated_delta_decode_step(int nseq, int heads, int dk, int dv, int dtype, float* S,
                                                  const void* q, const void* k, const void* v,
                                                  const float* beta, const float* log_a, float* o,

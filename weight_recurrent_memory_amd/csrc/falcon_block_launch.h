@@ -22,6 +22,27 @@ struct DeltaArgs {
 // (sizes and type count)
 size_t delta_workspace_bytes(const DeltaArgs& a);
 hipError_t launch_delta(const DeltaArgs& a, hipStream_t stream);
+struct DeltaBwdArgs {
+  int batch, heads, seqlen, ndk, ndv;
+  int dtype;
+  const void* q;
+  const void* k;
+  const void* v;
+  const float* beta;
+  const float* log_a;      // may be null
+  const float* S0;         // may be null
+  const float* dO;
+  const float* dS_L;       // may be null
+  float* dq;
+  float* dk;
+  float* dv;
+  float* dbeta;
+  float* dlog_a;           // may be null; null where log_a is
+  float* dS0;              // may be null
+  void* workspace;         // delta_bwd_workspace_bytes(...)
+};
+size_t delta_bwd_workspace_bytes(const DeltaBwdArgs& a);
+hipError_t launch_delta_bwd(const DeltaBwdArgs& a, hipStream_t stream);
 struct DeltaDecodeArgs {
   int nseq, heads, dk, dv;
   int dtype;

@@ -1,5 +1,5 @@
 // falcon_delta.hip - forward of the gated delta rule over a sequence (falcon_delta.h).
-#include "falcon_delta.h"
+#include "falcon_delta_walk.h"
 
 namespace falcon {
 namespace delta {
@@ -24,248 +24,34 @@ struct WalkArgs {
   int segs, per;           // segments of a chain, chunks of one
 };
 
-// Chunks that K and gates are in LDS before they are used.  Two where there are registers for
-// a chunk's first operands behind the chunk before it.
-template <typename T, int DK>
-constexpr int ahead() { return planes<T>() == 1 && DK <= 64 ? 2 : 1; }
-
-template <typename T, int DK>
-struct StateLds {
-  static constexpr int NP = planes<T>(), NQ = (DK + 31) / 32, R = ahead<T, DK>() + 1;
-  alignas(16) uint16_t k[R][NP][C * DK];
-  Gates gate[R];
-  alignas(16) unsigned char bad[4];
-};
 template <typename T, int DK, int ND>
 struct WalkLds : StateLds<T, DK> {
   alignas(16) uint4 s[2][ND][StateLds<T, DK>::NQ][3][64];     // S at the chunk's start, as operands
   alignas(16) uint4 u[2][ND][2][3][64];
 };
 
-// S^T: 16 value rows, columns of keys in tiles of 16.
-template <int DK>
-struct StateT {
-  static constexpr int NK = DK / 16, NQ = (DK + 31) / 32;
-  floatx4 t[NK];
-  __device__ __forceinline__ void load(const float* S) {       // rows of the 16, or null
-    const int m = threadIdx.x & 15, g = (threadIdx.x & 63) >> 4;
-#pragma unroll
-    for (int j = 0; j < NK; ++j)
-      t[j] = S ? *reinterpret_cast<const floatx4*>(S + m * DK + 16 * j + 4 * g) : floatx4{0.f, 0.f, 0.f, 0.f};
-  }
-  __device__ __forceinline__ void unit(int row0) {             // rows of the unit matrix
-    const int m = threadIdx.x & 15, g = (threadIdx.x & 63) >> 4;
-#pragma unroll
-    for (int j = 0; j < NK; ++j)
-#pragma unroll
-      for (int r = 0; r < 4; ++r) t[j][r] = row0 + m == 16 * j + 4 * g + r ? 1.0f : 0.0f;
-  }
-  __device__ __forceinline__ void store(float* S) const {
-    const int m = threadIdx.x & 15, g = (threadIdx.x & 63) >> 4;
-#pragma unroll
-    for (int j = 0; j < NK; ++j) *reinterpret_cast<floatx4*>(S + m * DK + 16 * j + 4 * g) = t[j];
-  }
-  __device__ __forceinline__ void store_transposed(float* S, int row0) const {
-    const int m = threadIdx.x & 15, g = (threadIdx.x & 63) >> 4;
-#pragma unroll
-    for (int j = 0; j < NK; ++j)
-#pragma unroll
-      for (int r = 0; r < 4; ++r) S[(16 * j + 4 * g + r) * DK + row0 + m] = t[j][r];
-  }
-  __device__ __forceinline__ void frag(int i, bf16x8 (&f)[3]) const {
-    const floatx4 zero = {0.f, 0.f, 0.f, 0.f};
-    if constexpr (DK == 16) frag_pair(t[0], zero, f);
-    else frag_pair(t[2 * i], t[2 * i + 1], f);
-  }
-  __device__ __forceinline__ bool finite() const {
-    float s = 0.0f;
-#pragma unroll
-    for (int j = 0; j < NK; ++j) s += (t[j].x + t[j].y) + (t[j].z + t[j].w);
-    return __builtin_isfinite(s);
-  }
-};
-
-// The wave that owns 16 value rows: S through the chunks of a segment.
-template <typename T, int DK>
-struct Walker {
-  static constexpr int NP = planes<T>(), NQ = (DK + 31) / 32, NK = DK / 16;
-  StateT<DK> S;
-  bf16x8 T_[kFrags][3];
-  float v[16];
-
-  __device__ __forceinline__ void load_T(const uint4* p) {
-    const int lane = threadIdx.x & 63;
-#pragma unroll
-    for (int f = 0; f < kFrags; ++f)
-#pragma unroll
-      for (int n = 0; n < 3; ++n) T_[f][n] = __builtin_bit_cast(bf16x8, p[(f * 3 + n) * 64 + lane]);
-  }
-  // v: the sequence's rows from the chunk's first token on; col: of the 16 rows' first
-  __device__ __forceinline__ void load_v(const T* p, long rows, int nv, int col) {
-    const int m = threadIdx.x & 15, g = (threadIdx.x & 63) >> 4;
-    const Window w(p, rows, nv, 0);
-#pragma unroll
-    for (int i = 0; i < 4; ++i)
-#pragma unroll
-      for (int r = 0; r < 4; ++r) v[4 * i + r] = load_one(w, (16 * i + 4 * g + r) * nv + col + m, T());
-  }
-
-  static constexpr bool kAhead = ahead<T, DK>() > 1;
-  bf16x8 kf[kAhead ? NQ : 1][4][NP];      // K's rows
-
-  __device__ __forceinline__ void load_k_step(const uint16_t* k, int n, bf16x8 (&f)[4][NP]) {
-#pragma unroll
-    for (int i = 0; i < 4; ++i) pair_frag<NP, DK>(k, 16 * i + (threadIdx.x & 15), n, f[i]);
-  }
-  __device__ __forceinline__ void load_k(const uint16_t* k) {
-    if constexpr (kAhead) {
-#pragma unroll
-      for (int n = 0; n < NQ; ++n) load_k_step(k, n, kf[n]);
-    }
-  }
-
-  // One chunk; store(which, index, plane, fragment) gets S's and U's operands.  load() is
-  // called once v and T are used, last() behind everything.
-  template <class Load, class Last, class Store>
-  __device__ __forceinline__ void chunk(const uint16_t* k, const Gates& gt, Load&& load, Last&& last, Store&& store) {
-    const int g = (threadIdx.x & 63) >> 4;
-    const floatx4 zero = {0.f, 0.f, 0.f, 0.f};
-    // K S^T
-    floatx4 x[4] = {zero, zero, zero, zero}, b[4], be[4];
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      b[i] = *reinterpret_cast<const floatx4*>(gt.b + 16 * i + 4 * g);
-      be[i] = *reinterpret_cast<const floatx4*>(gt.be + 16 * i + 4 * g);
-    }
-#pragma unroll
-    for (int n = 0; n < NQ; ++n) {
-      bf16x8 s[3];
-      S.frag(n, s);
-#pragma unroll
-      for (int p = 0; p < 3; ++p) store(0, n, p, s[p]);
-      bf16x8(&kn)[4][NP] = kf[kAhead ? n : 0];
-      if (!kAhead) load_k_step(k, n, kn);
-#pragma unroll
-      for (int p = 0; p < NP; ++p)
-#pragma unroll
-        for (int r = 0; p + r < 3; ++r)
-#pragma unroll
-          for (int i = 0; i < 4; ++i) x[i] = mfma16(kn[i][p], s[r], x[i]);
-    }
-    // X = b v - b e K S^T, then U = T X
-    bf16x8 xf[3];
-    floatx4 u[4] = {zero, zero, zero, zero};
-#pragma unroll
-    for (int j = 0; j < 2; ++j) {
-#pragma unroll
-      for (int i = 2 * j; i < 2 * j + 2; ++i)
-#pragma unroll
-        for (int r = 0; r < 4; ++r) x[i][r] = b[i][r] * v[4 * i + r] - be[i][r] * x[i][r];
-      frag_pair(x[2 * j], x[2 * j + 1], xf);
-#pragma unroll
-      for (int p = 0; p < 3; ++p)
-#pragma unroll
-        for (int r = 0; p + r < 3; ++r)
-#pragma unroll
-          for (int i = 2 * j; i < 4; ++i) u[i] = mfma16(T_[frag_of(i, j)][p], xf[r], u[i]);
-    }
-    load();
-    // S <- d S + (w U)^T K
-    bf16x8 f[3];
-    floatx4 w[4];
-#pragma unroll
-    for (int i = 0; i < 4; ++i) w[i] = *reinterpret_cast<const floatx4*>(gt.w + 16 * i + 4 * g);
-    const float d = gt.d;
-#pragma unroll
-    for (int j = 0; j < NK; ++j) S.t[j] *= d;
-#pragma unroll
-    for (int n = 0; n < 2; ++n) {
-      frag_pair(u[2 * n] * w[2 * n], u[2 * n + 1] * w[2 * n + 1], f);
-      constexpr int J = NK < 4 ? NK : 4;
-#pragma unroll
-      for (int j0 = 0; j0 < NK; j0 += J) {
-        bf16x8 kt[J][NP];
-#pragma unroll
-        for (int j = 0; j < J; ++j) pair_frag_t<NP, DK>(k, n, j0 + j, kt[j]);
-#pragma unroll
-        for (int p = 0; p < NP; ++p)
-#pragma unroll
-          for (int r = 0; p + r < 3; ++r)
-#pragma unroll
-            for (int j = 0; j < J; ++j) S.t[j0 + j] = mfma16(kt[j][p], f[r], S.t[j0 + j]);
-      }
-      frag_pair(u[2 * n], u[2 * n + 1], f);
-#pragma unroll
-      for (int p = 0; p < 3; ++p) store(1, n, p, f[p]);
-    }
-    last();
-  }
-};
-
-// K rows of a chunk on their way to LDS, by N waves.
-template <typename T, int DK, int NTH>
-struct StageK {
-  static constexpr int NP = planes<T>(), G = DK / 8, UNITS = C * G, N = (UNITS + NTH - 1) / NTH;
-  Raw<T> r[N];
-  __device__ __forceinline__ void load(const Window& w, int t) {
-#pragma unroll
-    for (int i = 0; i < N; ++i) {
-      const int u = t + i * NTH;
-      r[i].load(w, UNITS % NTH == 0 || u < UNITS ? 8 * u * (int)sizeof(T) : kNowhere);
-    }
-  }
-  __device__ __forceinline__ void store(uint16_t* k, int t) const {
-#pragma unroll
-    for (int i = 0; i < N; ++i) {
-      const int u = t + i * NTH;
-      if (UNITS % NTH != 0 && u >= UNITS) continue;
-      uint4 a[NP];
-      r[i].split(a);
-#pragma unroll
-      for (int p = 0; p < NP; ++p) *reinterpret_cast<uint4*>(k + p * C * DK + at<DK>(u / G, 8 * (u % G))) = a[p];
-    }
-  }
-};
-
-// Output waves of a workgroup of ND state waves (ND = 4: no outputs, two that read K), and the token tiles of output wave w.  (Waves
+// Output waves of a workgroup of ND state waves, and the token tiles of output wave w.  (Waves
 // go to the compute unit's four SIMDs in turn: with ND = 2 the tiles of most scores get the
 // SIMDs without a state wave.)
-constexpr int out_waves(int nd) { return nd < 4 ? 2 * nd : 2; }
+constexpr int out_waves(int nd) { return 2 * nd; }
 template <int ND>
 __device__ __forceinline__ constexpr int tile_of(int w, int n) {
   return ND == 1 ? (n == 0 ? w : 3 - w) : w < 2 ? 3 - w : w - 2;
 }
 
-// The other waves: K and gates of the next chunk, and the outputs of the one before.
-template <typename T, int DK, int ND, bool OUT, int ow>
-__device__ __forceinline__ void helper(const WalkArgs& a, WalkLds<T, DK, ND>& lds, long chain, long c0, int n,
-                                       int row0) {
+// The other waves: K and gates ahead, and the outputs of the chunk before.
+template <typename T, int DK, int ND, int ow>
+__device__ __forceinline__ void outputs(const WalkArgs& a, WalkLds<T, DK, ND>& lds, long chain, long c0, int n,
+                                        int row0) {
   constexpr int NP = planes<T>(), NQ = (DK + 31) / 32, NTO = 64 * out_waves(ND), NT_ = 4 / out_waves(ND);
   const int lane = threadIdx.x & 63, m = lane & 15, g = lane >> 4;
   const long len = a.seqlen, left = len - c0 * C;
-  const T* k = static_cast<const T*>(a.k) + (chain * len + c0 * C) * DK;
-  const int ot = threadIdx.x - 64 * ND;
-  const float* la = a.log_a ? a.log_a + chain * len + c0 * C : nullptr;
-  const float* be = a.beta + chain * len + c0 * C;
   const T* q = static_cast<const T*>(a.q) + (chain * len + c0 * C) * DK;
   float* o = a.o + (chain * len + c0 * C) * a.nv + row0;
-  constexpr int D = ahead<T, DK>(), R = D + 1;
-  StageK<T, DK, NTO> sk;
-  GateLoad gl;
-  auto load = [&](int c) {
-    sk.load(Window(k + (long)c * C * DK, left - (long)c * C, DK, 0), ot);
-    gl.load(la, be, (long)c * C, left);
-  };
-  auto store = [&](int c) {
-    sk.store(lds.k[c % R][0], ot);
-    if (ow == 0) gl.store(lds.gate[c % R]);
-  };
-#pragma unroll
-  for (int c = 0; c < D; ++c) {
-    if (c >= n) break;
-    load(c);
-    store(c);
-  }
+  Keys<T, DK, NTO, false> keys(lds, static_cast<const T*>(a.k) + (chain * len + c0 * C) * DK,
+                               a.log_a ? a.log_a + chain * len + c0 * C : nullptr, a.beta + chain * len + c0 * C, left,
+                               n, threadIdx.x - 64 * ND);
+  constexpr int D = keys.D, R = keys.R;
   bf16x8 qf[NT_][NQ][NP], pf[NT_][2][3];
   float ev[NT_];
   PairRow<T, DK> qr[NT_];
@@ -274,94 +60,92 @@ __device__ __forceinline__ void helper(const WalkArgs& a, WalkLds<T, DK, ND>& ld
 #pragma unroll
     for (int j = 0; j < NT_; ++j) qr[j].load(wq, 16 * tile_of<ND>(ow, j) + m);
   };
-  if (OUT) load_q(0);
+  load_q(0);
   for (int c = 0; c <= n; ++c) {
     __syncthreads();
-    if (c + D < n) load(c + D);
-    if (OUT) {
-      if (c > 0) {
-        const int b = (c - 1) & 1;
+    if (c + D < n) keys.load(c + D);
+    if (c > 0) {
+      const int b = (c - 1) & 1;
 #pragma unroll
-        for (int z = 0; z < ND; ++z) {
-          floatx4 acc[NT_];
+      for (int z = 0; z < ND; ++z) {
+        floatx4 acc[NT_];
 #pragma unroll
-          for (int j = 0; j < NT_; ++j) acc[j] = floatx4{0.f, 0.f, 0.f, 0.f};
+        for (int j = 0; j < NT_; ++j) acc[j] = floatx4{0.f, 0.f, 0.f, 0.f};
 #pragma unroll
-          for (int i = 0; i < NQ; ++i) {
-            bf16x8 s[3];
+        for (int i = 0; i < NQ; ++i) {
+          bf16x8 s[3];
 #pragma unroll
-            for (int p = 0; p < 3; ++p) s[p] = __builtin_bit_cast(bf16x8, lds.s[b][z][i][p][lane]);
+          for (int p = 0; p < 3; ++p) s[p] = __builtin_bit_cast(bf16x8, lds.s[b][z][i][p][lane]);
 #pragma unroll
-            for (int p = 0; p < 3; ++p)
+          for (int p = 0; p < 3; ++p)
 #pragma unroll
-              for (int r = 0; r < NP; ++r)
-                if (p + r < 3) {
+            for (int r = 0; r < NP; ++r)
+              if (p + r < 3) {
 #pragma unroll
-                  for (int j = 0; j < NT_; ++j) acc[j] = mfma16(s[p], qf[j][i][r], acc[j]);
-                }
-          }
-#pragma unroll
-          for (int j = 0; j < NT_; ++j) acc[j] *= ev[j];
-#pragma unroll
-          for (int i = 0; i < 2; ++i) {
-            bf16x8 u[3];
-#pragma unroll
-            for (int p = 0; p < 3; ++p) u[p] = __builtin_bit_cast(bf16x8, lds.u[b][z][i][p][lane]);
-#pragma unroll
-            for (int p = 0; p < 3; ++p)
-#pragma unroll
-              for (int r = 0; p + r < 3; ++r)
-#pragma unroll
-                for (int j = 0; j < NT_; ++j)
-                  if (i == 0 || tile_of<ND>(ow, j) >= 2) acc[j] = mfma16(u[p], pf[j][i][r], acc[j]);
-          }
-#pragma unroll
-          for (int j = 0; j < NT_; ++j) {
-            const long t = (long)(c - 1) * C + 16 * tile_of<ND>(ow, j) + m;
-            if (t < left)
-              __builtin_nontemporal_store(acc[j], reinterpret_cast<floatx4*>(o + t * a.nv + 16 * z + 4 * g));
-          }
+                for (int j = 0; j < NT_; ++j) acc[j] = mfma16(s[p], qf[j][i][r], acc[j]);
+              }
         }
-      }
-      if (c < n) {
-        // this chunk's scores, decayed: operands with rows t and slots s
-        const uint16_t* kl = lds.k[c % R][0];
-        const Gates& gt = lds.gate[c % R];
+#pragma unroll
+        for (int j = 0; j < NT_; ++j) acc[j] *= ev[j];
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+          bf16x8 u[3];
+#pragma unroll
+          for (int p = 0; p < 3; ++p) u[p] = __builtin_bit_cast(bf16x8, lds.u[b][z][i][p][lane]);
+#pragma unroll
+          for (int p = 0; p < 3; ++p)
+#pragma unroll
+            for (int r = 0; p + r < 3; ++r)
+#pragma unroll
+              for (int j = 0; j < NT_; ++j)
+                if (i == 0 || tile_of<ND>(ow, j) >= 2) acc[j] = mfma16(u[p], pf[j][i][r], acc[j]);
+        }
 #pragma unroll
         for (int j = 0; j < NT_; ++j) {
-          const int ti = tile_of<ND>(ow, j);
-#pragma unroll
-          for (int i = 0; i < NQ; ++i) qr[j].frag(i, qf[j][i]);
-          ev[j] = gt.e[16 * ti + m];
-          const float2 Gt = gt.g[16 * ti + m];
-#pragma unroll
-          for (int h = 0; h < 2; ++h) {
-            if (2 * h > ti) continue;
-            floatx4 p[2];
-#pragma unroll
-            for (int z = 0; z < 2; ++z) {
-              const int si = 2 * h + z;
-              p[z] = floatx4{0.f, 0.f, 0.f, 0.f};
-              if (si > ti) continue;
-#pragma unroll
-              for (int i = 0; i < NQ; ++i) {
-                bf16x8 kf[NP];
-                pair_frag<NP, DK>(kl, 16 * si + m, i, kf);
-                mma<NP, NP>(kf, qf[j][i], p[z]);
-              }
-#pragma unroll
-              for (int r = 0; r < 4; ++r) {
-                const float x = p[z][r] * decay(Gt, gt.g[16 * si + 4 * g + r]);
-                p[z][r] = (si < ti || 4 * g + r <= m) ? x : 0.0f;
-              }
-            }
-            frag_pair(p[0], p[1], pf[j][h]);
-          }
+          const long t = (long)(c - 1) * C + 16 * tile_of<ND>(ow, j) + m;
+          if (t < left)
+            __builtin_nontemporal_store(acc[j], reinterpret_cast<floatx4*>(o + t * a.nv + 16 * z + 4 * g));
         }
-        if (c + 1 < n) load_q(c + 1);
       }
     }
-    if (c + D < n) store(c + D);
+    if (c < n) {
+      // this chunk's scores, decayed: operands with rows t and slots s
+      const uint16_t* kl = lds.k[c % R][0];
+      const Gates& gt = lds.gate[c % R];
+#pragma unroll
+      for (int j = 0; j < NT_; ++j) {
+        const int ti = tile_of<ND>(ow, j);
+#pragma unroll
+        for (int i = 0; i < NQ; ++i) qr[j].frag(i, qf[j][i]);
+        ev[j] = gt.e[16 * ti + m];
+        const float2 Gt = gt.g[16 * ti + m];
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+          if (2 * h > ti) continue;
+          floatx4 p[2];
+#pragma unroll
+          for (int z = 0; z < 2; ++z) {
+            const int si = 2 * h + z;
+            p[z] = floatx4{0.f, 0.f, 0.f, 0.f};
+            if (si > ti) continue;
+#pragma unroll
+            for (int i = 0; i < NQ; ++i) {
+              bf16x8 kf[NP];
+              pair_frag<NP, DK>(kl, 16 * si + m, i, kf);
+              mma<NP, NP>(kf, qf[j][i], p[z]);
+            }
+#pragma unroll
+            for (int r = 0; r < 4; ++r) {
+              const float x = p[z][r] * decay(Gt, gt.g[16 * si + 4 * g + r]);
+              p[z][r] = (si < ti || 4 * g + r <= m) ? x : 0.0f;
+            }
+          }
+          frag_pair(p[0], p[1], pf[j][h]);
+        }
+      }
+      if (c + 1 < n) load_q(c + 1);
+    }
+    if (c + D < n) keys.store(lds, c + D);
   }
 }
 
@@ -422,7 +206,7 @@ __device__ __forceinline__ WalkArgs args_again() {
   return __builtin_bit_cast(WalkArgs, words);
 }
 
-constexpr int threads_of(int nd) { return 64 * (nd + out_waves(nd)); }
+constexpr int threads_of(int nd, bool out) { return 64 * (nd + (out ? out_waves(nd) : kKeyWaves)); }
 // Waves a SIMD that registers are held to: two, but where that spills.
 template <typename T, int DK, int ND, bool OUT>
 constexpr int waves_of() { return OUT && planes<T>() == 3 && DK == 128 ? 1 : 2; }
@@ -430,9 +214,9 @@ constexpr int waves_of() { return OUT && planes<T>() == 3 && DK == 128 ? 1 : 2; 
 // OUT: the main walk; else a segment's own write (blocks of value rows) and the matrix it
 // multiplies its start's rows with (blocks of unit rows behind them).
 template <typename T, int DK, int ND, bool OUT>
-__global__ __launch_bounds__(threads_of(ND), (waves_of<T, DK, ND, OUT>())) void walk_kernel(WalkArgs a) {
+__global__ __launch_bounds__(threads_of(ND, OUT), (waves_of<T, DK, ND, OUT>())) void walk_kernel(WalkArgs a) {
   extern __shared__ __align__(16) unsigned char smem[];
-  using L = WalkLds<T, DK, ND>;
+  using L = typename std::conditional<OUT, WalkLds<T, DK, ND>, StateLds<T, DK>>::type;
   constexpr int DZ = 16 * ND;
   L& lds = *reinterpret_cast<L*>(smem);
   const int vblocks = a.nv / DZ, blocks = OUT ? vblocks : vblocks + (DK + DZ - 1) / DZ;
@@ -470,7 +254,7 @@ __global__ __launch_bounds__(threads_of(ND), (waves_of<T, DK, ND, OUT>())) void 
       if (c == 0) w.load_k(lds.k[0][0]);
       // (what is behind the last chunk is loaded in its own place: no branch holds registers)
       const int next = c + 1 < n ? c + 1 : c;
-      w.chunk(lds.k[c % L::R][0], lds.gate[c % L::R],
+      w.template chunk<OUT>(lds.k[c % L::R][0], lds.gate[c % L::R],
               [&] {
                 // (loads come back in order: the one needed first is issued first)
                 load_v(next);
@@ -478,13 +262,15 @@ __global__ __launch_bounds__(threads_of(ND), (waves_of<T, DK, ND, OUT>())) void 
               },
               [&] { w.load_k(lds.k[next % L::R][0]); },
               [&](int which, int i, int p, const bf16x8& f) {
-                if (!OUT) return;
-                uint4* to = which == 0 ? lds.s[c & 1][wave][i][p] : lds.u[c & 1][wave][i][p];
-                to[lane] = __builtin_bit_cast(uint4, f);
-              });
+                if constexpr (OUT) {
+                  uint4* to = which == 0 ? lds.s[c & 1][wave][i][p] : lds.u[c & 1][wave][i][p];
+                  to[lane] = __builtin_bit_cast(uint4, f);
+                }
+              },
+              [](const floatx4 (&)[4]) {});
     }
     __syncthreads();
-    if (OUT) {
+    if constexpr (OUT) {
       const bool bad = __any(!w.S.finite());
       if (lane == 0) lds.bad[wave] = bad;
       if (!bad && a.S_out && seg == a.segs - 1) w.S.store(a.S_out + chain * state + (long)row * DK);
@@ -495,13 +281,19 @@ __global__ __launch_bounds__(threads_of(ND), (waves_of<T, DK, ND, OUT>())) void 
       w.S.store(a.starts + (chain * a.segs + seg + 1) * state + (long)row * DK);
     }
   } else {
-    if (wave == ND) helper<T, DK, ND, OUT, 0>(a, lds, chain, c0, n, row0);
-    else if (wave == ND + 1) helper<T, DK, ND, OUT, 1>(a, lds, chain, c0, n, row0);
-    else if (wave == ND + 2) helper<T, DK, ND, OUT, 2>(a, lds, chain, c0, n, row0);
-    else helper<T, DK, ND, OUT, 3>(a, lds, chain, c0, n, row0);
-    if (OUT) __syncthreads();
+    if constexpr (OUT) {
+      if (wave == ND) outputs<T, DK, ND, 0>(a, lds, chain, c0, n, row0);
+      else if (wave == ND + 1) outputs<T, DK, ND, 1>(a, lds, chain, c0, n, row0);
+      else if (wave == ND + 2) outputs<T, DK, ND, 2>(a, lds, chain, c0, n, row0);
+      else outputs<T, DK, ND, 3>(a, lds, chain, c0, n, row0);
+      __syncthreads();
+    } else {
+      keys_only<T, DK, false>(lds, static_cast<const T*>(a.k) + (chain * len + c0 * C) * DK,
+                              a.log_a ? a.log_a + chain * len + c0 * C : nullptr, a.beta + chain * len + c0 * C, left,
+                              n, threadIdx.x - 64 * ND);
+    }
   }
-  if (OUT) {
+  if constexpr (OUT) {
     bool bad = false;
 #pragma unroll
     for (int i = 0; i < ND; ++i) bad |= lds.bad[i] != 0;
@@ -612,7 +404,7 @@ hipError_t go(const WalkArgs& a, hipStream_t stream) {
   if (e != hipSuccess) return e;
   constexpr int DZ = 16 * ND;
   const int blocks = OUT ? a.nv / DZ : a.nv / DZ + (DK + DZ - 1) / DZ;
-  hipLaunchKernelGGL(kernel, dim3(grid_of(blocks, a.chains * (OUT ? a.segs : a.segs - 1))), dim3(threads_of(ND)), bytes,
+  hipLaunchKernelGGL(kernel, dim3(grid_of(blocks, a.chains * (OUT ? a.segs : a.segs - 1))), dim3(threads_of(ND, OUT)), bytes,
                      stream, a);
   return hipGetLastError();
 }

@@ -42,6 +42,38 @@ def gated_delta_fwd_chunk(q, k, v, beta, log_a=None, *, S0=None, out=None, S_out
     return (out, S_out) if return_state else out
 
 
+def gated_delta_bwd_chunk(q, k, v, beta, log_a, dO, *, S0=None, dS_L=None, stream=None,
+                          workspace="auto"):
+    """Gradients of sum <dO, o> + <dS_L, S_L>: a dict of float32 tensors dq, dk, dv, dbeta,
+    and dlog_a / dS0 when log_a / S0 are given.  dO [B,H,L,dv] and dS_L [B,H,dv,dk] float32.
+    workspace: "auto", or a device tensor of falcon_gated_delta_bwd_workspace_bytes(...)."""
+    import torch
+    lib = _bb.load_library()
+    sizes = B, H, L, dk, dv, dcode = _sizes(torch, q, k, v)
+    dev, f32 = q.device, torch.float32
+    qp, kp, vp, lp, sp = _inputs(torch, q, k, v, log_a, S0, sizes)
+    if beta is None or dO is None:
+        raise ValueError("beta and dO must be given")
+    bp = _b._expect(torch, "beta", beta, (B, H, L), f32, dev)
+    dOp = _b._expect(torch, "dO", dO, (B, H, L, dv), f32, dev)
+    dSp = _b._expect(torch, "dS_L", dS_L, (B, H, dv, dk), f32, dev)
+    with _b._guard(torch, dev, stream):
+        res = dict(dq=q.new_empty((B, H, L, dk), dtype=f32), dk=q.new_empty((B, H, L, dk), dtype=f32),
+                   dv=q.new_empty((B, H, L, dv), dtype=f32), dbeta=q.new_empty((B, H, L), dtype=f32))
+        if log_a is not None:
+            res["dlog_a"] = q.new_empty((B, H, L), dtype=f32)
+        if S0 is not None:
+            res["dS0"] = q.new_empty((B, H, dv, dk), dtype=f32)
+        need = lib.falcon_gated_delta_bwd_workspace_bytes(*sizes)
+        ws, wp, wb = _workspace(torch, workspace, max(need, 16), dev)
+        status = lib.falcon_gated_delta_bwd_chunk(
+            *sizes, qp, kp, vp, bp, lp, sp, dOp, dSp, res["dq"].data_ptr(), res["dk"].data_ptr(),
+            res["dv"].data_ptr(), res["dbeta"].data_ptr(), _b._address(res.get("dlog_a")),
+            _b._address(res.get("dS0")), wp, wb, _b._raw_stream(torch, dev, stream))
+    _bb.check("falcon_gated_delta_bwd_chunk", status)
+    return res
+
+
 def gated_delta_decode_step(S, q, k, v, beta, log_a=None, *, out=None, stream=None):
     """One token: S [N,H,dv,dk] float32 is updated in place, returns o [N,H,dv] float32.
     q, k [N,H,dk], v [N,H,dv] bfloat16 or float32; beta and log_a [N,H] float32, log_a
