@@ -187,12 +187,7 @@ struct BackWalker {
                                         Values&& values) {
     const int g = (threadIdx.x & 63) >> 4, m = threadIdx.x & 15;
     const floatx4 zero = {0.f, 0.f, 0.f, 0.f};
-    floatx4 x[4] = {zero, zero, zero, zero}, w[4], be[4];
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      w[i] = *reinterpret_cast<const floatx4*>(gt.w + 16 * i + 4 * g);
-      be[i] = *reinterpret_cast<const floatx4*>(gt.be + 16 * i + 4 * g);
-    }
+    floatx4 x[4] = {zero, zero, zero, zero};
     // K R^T
 #pragma unroll
     for (int n = 0; n < NQ; ++n) {
@@ -213,9 +208,11 @@ struct BackWalker {
 #pragma unroll
     for (int j = 0; j < 2; ++j) {
 #pragma unroll
-      for (int i = 2 * j; i < 2 * j + 2; ++i)
+      for (int i = 2 * j; i < 2 * j + 2; ++i) {
+        const floatx4 w = *reinterpret_cast<const floatx4*>(gt.w + 16 * i + 4 * g);
 #pragma unroll
-        for (int r = 0; r < 4; ++r) x[i][r] = h[i][r] + w[i][r] * x[i][r];
+        for (int r = 0; r < 4; ++r) x[i][r] = h[i][r] + w[r] * x[i][r];
+      }
       frag_pair(x[2 * j], x[2 * j + 1], f);
 #pragma unroll
       for (int p = 0; p < 3; ++p)
@@ -224,7 +221,10 @@ struct BackWalker {
 #pragma unroll
           for (int i = 0; i < 2 * j + 2; ++i) u[i] = mfma16(T_[frag_of(3 - i, 1 - j)][p], f[r], u[i]);
     }
+    // (keeps the next part's reads in that part: registers)
+    __builtin_amdgcn_sched_barrier(0);
     load();
+    values(u);
     // R <- d R + G - (b e du)^T K
     const float d = gt.d;
 #pragma unroll
@@ -234,7 +234,9 @@ struct BackWalker {
     load2();
 #pragma unroll
     for (int n = 0; n < 2; ++n) {
-      frag_pair(-be[2 * n] * u[2 * n], -be[2 * n + 1] * u[2 * n + 1], f);
+      const floatx4 b0 = *reinterpret_cast<const floatx4*>(gt.be + 32 * n + 4 * g);
+      const floatx4 b1 = *reinterpret_cast<const floatx4*>(gt.be + 32 * n + 16 + 4 * g);
+      frag_pair(-b0 * u[2 * n], -b1 * u[2 * n + 1], f);
       constexpr int J = NK < 4 ? NK : 4;
 #pragma unroll
       for (int j0 = 0; j0 < NK; j0 += J) {
@@ -249,19 +251,21 @@ struct BackWalker {
             for (int j = 0; j < J; ++j) R.t[j0 + j] = mfma16(kt[j][p], f[r], R.t[j0 + j]);
       }
     }
-    values(u);
   }
 };
 
-// u or du of a chunk, 16 value columns from `p` on.
-__device__ __forceinline__ void store_values(float* p, int nv, long left, const floatx4 (&u)[4]) {
+// u or du of a chunk's tokens (p: the first one's row), 16 value columns from `col` on; rows
+// behind the last token are outside of the window.
+__device__ __forceinline__ void store_values(const float* p, int nv, int col, long left, const floatx4 (&u)[4]) {
   const int g = (threadIdx.x & 63) >> 4, m = threadIdx.x & 15;
+  const Window w(p, left, nv, 0);
+  const int first = (4 * g * nv + col + m) * 4;
 #pragma unroll
   for (int i = 0; i < 4; ++i)
 #pragma unroll
     for (int r = 0; r < 4; ++r) {
-      const int t = 16 * i + 4 * g + r;
-      if (t < left) p[(long)t * nv + m] = u[i][r];
+      const float x = u[i][r];         // (a bit cast of a vector's element takes the first one's bits)
+      __builtin_amdgcn_raw_buffer_store_b32(__float_as_uint(x), w.r, first + (16 * i + r) * nv * 4, 0, 0);
     }
 }
 
@@ -295,7 +299,7 @@ __global__ __launch_bounds__(64 * (ND + kKeyWaves), 2) void walks_kernel(BwdArgs
     const T* v = static_cast<const T*>(a.v) + chain * len * a.nv;
     const uint4* Tp = a.T + chain * n * kT;
     float* S = a.S + chain * (n + 1) * state + at;
-    float* U = a.U + chain * len * a.nv + row;
+    const float* U = a.U + chain * len * a.nv;
     w.S.load(a.S0 ? a.S0 + chain * state + at : nullptr);
     w.load_T(Tp);
     w.load_v(v, len, a.nv, row);
@@ -310,7 +314,7 @@ __global__ __launch_bounds__(64 * (ND + kKeyWaves), 2) void walks_kernel(BwdArgs
                 w.load_T(Tp + (long)next * kT);
               },
               [&] { w.load_k(lds.k[next % L::R][0]); }, [](int, int, int, const bf16x8&) {},
-              [&](const floatx4 (&u)[4]) { store_values(U + (long)c * C * a.nv, a.nv, len - (long)c * C, u); });
+              [&](const floatx4 (&u)[4]) { store_values(U + (long)c * C * a.nv, a.nv, row, len - (long)c * C, u); });
     }
     __syncthreads();
     w.S.store(S + n * state);
@@ -322,7 +326,7 @@ __global__ __launch_bounds__(64 * (ND + kKeyWaves), 2) void walks_kernel(BwdArgs
   const float4* H = a.H + (chain * n * tiles + z) * 4 * 64;
   const float4* G = a.G + (chain * n * tiles + z) * NK * 64;
   float* R = a.R + chain * n * state + at;
-  float* du = a.dv + chain * len * a.nv + row;
+  const float* du = a.dv + chain * len * a.nv;
   w.R.load(a.dS_L ? a.dS_L + chain * state + at : nullptr);
   w.load_h(H + (long)(n - 1) * tiles * 4 * 64);
   w.load_T(Tp + (long)(n - 1) * kT);
@@ -337,7 +341,7 @@ __global__ __launch_bounds__(64 * (ND + kKeyWaves), 2) void walks_kernel(BwdArgs
               w.load_T(Tp + (long)next * kT);
             },
             [&] { w.load_G(G + (long)next * tiles * NK * 64); },
-            [&](const floatx4 (&u)[4]) { store_values(du + (long)c * C * a.nv, a.nv, len - (long)c * C, u); });
+            [&](const floatx4 (&u)[4]) { store_values(du + (long)c * C * a.nv, a.nv, row, len - (long)c * C, u); });
   }
   __syncthreads();
   if (a.dS0) w.R.store(a.dS0 + chain * state + at);
@@ -366,6 +370,15 @@ struct OutLds {
   alignas(16) double x[4];
 };
 
+// Offset of a slice's row and 16-byte group in LDS: rows of 64 bytes, so rows 4 apart meet in
+// their banks; the groups are XORed by that, and 16 rows' reads of one group fall apart.
+__device__ __forceinline__ int slice_at(int row, int group) { return row * kSlice + ((group ^ ((row >> 2) & 3)) << 3); }
+__device__ __forceinline__ void slice_frag(const uint16_t* p, int row, bf16x8 (&f)[3]) {
+  const int g = (threadIdx.x & 63) >> 4;
+#pragma unroll
+  for (int n = 0; n < 3; ++n) f[n] = frag_bf16(p + n * C * kSlice + slice_at(row, g));
+}
+
 // 64 rows of kSlice columns of a [token][nv] array, 8 of a row a thread.
 struct StageValues {
   Raw<float> r;
@@ -378,7 +391,7 @@ struct StageValues {
     r.split(f);
 #pragma unroll
     for (int n = 0; n < 3; ++n)
-      *reinterpret_cast<uint4*>(p + n * C * kSlice + at<kSlice>(threadIdx.x >> 2, 8 * (threadIdx.x & 3))) = f[n];
+      *reinterpret_cast<uint4*>(p + n * C * kSlice + slice_at(threadIdx.x >> 2, threadIdx.x & 3)) = f[n];
   }
 };
 // kSlice rows of a state.
@@ -421,7 +434,7 @@ struct StageState {
 
 // One chunk; wave w owns tokens 16 w.. (as columns m of its results).
 template <typename T, int DK>
-__global__ __launch_bounds__(256) void outputs_kernel(BwdArgs a, int chunks) {
+__global__ __launch_bounds__(256, (DK <= 64 ? 2 : 1)) void outputs_kernel(BwdArgs a, int chunks) {
   extern __shared__ __align__(16) unsigned char smem[];
   constexpr int NP = planes<T>(), NK = DK / 16;
   OutLds<T, DK>& lds = *reinterpret_cast<OutLds<T, DK>*>(smem);
@@ -464,6 +477,9 @@ __global__ __launch_bounds__(256) void outputs_kernel(BwdArgs a, int chunks) {
   for (int j = 0; j < 4; ++j) Z[j] = W[j] = zero;
 #pragma unroll
   for (int j = 0; j < NK; ++j) dq[j] = y[j] = dk[j] = zero;
+  StageK<T, DK, 256> sk, sq;
+  const Window wk(static_cast<const T*>(a.k) + row * DK, left, DK, 0),
+      wq(static_cast<const T*>(a.q) + row * DK, left, DK, 0);
   float duv = 0.0f;                  // of token threadIdx.x / 4: du . v over this thread's columns
   double X = 0.0;
   for (int col = 0; col < a.nv; col += kSlice) {
@@ -495,24 +511,29 @@ __global__ __launch_bounds__(256) void outputs_kernel(BwdArgs a, int chunks) {
         *reinterpret_cast<floatx4*>(p + 4) = b * hi;
       }
     }
-    if (col + kSlice < a.nv) fetch(col + kSlice);
+    if (col + kSlice < a.nv) {
+      fetch(col + kSlice);
+    } else if (planes<T>() == 1) {
+      sk.load(wk, threadIdx.x);
+      sq.load(wq, threadIdx.x);
+    }
     bf16x8 uf[3], of[3], df[3];
-    frag<3, kSlice>(lds.a.u[0], C * kSlice, 16 * wave + m, 8 * g, uf);
-    frag<3, kSlice>(lds.a.o[0], C * kSlice, 16 * wave + m, 8 * g, of);
-    frag<3, kSlice>(lds.a.d[0], C * kSlice, 16 * wave + m, 8 * g, df);
+    slice_frag(lds.a.u[0], 16 * wave + m, uf);
+    slice_frag(lds.a.o[0], 16 * wave + m, of);
+    slice_frag(lds.a.d[0], 16 * wave + m, df);
     mma<3, 3>(uf, of, Zd);
     mma<3, 3>(uf, df, Wd);
 #pragma unroll
     for (int j = 0; j < 4; ++j) {
       bf16x8 f[3];
       if (j < wave) {
-        frag<3, kSlice>(lds.a.u[0], C * kSlice, 16 * j + m, 8 * g, f);
+        slice_frag(lds.a.u[0], 16 * j + m, f);
         mma<3, 3>(f, of, Z[j]);
         mma<3, 3>(f, df, W[j]);
       } else {
-        frag<3, kSlice>(lds.a.o[0], C * kSlice, 16 * j + m, 8 * g, f);
+        slice_frag(lds.a.o[0], 16 * j + m, f);
         mma<3, 3>(f, uf, Z[j]);
-        frag<3, kSlice>(lds.a.d[0], C * kSlice, 16 * j + m, 8 * g, f);
+        slice_frag(lds.a.d[0], 16 * j + m, f);
         mma<3, 3>(f, uf, W[j]);
       }
     }
@@ -527,11 +548,10 @@ __global__ __launch_bounds__(256) void outputs_kernel(BwdArgs a, int chunks) {
     }
   }
   // K and Q in the slices' place
-  StageK<T, DK, 256> sk, sq;
-  const Window wk(static_cast<const T*>(a.k) + row * DK, left, DK, 0),
-      wq(static_cast<const T*>(a.q) + row * DK, left, DK, 0);
-  sk.load(wk, threadIdx.x);
-  sq.load(wq, threadIdx.x);
+  if (planes<T>() > 1) {
+    sk.load(wk, threadIdx.x);
+    sq.load(wq, threadIdx.x);
+  }
   __syncthreads();
   sk.store(lds.b.k[0], threadIdx.x);
   sq.store(lds.b.q[0], threadIdx.x);

@@ -148,6 +148,7 @@ struct Walker {
           for (int i = 2 * j; i < 4; ++i) u[i] = mfma16(T_[frag_of(i, j)][p], xf[r], u[i]);
     }
     load();
+    values(u);
     // S <- d S + (w U)^T K
     bf16x8 f[3];
     floatx4 w[4];
@@ -178,7 +179,6 @@ struct Walker {
         for (int p = 0; p < 3; ++p) store(1, n, p, f[p]);
       }
     }
-    values(u);
     last();
   }
 };
