@@ -17,7 +17,7 @@ struct WalkArgs {
   float* S_out;            // or null; may be S0
   float* starts;           // [chain][segs][dv][dk]: slot j + 1 first segment j's own write,
                            // then slot j the state that segment j starts from
-  float* moves;            // [chain][segs - 1][dk][dk]: what a segment multiplies its start's
+  float* moves;            // [chain][segs][dk][dk]: what a segment multiplies its start's
                            // rows with, transposed
   long chains;
   int seqlen, nv;
@@ -276,7 +276,7 @@ __global__ __launch_bounds__(threads_of(ND, OUT), (waves_of<T, DK, ND, OUT>())) 
       if (!bad && a.S_out && seg == a.segs - 1) w.S.store(a.S_out + chain * state + (long)row * DK);
       __syncthreads();
     } else if (unit_rows) {
-      if (row < DK) w.S.store_transposed(a.moves + (chain * steps + seg) * DK * DK, row);
+      if (row < DK) w.S.store_transposed(a.moves + (chain * a.segs + seg) * DK * DK, row);
     } else {
       w.S.store(a.starts + (chain * a.segs + seg + 1) * state + (long)row * DK);
     }
@@ -307,63 +307,6 @@ __global__ __launch_bounds__(threads_of(ND, OUT), (waves_of<T, DK, ND, OUT>())) 
 }
 
 
-// The states that segments start from: start of j + 1 = (start of j) M_j + write of j, in
-// place.  A workgroup takes 16 value rows of a chain, a wave 16 columns of the result.
-template <int DK>
-__global__ __launch_bounds__(4 * DK) void join_kernel(WalkArgs a) {
-  constexpr int NQ = (DK + 31) / 32;
-  __shared__ __align__(16) uint2 s[2][NQ][3][64][2];
-  const int wave = wave_id(), lane = threadIdx.x & 63, m = lane & 15, g = lane >> 4;
-  const int blocks = a.nv / 16;
-  const long chain = blockIdx.x / blocks, state = (long)a.nv * DK;
-  const long row = (blockIdx.x % blocks) * 16 + m;
-  const long at = row * DK + 16 * wave + 4 * g;
-  float* starts = a.starts + chain * a.segs * state + at;
-  const float* moves = a.moves + chain * (a.segs - 1) * DK * DK + (16 * wave + m) * DK + 4 * g;
-  const floatx4 zero = {0.f, 0.f, 0.f, 0.f};
-  floatx4 x = a.S0 ? *reinterpret_cast<const floatx4*>(a.S0 + chain * state + at) : zero;
-  *reinterpret_cast<floatx4*>(starts) = x;
-  if (DK == 16) {
-    for (int i = threadIdx.x; i < 2 * 3 * 64; i += 64) (&s[0][0][0][0][0])[2 * i + 1] = uint2{0u, 0u};
-  }
-  floatx4 lo[NQ], hi[NQ], w;
-  auto fetch = [&](int j) {
-    w = *reinterpret_cast<const floatx4*>(starts + (j + 1) * state);
-#pragma unroll
-    for (int i = 0; i < NQ; ++i) {
-      lo[i] = *reinterpret_cast<const floatx4*>(moves + (long)j * DK * DK + 32 * i);
-      hi[i] = DK > 16 ? *reinterpret_cast<const floatx4*>(moves + (long)j * DK * DK + 32 * i + 16) : zero;
-    }
-  };
-  fetch(0);
-  for (int j = 0; j < a.segs - 1; ++j) {
-    uint2 h, mi, l;
-    split3(x.x, x.y, h.x, mi.x, l.x);
-    split3(x.z, x.w, h.y, mi.y, l.y);
-    uint2 (*to)[64][2] = s[j & 1][wave / 2];
-    to[0][lane][wave & 1] = h;
-    to[1][lane][wave & 1] = mi;
-    to[2][lane][wave & 1] = l;
-    bf16x8 f[NQ][3];
-#pragma unroll
-    for (int i = 0; i < NQ; ++i) frag_pair(lo[i], hi[i], f[i]);
-    x = w;
-    __syncthreads();
-    if (j + 2 < a.segs) fetch(j + 1);
-    floatx4 y = zero;
-#pragma unroll
-    for (int i = 0; i < NQ; ++i) {
-      bf16x8 b[3];
-#pragma unroll
-      for (int p = 0; p < 3; ++p) b[p] = __builtin_bit_cast(bf16x8, *reinterpret_cast<const uint4*>(s[j & 1][i][p][lane]));
-      if (i & 1) mma<3, 3>(f[i], b, y);
-      else mma<3, 3>(f[i], b, x);
-    }
-    x += y;
-    *reinterpret_cast<floatx4*>(starts + (j + 1) * state) = x;
-  }
-}
-
 // ------------------------------------------------------------------- plans
 
 struct Plan {
@@ -372,26 +315,17 @@ struct Plan {
   size_t T_bytes, starts, moves;      // bytes
   size_t bytes() const { return T_bytes + starts + moves; }
 };
-constexpr long kWhole = 16, kSlots = 256;
 Plan plan_of(const DeltaArgs& a) {
   Plan p;
   p.chains = (long)a.batch * a.heads;
   const long chunks = ((long)a.seqlen + C - 1) / C;
   p.nd = a.dv >= 32 ? 2 : 1;
   if (a.dtype != 0 && a.dk == 128) p.nd = 1;
-  p.segs = 1;
-  p.per = (int)chunks;
   // segments: walked twice, and the first time with dk unit rows more
-  const long units = p.chains * ((a.dv + a.dk + 63) / 64);
-  if (chunks >= kWhole && units <= kSlots / 4) {
-    long n = kSlots / units;
-    if (n > chunks / 4) n = chunks / 4;
-    p.per = (int)((chunks + n - 1) / n);
-    p.segs = (int)((chunks + p.per - 1) / p.per);
-  }
+  cut(chunks, p.chains * ((a.dv + a.dk + 63) / 64), p.segs, p.per);
   p.T_bytes = (size_t)p.chains * chunks * kT * 16;
   p.starts = p.segs > 1 ? (size_t)p.chains * p.segs * a.dv * a.dk * 4 : 0;
-  p.moves = p.segs > 1 ? (size_t)p.chains * (p.segs - 1) * a.dk * a.dk * 4 : 0;
+  p.moves = p.segs > 1 ? (size_t)p.chains * p.segs * a.dk * a.dk * 4 : 0;
   return p;
 }
 
@@ -425,8 +359,8 @@ hipError_t run(const DeltaArgs& a, const Plan& p, hipStream_t stream) {
         // (a state wave for each SIMD of a compute unit)
         hipError_t e = a.dv >= 64 ? go<T, DK, 4, false>(w, stream) : go<T, DK, ND, false>(w, stream);
         if (e != hipSuccess) return e;
-        hipLaunchKernelGGL((join_kernel<DK>), dim3((unsigned)(p.chains * (a.dv / 16))), dim3(4 * DK), 0, stream, w);
-        if ((e = hipGetLastError()) != hipSuccess) return e;
+        const Joins j{{{a.S0, w.starts, w.moves, false}, {}}, p.chains, a.dv, p.segs};
+        if ((e = launch_join<DK>(j, 1, stream)) != hipSuccess) return e;
       }
       return go<T, DK, ND, true>(w, stream);
     };

@@ -47,6 +47,13 @@ struct BwdArgs {
   float* R;                // [chain][chunks][dv][dk]: behind each chunk
   long chains;
   int seqlen, nv;
+  // segments of a chain, chunks of one; with several, what each walk starts from (Joins of the
+  // two directions; a segment is a step, the last one the backward walk's first)
+  int segs, per;
+  float* starts_S;
+  float* starts_R;
+  float* moves;            // [chain][segs][dk][dk]: what a segment multiplies its start's rows with, transposed
+  float* moves_t;          // the same as it is, which is what R's rows are multiplied with, transposed
 };
 
 // ----------------------------------------------- P^T dO and dO^T (e Q)
@@ -269,82 +276,111 @@ __device__ __forceinline__ void store_values(const float* p, int nv, int col, lo
     }
 }
 
-// ND walkers; the first half of the blocks walks forward, the other backward.
-template <typename T, int DK, int ND>
-__global__ __launch_bounds__(64 * (ND + kKeyWaves), 2) void walks_kernel(BwdArgs a, int n) {
+// ND walkers of one segment; the first blocks walk forward, as many more backward.  WRITE: each
+// segment's own write from zero, and behind them unit rows, which give the matrix that a segment
+// multiplies its start's rows with.
+template <typename T, int DK, int ND, bool WRITE>
+__global__ __launch_bounds__(64 * (ND + kKeyWaves), 2) void walks_kernel(BwdArgs a, int chunks) {
   extern __shared__ __align__(16) unsigned char smem[];
   using L = StateLds<T, DK>;
   constexpr int DZ = 16 * ND, NK = DK / 16;
   L& lds = *reinterpret_cast<L*>(smem);
   const int vblocks = a.nv / DZ;
   int blk;
-  long chain;
-  if (!place(2 * vblocks, a.chains, blk, chain)) return;
-  const bool back = blk >= vblocks;
-  const int row0 = (back ? blk - vblocks : blk) * DZ;
+  long unit;
+  if (!place(2 * vblocks + (WRITE ? (DK + DZ - 1) / DZ : 0), a.chains * a.segs, blk, unit)) return;
+  const long chain = unit / a.segs;
+  const int seg = (int)(unit % a.segs);
+  const bool unit_rows = WRITE && blk >= 2 * vblocks, back = !unit_rows && blk >= vblocks;
+  const int row0 = (blk - (unit_rows ? 2 * vblocks : back ? vblocks : 0)) * DZ;
   const int wave = wave_id();
-  const long len = a.seqlen;
-  const T* k = static_cast<const T*>(a.k) + chain * len * DK;
-  const float* la = a.log_a ? a.log_a + chain * len : nullptr;
-  const float* be = a.beta + chain * len;
+  const long c0 = (long)seg * a.per, first = chain * a.seqlen + c0 * C, left = a.seqlen - c0 * C;
+  const int n = chunks - c0 < a.per ? (int)(chunks - c0) : a.per;
   if (wave >= ND) {
-    if (back) keys_only<T, DK, true>(lds, k, la, be, len, n, threadIdx.x - 64 * ND);
-    else keys_only<T, DK, false>(lds, k, la, be, len, n, threadIdx.x - 64 * ND);
+    const T* k = static_cast<const T*>(a.k) + first * DK;
+    const float* la = a.log_a ? a.log_a + first : nullptr;
+    if (back) keys_only<T, DK, true>(lds, k, la, a.beta + first, left, n, threadIdx.x - 64 * ND);
+    else keys_only<T, DK, false>(lds, k, la, a.beta + first, left, n, threadIdx.x - 64 * ND);
     return;
   }
-  const int row = row0 + 16 * wave;
+  const int row = row0 + 16 * wave;            // (unit rows behind the last one are zeros)
   const long state = (long)a.nv * DK, at = (long)row * DK;
   if (!back) {
     Walker<T, DK> w;
-    const T* v = static_cast<const T*>(a.v) + chain * len * a.nv;
-    const uint4* Tp = a.T + chain * n * kT;
-    float* S = a.S + chain * (n + 1) * state + at;
-    const float* U = a.U + chain * len * a.nv;
-    w.S.load(a.S0 ? a.S0 + chain * state + at : nullptr);
+    const T* v = static_cast<const T*>(a.v) + first * a.nv;
+    const uint4* Tp = a.T + (chain * chunks + c0) * kT;
+    float* S = a.S + (chain * (chunks + 1) + c0) * state + at;
+    const float* U = a.U + first * a.nv;
+    if (unit_rows) w.S.unit(row);
+    else if (WRITE) w.S.load(nullptr);
+    else if (a.segs > 1) w.S.load(a.starts_S + unit * state + at);
+    else w.S.load(a.S0 ? a.S0 + chain * state + at : nullptr);
     w.load_T(Tp);
-    w.load_v(v, len, a.nv, row);
+    auto load_v = [&](int c) {
+      w.load_v(v + (long)c * C * a.nv, unit_rows ? 0 : left - (long)c * C, a.nv, row);
+    };
+    load_v(0);
     for (int c = 0; c < n; ++c) {
       __syncthreads();
       if (c == 0) w.load_k(lds.k[0][0]);
       const int next = c + 1 < n ? c + 1 : c;
-      w.S.store(S + c * state);
+      if (!WRITE) w.S.store(S + c * state);
       w.template chunk<false>(lds.k[c % L::R][0], lds.gate[c % L::R],
               [&] {
-                w.load_v(v + (long)next * C * a.nv, len - (long)next * C, a.nv, row);
+                load_v(next);
                 w.load_T(Tp + (long)next * kT);
               },
               [&] { w.load_k(lds.k[next % L::R][0]); }, [](int, int, int, const bf16x8&) {},
-              [&](const floatx4 (&u)[4]) { store_values(U + (long)c * C * a.nv, a.nv, row, len - (long)c * C, u); });
+              [&](const floatx4 (&u)[4]) {
+                if (!WRITE) store_values(U + (long)c * C * a.nv, a.nv, row, left - (long)c * C, u);
+              });
     }
     __syncthreads();
-    w.S.store(S + n * state);
+    if (!WRITE) {
+      if (seg == a.segs - 1) w.S.store(S + n * state);
+    } else if (unit_rows) {
+      if (row >= DK) return;
+      w.S.store_transposed(a.moves + unit * DK * DK, row);
+      w.S.store(a.moves_t + unit * DK * DK + at);
+    } else if (seg < a.segs - 1) {
+      w.S.store(a.starts_S + (unit + 1) * state + at);
+    }
     return;
   }
   BackWalker<T, DK> w;
   const int tiles = a.nv / 16, z = row / 16;
-  const uint4* Tp = a.Tt + chain * n * kT;
-  const float4* H = a.H + (chain * n * tiles + z) * 4 * 64;
-  const float4* G = a.G + (chain * n * tiles + z) * NK * 64;
-  float* R = a.R + chain * n * state + at;
-  const float* du = a.dv + chain * len * a.nv;
-  w.R.load(a.dS_L ? a.dS_L + chain * state + at : nullptr);
+  const uint4* Tp = a.Tt + (chain * chunks + c0) * kT;
+  const float4* H = a.H + ((chain * chunks + c0) * tiles + z) * 4 * 64;
+  const float4* G = a.G + ((chain * chunks + c0) * tiles + z) * NK * 64;
+  float* R = a.R + (chain * chunks + c0) * state + at;
+  const float* du = a.dv + first * a.nv;
+  const long step = chain * a.segs + a.segs - 1 - seg;
+  if (WRITE) w.R.load(nullptr);
+  else if (a.segs > 1) w.R.load(a.starts_R + step * state + at);
+  else w.R.load(a.dS_L ? a.dS_L + chain * state + at : nullptr);
   w.load_h(H + (long)(n - 1) * tiles * 4 * 64);
   w.load_T(Tp + (long)(n - 1) * kT);
   w.load_G(G + (long)(n - 1) * tiles * NK * 64);
   for (int i = 0; i < n; ++i) {
     __syncthreads();
     const int c = n - 1 - i, next = c > 0 ? c - 1 : 0;
-    w.R.store(R + c * state);
+    if (!WRITE) w.R.store(R + c * state);
     w.chunk(lds.k[i % L::R][0], lds.gate[i % L::R],
             [&] {
               w.load_h(H + (long)next * tiles * 4 * 64);
               w.load_T(Tp + (long)next * kT);
             },
             [&] { w.load_G(G + (long)next * tiles * NK * 64); },
-            [&](const floatx4 (&u)[4]) { store_values(du + (long)c * C * a.nv, a.nv, row, len - (long)c * C, u); });
+            [&](const floatx4 (&u)[4]) {
+              if (!WRITE) store_values(du + (long)c * C * a.nv, a.nv, row, left - (long)c * C, u);
+            });
   }
   __syncthreads();
-  if (a.dS0) w.R.store(a.dS0 + chain * state + at);
+  if (WRITE) {
+    if (seg > 0) w.R.store(a.starts_R + (step + 1) * state + at);
+  } else if (a.dS0 && seg == 0) {
+    w.R.store(a.dS0 + chain * state + at);
+  }
 }
 
 // --------------------------------------------------------------- outputs
@@ -673,8 +709,9 @@ __global__ __launch_bounds__(256, (DK <= 64 ? 2 : 1)) void outputs_kernel(BwdArg
 
 struct Plan {
   long chains, chunks;
-  size_t T, H, G, U, S, R;           // bytes
-  size_t bytes() const { return 2 * T + H + G + U + S + R; }
+  int segs, per;
+  size_t T, H, G, U, S, R, starts, moves;      // bytes
+  size_t bytes() const { return 2 * T + H + G + U + S + R + 2 * starts + 2 * moves; }
 };
 Plan plan_of(const DeltaBwdArgs& a) {
   Plan p;
@@ -687,6 +724,11 @@ Plan plan_of(const DeltaBwdArgs& a) {
   p.U = (size_t)p.chains * a.seqlen * a.ndv * 4;
   p.S = (units + p.chains) * state;
   p.R = units * state;
+  // segments: walked twice, and the first time with dk unit rows more
+  const long walks = p.chains * (2 * ((a.ndv + 63) / 64) + (a.ndk + 63) / 64);
+  cut(p.chunks, walks, p.segs, p.per);
+  p.starts = p.segs > 1 ? (size_t)p.chains * p.segs * state : 0;
+  p.moves = p.segs > 1 ? (size_t)p.chains * p.segs * a.ndk * a.ndk * 4 : 0;
   return p;
 }
 
@@ -715,10 +757,16 @@ hipError_t run(const DeltaBwdArgs& a, const Plan& p, hipStream_t stream) {
   w.G = reinterpret_cast<float4*>(take(p.G));
   w.S = reinterpret_cast<float*>(take(p.S));
   w.R = reinterpret_cast<float*>(take(p.R));
-  w.U = reinterpret_cast<float*>(take(p.U));
   w.chains = p.chains;
   w.seqlen = a.seqlen;
   w.nv = a.ndv;
+  w.segs = p.segs;
+  w.per = p.per;
+  w.starts_S = reinterpret_cast<float*>(take(p.starts));
+  w.starts_R = reinterpret_cast<float*>(take(p.starts));
+  w.moves = reinterpret_cast<float*>(take(p.moves));
+  w.moves_t = reinterpret_cast<float*>(take(p.moves));
+  w.U = reinterpret_cast<float*>(take(p.U));
   const SolveArgs s{a.k, a.beta, a.log_a, T_, Tt, p.chains, a.seqlen};
   const hipError_t e = launch_solve(s, a.ndk, a.dtype, stream);
   if (e != hipSuccess) return e;
@@ -729,8 +777,17 @@ hipError_t run(const DeltaBwdArgs& a, const Plan& p, hipStream_t stream) {
     hipError_t e = go(prep_kernel<T, DK>, units, 256, sizeof(PrepLds<T, DK>), stream, w, n);
     if (e != hipSuccess) return e;
     auto walks = [&](auto nd) {
-      constexpr int ND = decltype(nd)::value;
-      return go(walks_kernel<T, DK, ND>, grid_of(2 * (a.ndv / (16 * ND)), p.chains), 64 * (ND + kKeyWaves),
+      constexpr int ND = decltype(nd)::value, threads = 64 * (ND + kKeyWaves);
+      const int vblocks = a.ndv / (16 * ND), ublocks = (DK + 16 * ND - 1) / (16 * ND);
+      if (p.segs > 1) {
+        hipError_t e = go(walks_kernel<T, DK, ND, true>, grid_of(2 * vblocks + ublocks, p.chains * p.segs), threads,
+                          sizeof(StateLds<T, DK>), stream, w, n);
+        if (e != hipSuccess) return e;
+        const Joins j{{{a.S0, w.starts_S, w.moves, false}, {a.dS_L, w.starts_R, w.moves_t, true}},
+                      p.chains, a.ndv, p.segs};
+        if ((e = launch_join<DK>(j, 2, stream)) != hipSuccess) return e;
+      }
+      return go(walks_kernel<T, DK, ND, false>, grid_of(2 * vblocks, p.chains * p.segs), threads,
                 sizeof(StateLds<T, DK>), stream, w, n);
     };
     e = a.ndv >= 64   ? walks(std::integral_constant<int, 4>())

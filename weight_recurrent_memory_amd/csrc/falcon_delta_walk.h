@@ -256,6 +256,108 @@ __device__ __forceinline__ void keys_only(StateLds<T, DK>& lds, const T* k, cons
   __syncthreads();
 }
 
+// ------------------------------------------------------------- segments
+// A long sequence of few chains is cut into segments that are walked side by side.  The rule
+// is affine in S, S -> S M + N with M (dk x dk) and N of the segment alone: a first launch
+// walks every segment from zero (N) and from unit rows (M), a second joins them in order, the
+// main walk then starts each segment from its state.  R -> R M^T + N' for the gradient's.
+
+// units: workgroups of the first launch over all chains for one segment each.
+constexpr long kWhole = 16, kSlots = 256;
+inline void cut(long chunks, long units, int& segs, int& per) {
+  segs = 1;
+  per = (int)chunks;
+  if (chunks < kWhole || units > kSlots / 4) return;
+  long n = kSlots / units;
+  if (n > chunks / 4) n = chunks / 4;
+  per = (int)((chunks + n - 1) / n);
+  segs = (int)((chunks + per - 1) / per);
+}
+
+struct Join {
+  const float* S0;         // or null
+  float* starts;           // [chain][segs][dv][dk]: slot j + 1 step j's own write, then slot j what step j starts from
+  const float* moves;      // [chain][segs][dk][dk], transposed
+  bool reverse;            // the first step is the last segment
+};
+struct Joins {
+  Join j[2];
+  long chains;
+  int nv, segs;
+};
+
+// start of step j + 1 = (start of j) M_j + write of j, in place.  A workgroup takes 16 value rows of
+// a chain, a wave 16 columns of the result; operands of two steps are on their way.
+template <int DK>
+__global__ __launch_bounds__(4 * DK) void join_kernel(Joins all) {
+  constexpr int NQ = (DK + 31) / 32;
+  __shared__ __align__(16) uint2 s[2][NQ][3][64][2];
+  const Join a = all.j[blockIdx.y];
+  const int wave = wave_id(), lane = threadIdx.x & 63, m = lane & 15, g = lane >> 4;
+  const int blocks = all.nv / 16, steps = all.segs - 1;
+  const long chain = blockIdx.x / blocks, state = (long)all.nv * DK;
+  const long row = (blockIdx.x % blocks) * 16 + m;
+  const long at = row * DK + 16 * wave + 4 * g;
+  float* starts = a.starts + chain * all.segs * state + at;
+  const float* moves = a.moves + (chain * all.segs + (a.reverse ? steps : 0)) * DK * DK + (16 * wave + m) * DK + 4 * g;
+  const long stride = a.reverse ? -(long)DK * DK : (long)DK * DK;
+  const floatx4 zero = {0.f, 0.f, 0.f, 0.f};
+  floatx4 x = a.S0 ? *reinterpret_cast<const floatx4*>(a.S0 + chain * state + at) : zero;
+  *reinterpret_cast<floatx4*>(starts) = x;
+  if (DK == 16) {
+    for (int i = threadIdx.x; i < 2 * 3 * 64; i += 64) (&s[0][0][0][0][0])[2 * i + 1] = uint2{0u, 0u};
+  }
+  struct Step {
+    floatx4 lo[NQ], hi[NQ], w;
+  } ahead[2];
+  auto fetch = [&](Step& o, int j) {
+    if (j >= steps) return;
+    o.w = *reinterpret_cast<const floatx4*>(starts + (j + 1) * state);
+#pragma unroll
+    for (int i = 0; i < NQ; ++i) {
+      o.lo[i] = *reinterpret_cast<const floatx4*>(moves + j * stride + 32 * i);
+      o.hi[i] = DK > 16 ? *reinterpret_cast<const floatx4*>(moves + j * stride + 32 * i + 16) : zero;
+    }
+  };
+  auto step = [&](Step& o, int j, int buf) {
+    uint2 h, mi, l;
+    split3(x.x, x.y, h.x, mi.x, l.x);
+    split3(x.z, x.w, h.y, mi.y, l.y);
+    uint2 (*to)[64][2] = s[buf][wave / 2];
+    to[0][lane][wave & 1] = h;
+    to[1][lane][wave & 1] = mi;
+    to[2][lane][wave & 1] = l;
+    bf16x8 f[NQ][3];
+#pragma unroll
+    for (int i = 0; i < NQ; ++i) frag_pair(o.lo[i], o.hi[i], f[i]);
+    x = o.w;
+    fetch(o, j + 2);
+    __syncthreads();
+    floatx4 y = zero;
+#pragma unroll
+    for (int i = 0; i < NQ; ++i) {
+      bf16x8 b[3];
+#pragma unroll
+      for (int p = 0; p < 3; ++p) b[p] = __builtin_bit_cast(bf16x8, *reinterpret_cast<const uint4*>(s[buf][i][p][lane]));
+      if (i & 1) mma<3, 3>(f[i], b, y);
+      else mma<3, 3>(f[i], b, x);
+    }
+    x += y;
+    *reinterpret_cast<floatx4*>(starts + (j + 1) * state) = x;
+  };
+  fetch(ahead[0], 0);
+  fetch(ahead[1], 1);
+  for (int j = 0; j < steps; j += 2) {
+    step(ahead[0], j, 0);
+    if (j + 1 < steps) step(ahead[1], j + 1, 1);
+  }
+}
+template <int DK>
+hipError_t launch_join(const Joins& j, int directions, hipStream_t stream) {
+  hipLaunchKernelGGL((join_kernel<DK>), dim3((unsigned)(j.chains * (j.nv / 16)), directions), dim3(4 * DK), 0, stream, j);
+  return hipGetLastError();
+}
+
 }  // namespace
 }  // namespace delta
 }  // namespace falcon
