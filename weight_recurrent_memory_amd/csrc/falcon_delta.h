@@ -109,6 +109,11 @@ __device__ __forceinline__ float load_one(const Window& w, int i, uint16_t) {
 }
 __device__ __forceinline__ float load_one(const Window& w, int i, float) { return load_f32(w, 4 * i); }
 
+// Four consecutive floats in LDS, 16-byte aligned.
+__device__ __forceinline__ floatx4 four(const float* p) {
+  return *static_cast<const floatx4*>(__builtin_assume_aligned(p, 16));
+}
+
 // A chunk's gates, one token a lane.
 struct Gates {
   alignas(16) float2 g[C];           // sums of log2 decays

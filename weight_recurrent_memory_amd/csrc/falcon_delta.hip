@@ -27,7 +27,11 @@ struct WalkArgs {
 template <typename T, int DK, int ND>
 struct WalkLds : StateLds<T, DK> {
   alignas(16) uint4 s[2][ND][StateLds<T, DK>::NQ][3][64];     // S at the chunk's start, as operands
-  alignas(16) uint4 u[2][ND][2][3][64];
+  // U: as it is, for the output waves to split; at 128 columns, where they have more to do than
+  // the state waves, as operands (us of the kernel: 1x4x32771x128 118 against 134, 8x12x2048x64
+  // 79 against 75)
+  static constexpr bool kSplit = DK == 128;
+  alignas(16) uint4 u[2][ND][kSplit ? 6 : 4][64];
 };
 
 // Output waves of a workgroup of ND state waves, and the token tiles of output wave w.  (Waves
@@ -61,11 +65,28 @@ __device__ __forceinline__ void outputs(const WalkArgs& a, WalkLds<T, DK, ND>& l
     for (int j = 0; j < NT_; ++j) qr[j].load(wq, 16 * tile_of<ND>(ow, j) + m);
   };
   load_q(0);
+#pragma unroll
+  for (int j = 0; j < NT_; ++j) {
+    ev[j] = 0.0f;
+#pragma unroll
+    for (int i = 0; i < NQ; ++i)
+#pragma unroll
+      for (int p = 0; p < NP; ++p) qf[j][i][p] = zero_frag();
+#pragma unroll
+    for (int i = 0; i < 2; ++i)
+#pragma unroll
+      for (int p = 0; p < 3; ++p) pf[j][i][p] = zero_frag();
+  }
+  // No branch in a step: one would make a wait for a load wait for the stores behind it.  Before
+  // the first chunk the outputs go to a window of no rows, behind the last one K, q and the scores
+  // are formed once more.
   for (int c = 0; c <= n; ++c) {
     __syncthreads();
-    if (c + D < n) keys.load(c + D);
-    if (c > 0) {
-      const int b = (c - 1) & 1;
+    const int cc = c < n ? c : n - 1, ahead = c + D < n ? c + D : n - 1;
+    keys.load(ahead);
+    {
+      const int b = (c + 1) & 1;
+      const Window wo(o + (long)(c - 1) * C * a.nv, c > 0 ? left - (long)(c - 1) * C : 0, a.nv, c > 0 ? row0 : 0);
 #pragma unroll
       for (int z = 0; z < ND; ++z) {
         floatx4 acc[NT_];
@@ -89,9 +110,15 @@ __device__ __forceinline__ void outputs(const WalkArgs& a, WalkLds<T, DK, ND>& l
         for (int j = 0; j < NT_; ++j) acc[j] *= ev[j];
 #pragma unroll
         for (int i = 0; i < 2; ++i) {
+          if (i == 1 && tile_of<ND>(ow, NT_ - 1) < 2) continue;
           bf16x8 u[3];
+          if constexpr (WalkLds<T, DK, ND>::kSplit) {
 #pragma unroll
-          for (int p = 0; p < 3; ++p) u[p] = __builtin_bit_cast(bf16x8, lds.u[b][z][i][p][lane]);
+            for (int p = 0; p < 3; ++p) u[p] = __builtin_bit_cast(bf16x8, lds.u[b][z][3 * i + p][lane]);
+          } else {
+            frag_pair(__builtin_bit_cast(floatx4, lds.u[b][z][2 * i][lane]),
+                      __builtin_bit_cast(floatx4, lds.u[b][z][2 * i + 1][lane]), u);
+          }
 #pragma unroll
           for (int p = 0; p < 3; ++p)
 #pragma unroll
@@ -102,16 +129,16 @@ __device__ __forceinline__ void outputs(const WalkArgs& a, WalkLds<T, DK, ND>& l
         }
 #pragma unroll
         for (int j = 0; j < NT_; ++j) {
-          const long t = (long)(c - 1) * C + 16 * tile_of<ND>(ow, j) + m;
-          if (t < left)
-            __builtin_nontemporal_store(acc[j], reinterpret_cast<floatx4*>(o + t * a.nv + 16 * z + 4 * g));
+          // (2: past the caches)
+          __builtin_amdgcn_raw_buffer_store_b128(__builtin_bit_cast(uint4_t, acc[j]), wo.r,
+                                                 ((16 * tile_of<ND>(ow, j) + m) * a.nv + 16 * z + 4 * g) * 4, 0, 2);
         }
       }
     }
-    if (c < n) {
+    {
       // this chunk's scores, decayed: operands with rows t and slots s
-      const uint16_t* kl = lds.k[c % R][0];
-      const Gates& gt = lds.gate[c % R];
+      const uint16_t* kl = lds.k[cc % R][0];
+      const Gates& gt = lds.gate[cc % R];
 #pragma unroll
       for (int j = 0; j < NT_; ++j) {
         const int ti = tile_of<ND>(ow, j);
@@ -143,9 +170,9 @@ __device__ __forceinline__ void outputs(const WalkArgs& a, WalkLds<T, DK, ND>& l
           frag_pair(p[0], p[1], pf[j][h]);
         }
       }
-      if (c + 1 < n) load_q(c + 1);
+      load_q(c + 1 < n ? c + 1 : n - 1);
     }
-    if (c + D < n) keys.store(lds, c + D);
+    keys.store(lds, c + D);
   }
 }
 
@@ -254,20 +281,34 @@ __global__ __launch_bounds__(threads_of(ND, OUT), (waves_of<T, DK, ND, OUT>())) 
       if (c == 0) w.load_k(lds.k[0][0]);
       // (what is behind the last chunk is loaded in its own place: no branch holds registers)
       const int next = c + 1 < n ? c + 1 : c;
-      w.template chunk<OUT>(lds.k[c % L::R][0], lds.gate[c % L::R],
+      w.chunk(lds.k[c % L::R][0], lds.gate[c % L::R],
               [&] {
                 // (loads come back in order: the one needed first is issued first)
                 load_v(next);
                 w.load_T(Tp + (long)next * kT);
               },
               [&] { w.load_k(lds.k[next % L::R][0]); },
-              [&](int which, int i, int p, const bf16x8& f) {
+              [&](int i, int p, const bf16x8& f) {
+                if constexpr (OUT) lds.s[c & 1][wave][i][p][lane] = __builtin_bit_cast(uint4, f);
+              },
+              [&](const floatx4 (&u)[4]) {
                 if constexpr (OUT) {
-                  uint4* to = which == 0 ? lds.s[c & 1][wave][i][p] : lds.u[c & 1][wave][i][p];
-                  to[lane] = __builtin_bit_cast(uint4, f);
+                  if constexpr (!L::kSplit) {
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) lds.u[c & 1][wave][i][lane] = __builtin_bit_cast(uint4, u[i]);
+                  }
                 }
               },
-              [](const floatx4 (&)[4]) {});
+              [&](int i, const floatx4 (&u)[4]) {
+                if constexpr (OUT) {
+                  if constexpr (L::kSplit) {
+                    bf16x8 f[3];
+                    frag_pair(u[2 * i], u[2 * i + 1], f);
+#pragma unroll
+                    for (int p = 0; p < 3; ++p) lds.u[c & 1][wave][3 * i + p][lane] = __builtin_bit_cast(uint4, f[p]);
+                  }
+                }
+              });
     }
     __syncthreads();
     if constexpr (OUT) {

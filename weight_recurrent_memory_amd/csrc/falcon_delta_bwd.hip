@@ -145,7 +145,7 @@ __global__ __launch_bounds__(256) void prep_kernel(BwdArgs a, int chunks) {
       *reinterpret_cast<floatx4*>(H + s * 64) = x;
     }
 #pragma unroll
-    for (int i = 0; i < 4; ++i) o[i] *= *reinterpret_cast<const floatx4*>(lds.gate.e + 16 * i + 4 * g);
+    for (int i = 0; i < 4; ++i) o[i] *= four(lds.gate.e + 16 * i + 4 * g);
     frag_pair(o[0], o[1], of[0]);
     frag_pair(o[2], o[3], of[1]);
     float4* G = a.G + (unit * tiles + z) * NK * 64 + lane;
@@ -216,7 +216,7 @@ struct BackWalker {
     for (int j = 0; j < 2; ++j) {
 #pragma unroll
       for (int i = 2 * j; i < 2 * j + 2; ++i) {
-        const floatx4 w = *reinterpret_cast<const floatx4*>(gt.w + 16 * i + 4 * g);
+        const floatx4 w = four(gt.w + 16 * i + 4 * g);
 #pragma unroll
         for (int r = 0; r < 4; ++r) x[i][r] = h[i][r] + w[r] * x[i][r];
       }
@@ -241,8 +241,8 @@ struct BackWalker {
     load2();
 #pragma unroll
     for (int n = 0; n < 2; ++n) {
-      const floatx4 b0 = *reinterpret_cast<const floatx4*>(gt.be + 32 * n + 4 * g);
-      const floatx4 b1 = *reinterpret_cast<const floatx4*>(gt.be + 32 * n + 16 + 4 * g);
+      const floatx4 b0 = four(gt.be + 32 * n + 4 * g);
+      const floatx4 b1 = four(gt.be + 32 * n + 16 + 4 * g);
       frag_pair(-b0 * u[2 * n], -b1 * u[2 * n + 1], f);
       constexpr int J = NK < 4 ? NK : 4;
 #pragma unroll
@@ -325,15 +325,16 @@ __global__ __launch_bounds__(64 * (ND + kKeyWaves), 2) void walks_kernel(BwdArgs
       if (c == 0) w.load_k(lds.k[0][0]);
       const int next = c + 1 < n ? c + 1 : c;
       if (!WRITE) w.S.store(S + c * state);
-      w.template chunk<false>(lds.k[c % L::R][0], lds.gate[c % L::R],
+      w.chunk(lds.k[c % L::R][0], lds.gate[c % L::R],
               [&] {
                 load_v(next);
                 w.load_T(Tp + (long)next * kT);
               },
-              [&] { w.load_k(lds.k[next % L::R][0]); }, [](int, int, int, const bf16x8&) {},
+              [&] { w.load_k(lds.k[next % L::R][0]); }, [](int, int, const bf16x8&) {},
               [&](const floatx4 (&u)[4]) {
                 if (!WRITE) store_values(U + (long)c * C * a.nv, a.nv, row, left - (long)c * C, u);
-              });
+              },
+              [](int, const floatx4 (&)[4]) {});
     }
     __syncthreads();
     if (!WRITE) {

@@ -101,26 +101,27 @@ struct Walker {
     }
   }
 
-  // One chunk; store(which, index, plane, fragment) gets S's and (FRAGS) U's operands,
-  // values(U) U itself.  load() is called once v and T are used, last() behind everything.
-  template <bool FRAGS, class Load, class Last, class Store, class Values>
+  // One chunk; store(index, plane, fragment) gets S's operands, values(U) U, pairs(n, U) U once
+  // tiles 2 n and 2 n + 1 are on their way into S.  load() is called once v and T are used,
+  // last() behind everything.
+  template <class Load, class Last, class Store, class Values, class Pairs>
   __device__ __forceinline__ void chunk(const uint16_t* k, const Gates& gt, Load&& load, Last&& last, Store&& store,
-                                        Values&& values) {
+                                        Values&& values, Pairs&& pairs) {
     const int g = (threadIdx.x & 63) >> 4;
     const floatx4 zero = {0.f, 0.f, 0.f, 0.f};
     // K S^T
     floatx4 x[4] = {zero, zero, zero, zero}, b[4], be[4];
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
-      b[i] = *reinterpret_cast<const floatx4*>(gt.b + 16 * i + 4 * g);
-      be[i] = *reinterpret_cast<const floatx4*>(gt.be + 16 * i + 4 * g);
+      b[i] = four(gt.b + 16 * i + 4 * g);
+      be[i] = four(gt.be + 16 * i + 4 * g);
     }
 #pragma unroll
     for (int n = 0; n < NQ; ++n) {
       bf16x8 s[3];
       S.frag(n, s);
 #pragma unroll
-      for (int p = 0; p < 3; ++p) store(0, n, p, s[p]);
+      for (int p = 0; p < 3; ++p) store(n, p, s[p]);
       bf16x8(&kn)[4][NP] = kf[kAhead ? n : 0];
       if (!kAhead) load_k_step(k, n, kn);
 #pragma unroll
@@ -153,7 +154,7 @@ struct Walker {
     bf16x8 f[3];
     floatx4 w[4];
 #pragma unroll
-    for (int i = 0; i < 4; ++i) w[i] = *reinterpret_cast<const floatx4*>(gt.w + 16 * i + 4 * g);
+    for (int i = 0; i < 4; ++i) w[i] = four(gt.w + 16 * i + 4 * g);
     const float d = gt.d;
 #pragma unroll
     for (int j = 0; j < NK; ++j) S.t[j] *= d;
@@ -173,11 +174,7 @@ struct Walker {
 #pragma unroll
             for (int j = 0; j < J; ++j) S.t[j0 + j] = mfma16(kt[j][p], f[r], S.t[j0 + j]);
       }
-      if constexpr (FRAGS) {
-        frag_pair(u[2 * n], u[2 * n + 1], f);
-#pragma unroll
-        for (int p = 0; p < 3; ++p) store(1, n, p, f[p]);
-      }
+      pairs(n, u);
     }
     last();
   }
@@ -224,9 +221,10 @@ struct Keys {
     sk.load(Window(k + at * DK, left - at, DK, 0), t);
     gl.load(la, be, at, left);
   }
-  __device__ __forceinline__ void store(StateLds<T, DK>& lds, int c) const {
-    sk.store(lds.k[c % R][0], t);
-    if (t < 64) gl.store(lds.gate[c % R]);
+  // to the place of chunk `to`
+  __device__ __forceinline__ void store(StateLds<T, DK>& lds, int to) const {
+    sk.store(lds.k[to % R][0], t);
+    if (t < 64) gl.store(lds.gate[to % R]);
   }
   // t: thread of the NTH; k, la, be and `left` tokens from the walk's first token on
   __device__ __forceinline__ Keys(StateLds<T, DK>& lds, const T* k_, const float* la_, const float* be_, long left_,
@@ -295,8 +293,10 @@ __global__ __launch_bounds__(4 * DK) void join_kernel(Joins all) {
   const Join a = all.j[blockIdx.y];
   const int wave = wave_id(), lane = threadIdx.x & 63, m = lane & 15, g = lane >> 4;
   const int blocks = all.nv / 16, steps = all.segs - 1;
-  const long chain = blockIdx.x / blocks, state = (long)all.nv * DK;
-  const long row = (blockIdx.x % blocks) * 16 + m;
+  int blk;
+  long chain;
+  if (!place(blocks, all.chains, blk, chain)) return;      // (a chain's blocks read its moves in one XCD's L2)
+  const long state = (long)all.nv * DK, row = blk * 16 + m;
   const long at = row * DK + 16 * wave + 4 * g;
   float* starts = a.starts + chain * all.segs * state + at;
   const float* moves = a.moves + (chain * all.segs + (a.reverse ? steps : 0)) * DK * DK + (16 * wave + m) * DK + 4 * g;
@@ -311,7 +311,7 @@ __global__ __launch_bounds__(4 * DK) void join_kernel(Joins all) {
     floatx4 lo[NQ], hi[NQ], w;
   } ahead[2];
   auto fetch = [&](Step& o, int j) {
-    if (j >= steps) return;
+    if (j >= steps) j = steps - 1;       // (no branch: one would wait for what is on its way)
     o.w = *reinterpret_cast<const floatx4*>(starts + (j + 1) * state);
 #pragma unroll
     for (int i = 0; i < NQ; ++i) {
@@ -354,7 +354,7 @@ __global__ __launch_bounds__(4 * DK) void join_kernel(Joins all) {
 }
 template <int DK>
 hipError_t launch_join(const Joins& j, int directions, hipStream_t stream) {
-  hipLaunchKernelGGL((join_kernel<DK>), dim3((unsigned)(j.chains * (j.nv / 16)), directions), dim3(4 * DK), 0, stream, j);
+  hipLaunchKernelGGL((join_kernel<DK>), dim3(grid_of(j.nv / 16, j.chains), directions), dim3(4 * DK), 0, stream, j);
   return hipGetLastError();
 }
 

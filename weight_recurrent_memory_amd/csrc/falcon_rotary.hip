@@ -17,6 +17,25 @@ namespace falcon {
 using namespace rows;
 namespace {
 
+// 16 bytes of a row on their way, 0 where there is no row, and their values.
+template <typename T>
+__device__ __forceinline__ uint4 fetch(const T* x, bool in, long at) {
+  return in ? *reinterpret_cast<const uint4*>(x + at) : uint4{0u, 0u, 0u, 0u};
+}
+template <typename T>
+__device__ __forceinline__ void floats_of(const uint4& u, float (&x)[Vec<T>::V]) {
+  const uint32_t w[4] = {u.x, u.y, u.z, u.w};
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    if constexpr (sizeof(T) == 2) {
+      x[2 * i] = __uint_as_float(w[i] << 16);
+      x[2 * i + 1] = __uint_as_float(w[i] & 0xFFFF0000u);
+    } else {
+      x[i] = __uint_as_float(w[i]);
+    }
+  }
+}
+
 template <int D, int TT>
 struct Angles {
   alignas(16) float cos[TT][D / 2];
@@ -107,6 +126,8 @@ __device__ __forceinline__ void rotary_in_rows(const T* x, long ld, T* y, const 
   const long N = (long)a.batch * a.seqlen;
   const int rows = TT * a.heads;
   for (long tile = blockIdx.x; tile * TT < N; tile += gridDim.x) {
+    Row next = row_at<TT>(tile, (int)threadIdx.x / VPR, N, a.heads, a.seqlen);
+    uint4 raw = fetch<T>(x, next.in, next.tok * ld + (long)next.h * D + c);
     if (TURN) {
       __syncthreads();
       angles_of<D, TT>(lds.a, a.r, tile, N);
@@ -114,11 +135,13 @@ __device__ __forceinline__ void rotary_in_rows(const T* x, long ld, T* y, const 
     }
     for (int r0 = 0; r0 < rows; r0 += RPP) {
       const int at = r0 + (int)threadIdx.x / VPR;
-      const Row w = row_at<TT>(tile, at, N, a.heads, a.seqlen);
+      const Row w = next;
       float f[V];
-#pragma unroll
-      for (int i = 0; i < V; ++i) f[i] = 0.0f;
-      if (w.in) Vec<T>::load(x + w.tok * ld + (long)w.h * D + c, f);
+      floats_of<T>(raw, f);
+      if (r0 + RPP < rows) {
+        next = row_at<TT>(tile, at + RPP, N, a.heads, a.seqlen);
+        raw = fetch<T>(x, next.in, next.tok * ld + (long)next.h * D + c);
+      }
       if (TURN) {
         if (a.r.normalize) {
           float s = 0.0f;
