@@ -11,8 +11,8 @@
 //                                             - sum_{s>t} D_st b_s (du_s . u_t) k_s
 //   dbeta_t = du_t . v_t - y_t . k_t
 //   dlog_a_t = <a_t (R_t - dv_t k_t^T), S_{t-1}>, what passes the border before t;
-//   dlog_a_t - dlog_a_{t+1} = q_t . dq_t - v_t . dv_t, summed in float64 from <R, S> behind
-//   the chunk.  At a reset it is 0 and the sum begins anew.
+//   dlog_a_t - dlog_a_{t+1} = q_t . dq_t - v_t . dv_t, summed in float64 from <R, S'> behind
+//   the chunk, S' = d S + sum_s w_s u_s k_s^T.  At a reset it is 0 and the sum begins anew.
 //
 // Four launches: every chunk's T and its transpose; P^T dO and dO^T (e Q) of every chunk;
 // the walks, S and u from the first chunk on and R and du from the last one, side by side,
@@ -43,7 +43,7 @@ struct BwdArgs {
   float4* H;               // P^T dO: [chain][chunk][value tile][4][64], a walker's tiles
   float4* G;               // dO^T (e Q): [chain][chunk][value tile][dk / 16][64]
   float* U;                // [chain][L][dv]
-  float* S;                // [chain][chunks + 1][dv][dk]: before each chunk, and the last
+  float* S;                // [chain][chunks][dv][dk]: before each chunk
   float* R;                // [chain][chunks][dv][dk]: behind each chunk
   long chains;
   int seqlen, nv;
@@ -309,7 +309,7 @@ __global__ __launch_bounds__(64 * (ND + kKeyWaves), 2) void walks_kernel(BwdArgs
     Walker<T, DK> w;
     const T* v = static_cast<const T*>(a.v) + first * a.nv;
     const uint4* Tp = a.T + (chain * chunks + c0) * kT;
-    float* S = a.S + (chain * (chunks + 1) + c0) * state + at;
+    float* S = a.S + (chain * chunks + c0) * state + at;
     const float* U = a.U + first * a.nv;
     if (unit_rows) w.S.unit(row);
     else if (WRITE) w.S.load(nullptr);
@@ -337,9 +337,8 @@ __global__ __launch_bounds__(64 * (ND + kKeyWaves), 2) void walks_kernel(BwdArgs
               [](int, const floatx4 (&)[4]) {});
     }
     __syncthreads();
-    if (!WRITE) {
-      if (seg == a.segs - 1) w.S.store(S + n * state);
-    } else if (unit_rows) {
+    if (!WRITE) return;
+    if (unit_rows) {
       if (row >= DK) return;
       w.S.store_transposed(a.moves + unit * DK * DK, row);
       w.S.store(a.moves_t + unit * DK * DK + at);
@@ -483,13 +482,13 @@ __global__ __launch_bounds__(256, (DK <= 64 ? 2 : 1)) void outputs_kernel(BwdArg
   const long state = (long)a.nv * DK;
   const Window wu(a.U + row * a.nv, left, a.nv, 0), wo(a.dO + row * a.nv, left, a.nv, 0),
       wd(a.dv + row * a.nv, left, a.nv, 0);
-  const float* S = a.S + (chain * (chunks + 1) + chunk) * state;
+  const float* S = a.S + (chain * chunks + chunk) * state;
   const float* R = a.R + (chain * chunks + chunk) * state;
   const T* v = static_cast<const T*>(a.v) + row * a.nv;
   const Window wv(v, left, a.nv, 0);
 
   StageValues su, so, sd;
-  StageState<DK> ss, sr, sn;
+  StageState<DK> ss, sr;
   GateLoad gl;
   Raw<T> rv;
   auto fetch = [&](int col) {
@@ -498,7 +497,6 @@ __global__ __launch_bounds__(256, (DK <= 64 ? 2 : 1)) void outputs_kernel(BwdArg
     sd.load(wd, a.nv, col);
     ss.load(S + (long)col * DK, a.nv - col);
     sr.load(R + (long)col * DK, a.nv - col);
-    if (a.dlog_a) sn.load(S + state + (long)col * DK, a.nv - col);
     rv.load(wv, col + 8 * (threadIdx.x & 3) < a.nv
                     ? ((threadIdx.x >> 2) * a.nv + col + 8 * (threadIdx.x & 3)) * (int)sizeof(T) : kNowhere);
   };
@@ -518,7 +516,7 @@ __global__ __launch_bounds__(256, (DK <= 64 ? 2 : 1)) void outputs_kernel(BwdArg
   const Window wk(static_cast<const T*>(a.k) + row * DK, left, DK, 0),
       wq(static_cast<const T*>(a.q) + row * DK, left, DK, 0);
   float duv = 0.0f;                  // of token threadIdx.x / 4: du . v over this thread's columns
-  double X = 0.0;
+  double X = 0.0;                    // <R, S> of this thread's part
   for (int col = 0; col < a.nv; col += kSlice) {
     if (col) __syncthreads();
     su.store(lds.a.u[0]);
@@ -526,7 +524,7 @@ __global__ __launch_bounds__(256, (DK <= 64 ? 2 : 1)) void outputs_kernel(BwdArg
     sd.store(lds.a.d[0]);
     ss.store(lds.a.s[0]);
     sr.store(lds.a.r[0]);
-    if (a.dlog_a) X += sr.dot(sn);
+    if (a.dlog_a) X += sr.dot(ss);
     __syncthreads();
     // dv = b du, and du . v
     {
@@ -595,14 +593,26 @@ __global__ __launch_bounds__(256, (DK <= 64 ? 2 : 1)) void outputs_kernel(BwdArg
   duv += __shfl_xor(duv, 1, 64);
   duv += __shfl_xor(duv, 2, 64);
   if ((threadIdx.x & 3) == 0) lds.step[threadIdx.x >> 2] = duv;
+  const int ti = 16 * wave + m;      // this lane's token
   if (a.dlog_a) {
+    // what passes the border behind the chunk: <R, d S + sum_s w_s u_s k_s^T>, of which
+    // k_s . (R^T u_s) is on the way to dk
+    double sum = 0.0;
+#pragma unroll
+    for (int j = 0; j < NK; ++j) {
+      Raw4<T> rk;
+      rk.load(wk, (ti * DK + 16 * j + 4 * g) * (int)sizeof(T));
+      const floatx4 kv = rk.values();
+#pragma unroll
+      for (int r = 0; r < 4; ++r) sum += (double)kv[r] * dk[j][r];
+    }
+    X = lds.gate.d * X + lds.gate.w[ti] * sum;
 #pragma unroll
     for (int i = 32; i >= 1; i >>= 1) X += __shfl_xor(X, i, 64);
     if (lane == 0) lds.x[wave] = X;
   }
   __syncthreads();
 
-  const int ti = 16 * wave + m;      // this lane's token
   const float2 Gt = lds.gate.g[ti];
   const float e = lds.gate.e[ti], w = lds.gate.w[ti], b = lds.gate.b[ti];
   duv = lds.step[ti];
@@ -723,7 +733,7 @@ Plan plan_of(const DeltaBwdArgs& a) {
   p.H = units * C * a.ndv * 4;
   p.G = units * state;
   p.U = (size_t)p.chains * a.seqlen * a.ndv * 4;
-  p.S = (units + p.chains) * state;
+  p.S = units * state;
   p.R = units * state;
   // segments: walked twice, and the first time with dk unit rows more
   const long walks = p.chains * (2 * ((a.ndv + 63) / 64) + (a.ndk + 63) / 64);
