@@ -243,7 +243,7 @@ constexpr int waves_of() { return OUT && planes<T>() == 3 && DK == 128 ? 1 : 2; 
 template <typename T, int DK, int ND, bool OUT>
 __global__ __launch_bounds__(threads_of(ND, OUT), (waves_of<T, DK, ND, OUT>())) void walk_kernel(WalkArgs a) {
   extern __shared__ __align__(16) unsigned char smem[];
-  using L = typename std::conditional<OUT, WalkLds<T, DK, ND>, StateLds<T, DK>>::type;
+  using L = typename std::conditional<OUT, WalkLds<T, DK, ND>, KeyLds<T, DK>>::type;
   constexpr int DZ = 16 * ND;
   L& lds = *reinterpret_cast<L*>(smem);
   const int vblocks = a.nv / DZ, blocks = OUT ? vblocks : vblocks + (DK + DZ - 1) / DZ;
@@ -262,7 +262,7 @@ __global__ __launch_bounds__(threads_of(ND, OUT), (waves_of<T, DK, ND, OUT>())) 
 
   if (wave < ND) {
     const int row = row0 + 16 * wave;          // (unit rows behind the last one are zeros)
-    Walker<T, DK> w;
+    Walker<T, DK, typename std::conditional<OUT, RegT, LdsT>::type> w;
     const T* v = static_cast<const T*>(a.v) + (chain * len + c0 * C) * a.nv;
     const uint4* Tp = a.T + (chain * chunks + c0) * kT;
     const long state = (long)a.nv * DK;
@@ -270,7 +270,7 @@ __global__ __launch_bounds__(threads_of(ND, OUT), (waves_of<T, DK, ND, OUT>())) 
     else if (!OUT) w.S.load(nullptr);
     else if (a.segs > 1) w.S.load(a.starts + (chain * a.segs + seg) * state + (long)row * DK);
     else w.S.load(a.S0 ? a.S0 + chain * state + (long)row * DK : nullptr);
-    w.load_T(Tp);
+    if constexpr (OUT) w.t.load(Tp);
     // (unit rows have no v: a window of no rows reads 0)
     auto load_v = [&](int c) {
       w.load_v(v + (long)c * C * a.nv, unit_rows ? 0 : left - (long)c * C, a.nv, row);
@@ -281,11 +281,12 @@ __global__ __launch_bounds__(threads_of(ND, OUT), (waves_of<T, DK, ND, OUT>())) 
       if (c == 0) w.load_k(lds.k[0][0]);
       // (what is behind the last chunk is loaded in its own place: no branch holds registers)
       const int next = c + 1 < n ? c + 1 : c;
+      if constexpr (!OUT) w.t.p = lds.t[c & 1];
       w.chunk(lds.k[c % L::R][0], lds.gate[c % L::R],
               [&] {
                 // (loads come back in order: the one needed first is issued first)
                 load_v(next);
-                w.load_T(Tp + (long)next * kT);
+                if constexpr (OUT) w.t.load(Tp + (long)next * kT);
               },
               [&] { w.load_k(lds.k[next % L::R][0]); },
               [&](int i, int p, const bf16x8& f) {
@@ -330,8 +331,8 @@ __global__ __launch_bounds__(threads_of(ND, OUT), (waves_of<T, DK, ND, OUT>())) 
       __syncthreads();
     } else {
       keys_only<T, DK, false>(lds, static_cast<const T*>(a.k) + (chain * len + c0 * C) * DK,
-                              a.log_a ? a.log_a + chain * len + c0 * C : nullptr, a.beta + chain * len + c0 * C, left,
-                              n, threadIdx.x - 64 * ND);
+                              a.log_a ? a.log_a + chain * len + c0 * C : nullptr, a.beta + chain * len + c0 * C,
+                              a.T + (chain * chunks + c0) * kT, left, n, threadIdx.x - 64 * ND);
     }
   }
   if constexpr (OUT) {
@@ -372,7 +373,7 @@ Plan plan_of(const DeltaArgs& a) {
 
 template <typename T, int DK, int ND, bool OUT>
 hipError_t go(const WalkArgs& a, hipStream_t stream) {
-  constexpr size_t bytes = OUT ? sizeof(WalkLds<T, DK, ND>) : sizeof(StateLds<T, DK>);
+  constexpr size_t bytes = OUT ? sizeof(WalkLds<T, DK, ND>) : sizeof(KeyLds<T, DK>);
   static_assert(bytes <= 163840, "LDS of a workgroup");
   auto kernel = walk_kernel<T, DK, ND, OUT>;
   const hipError_t e = lds_limit(kernel, bytes);

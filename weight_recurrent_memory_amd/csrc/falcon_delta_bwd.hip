@@ -170,16 +170,9 @@ template <typename T, int DK>
 struct BackWalker {
   static constexpr int NP = planes<T>(), NQ = (DK + 31) / 32, NK = DK / 16;
   StateT<DK> R;
-  bf16x8 T_[kFrags][3];
+  LdsT t;
   floatx4 h[4], G[NK];
 
-  __device__ __forceinline__ void load_T(const uint4* p) {
-    const int lane = threadIdx.x & 63;
-#pragma unroll
-    for (int f = 0; f < kFrags; ++f)
-#pragma unroll
-      for (int n = 0; n < 3; ++n) T_[f][n] = __builtin_bit_cast(bf16x8, p[(f * 3 + n) * 64 + lane]);
-  }
   __device__ __forceinline__ void load_h(const float4* p) {
 #pragma unroll
     for (int i = 0; i < 4; ++i) h[i] = *reinterpret_cast<const floatx4*>(p + i * 64 + (threadIdx.x & 63));
@@ -224,9 +217,11 @@ struct BackWalker {
 #pragma unroll
       for (int p = 0; p < 3; ++p)
 #pragma unroll
-        for (int r = 0; p + r < 3; ++r)
+        for (int i = 0; i < 2 * j + 2; ++i) {
+          const bf16x8 tf = t.get(frag_of(3 - i, 1 - j), p);
 #pragma unroll
-          for (int i = 0; i < 2 * j + 2; ++i) u[i] = mfma16(T_[frag_of(3 - i, 1 - j)][p], f[r], u[i]);
+          for (int r = 0; p + r < 3; ++r) u[i] = mfma16(tf, f[r], u[i]);
+        }
     }
     // (keeps the next part's reads in that part: registers)
     __builtin_amdgcn_sched_barrier(0);
@@ -282,7 +277,7 @@ __device__ __forceinline__ void store_values(const float* p, int nv, int col, lo
 template <typename T, int DK, int ND, bool WRITE>
 __global__ __launch_bounds__(64 * (ND + kKeyWaves), 2) void walks_kernel(BwdArgs a, int chunks) {
   extern __shared__ __align__(16) unsigned char smem[];
-  using L = StateLds<T, DK>;
+  using L = KeyLds<T, DK>;
   constexpr int DZ = 16 * ND, NK = DK / 16;
   L& lds = *reinterpret_cast<L*>(smem);
   const int vblocks = a.nv / DZ;
@@ -299,23 +294,21 @@ __global__ __launch_bounds__(64 * (ND + kKeyWaves), 2) void walks_kernel(BwdArgs
   if (wave >= ND) {
     const T* k = static_cast<const T*>(a.k) + first * DK;
     const float* la = a.log_a ? a.log_a + first : nullptr;
-    if (back) keys_only<T, DK, true>(lds, k, la, a.beta + first, left, n, threadIdx.x - 64 * ND);
-    else keys_only<T, DK, false>(lds, k, la, a.beta + first, left, n, threadIdx.x - 64 * ND);
+    if (back) keys_only<T, DK, true>(lds, k, la, a.beta + first, a.Tt + (chain * chunks + c0) * kT, left, n, threadIdx.x - 64 * ND);
+    else keys_only<T, DK, false>(lds, k, la, a.beta + first, a.T + (chain * chunks + c0) * kT, left, n, threadIdx.x - 64 * ND);
     return;
   }
   const int row = row0 + 16 * wave;            // (unit rows behind the last one are zeros)
   const long state = (long)a.nv * DK, at = (long)row * DK;
   if (!back) {
-    Walker<T, DK> w;
+    Walker<T, DK, LdsT> w;
     const T* v = static_cast<const T*>(a.v) + first * a.nv;
-    const uint4* Tp = a.T + (chain * chunks + c0) * kT;
     float* S = a.S + (chain * chunks + c0) * state + at;
     const float* U = a.U + first * a.nv;
     if (unit_rows) w.S.unit(row);
     else if (WRITE) w.S.load(nullptr);
     else if (a.segs > 1) w.S.load(a.starts_S + unit * state + at);
     else w.S.load(a.S0 ? a.S0 + chain * state + at : nullptr);
-    w.load_T(Tp);
     auto load_v = [&](int c) {
       w.load_v(v + (long)c * C * a.nv, unit_rows ? 0 : left - (long)c * C, a.nv, row);
     };
@@ -325,11 +318,9 @@ __global__ __launch_bounds__(64 * (ND + kKeyWaves), 2) void walks_kernel(BwdArgs
       if (c == 0) w.load_k(lds.k[0][0]);
       const int next = c + 1 < n ? c + 1 : c;
       if (!WRITE) w.S.store(S + c * state);
+      w.t.p = lds.t[c & 1];
       w.chunk(lds.k[c % L::R][0], lds.gate[c % L::R],
-              [&] {
-                load_v(next);
-                w.load_T(Tp + (long)next * kT);
-              },
+              [&] { load_v(next); },
               [&] { w.load_k(lds.k[next % L::R][0]); }, [](int, int, const bf16x8&) {},
               [&](const floatx4 (&u)[4]) {
                 if (!WRITE) store_values(U + (long)c * C * a.nv, a.nv, row, left - (long)c * C, u);
@@ -349,7 +340,6 @@ __global__ __launch_bounds__(64 * (ND + kKeyWaves), 2) void walks_kernel(BwdArgs
   }
   BackWalker<T, DK> w;
   const int tiles = a.nv / 16, z = row / 16;
-  const uint4* Tp = a.Tt + (chain * chunks + c0) * kT;
   const float4* H = a.H + ((chain * chunks + c0) * tiles + z) * 4 * 64;
   const float4* G = a.G + ((chain * chunks + c0) * tiles + z) * NK * 64;
   float* R = a.R + (chain * chunks + c0) * state + at;
@@ -359,17 +349,14 @@ __global__ __launch_bounds__(64 * (ND + kKeyWaves), 2) void walks_kernel(BwdArgs
   else if (a.segs > 1) w.R.load(a.starts_R + step * state + at);
   else w.R.load(a.dS_L ? a.dS_L + chain * state + at : nullptr);
   w.load_h(H + (long)(n - 1) * tiles * 4 * 64);
-  w.load_T(Tp + (long)(n - 1) * kT);
   w.load_G(G + (long)(n - 1) * tiles * NK * 64);
   for (int i = 0; i < n; ++i) {
     __syncthreads();
     const int c = n - 1 - i, next = c > 0 ? c - 1 : 0;
     if (!WRITE) w.R.store(R + c * state);
+    w.t.p = lds.t[i & 1];
     w.chunk(lds.k[i % L::R][0], lds.gate[i % L::R],
-            [&] {
-              w.load_h(H + (long)next * tiles * 4 * 64);
-              w.load_T(Tp + (long)next * kT);
-            },
+            [&] { w.load_h(H + (long)next * tiles * 4 * 64); },
             [&] { w.load_G(G + (long)next * tiles * NK * 64); },
             [&](const floatx4 (&u)[4]) {
               if (!WRITE) store_values(du + (long)c * C * a.nv, a.nv, row, left - (long)c * C, u);
@@ -792,14 +779,14 @@ hipError_t run(const DeltaBwdArgs& a, const Plan& p, hipStream_t stream) {
       const int vblocks = a.ndv / (16 * ND), ublocks = (DK + 16 * ND - 1) / (16 * ND);
       if (p.segs > 1) {
         hipError_t e = go(walks_kernel<T, DK, ND, true>, grid_of(2 * vblocks + ublocks, p.chains * p.segs), threads,
-                          sizeof(StateLds<T, DK>), stream, w, n);
+                          sizeof(KeyLds<T, DK>), stream, w, n);
         if (e != hipSuccess) return e;
         const Joins j{{{a.S0, w.starts_S, w.moves, false}, {a.dS_L, w.starts_R, w.moves_t, true}},
                       p.chains, a.ndv, p.segs};
         if ((e = launch_join<DK>(j, 2, stream)) != hipSuccess) return e;
       }
       return go(walks_kernel<T, DK, ND, false>, grid_of(2 * vblocks, p.chains * p.segs), threads,
-                sizeof(StateLds<T, DK>), stream, w, n);
+                sizeof(KeyLds<T, DK>), stream, w, n);
     };
     e = a.ndv >= 64   ? walks(std::integral_constant<int, 4>())
         : a.ndv == 32 ? walks(std::integral_constant<int, 2>())

@@ -19,6 +19,33 @@ struct StateLds {
   Gates gate[R];
   alignas(16) unsigned char bad[4];
 };
+// The same with T, for workgroups of walkers alone: one read of T from memory serves them all
+// (each wave with T in registers reads its own 18 KB a chunk: us of the gradients' walks at
+// 8x12x2048x64 PLACEHOLDER).
+template <typename T, int DK>
+struct KeyLds : StateLds<T, DK> {
+  alignas(16) uint4 t[2][kT];
+};
+
+// T's operands as a walker has them: read ahead into registers, or from LDS where they are used.
+struct RegT {
+  bf16x8 f[kFrags][3];
+  __device__ __forceinline__ void load(const uint4* p) {
+    const int lane = threadIdx.x & 63;
+#pragma unroll
+    for (int i = 0; i < kFrags; ++i)
+#pragma unroll
+      for (int n = 0; n < 3; ++n) f[i][n] = __builtin_bit_cast(bf16x8, p[(i * 3 + n) * 64 + lane]);
+  }
+  __device__ __forceinline__ bf16x8 get(int i, int n) const { return f[i][n]; }
+};
+struct LdsT {
+  const uint4* p;
+  __device__ __forceinline__ bf16x8 get(int i, int n) const {
+    return __builtin_bit_cast(bf16x8, p[(i * 3 + n) * 64 + (threadIdx.x & 63)]);
+  }
+};
+
 // S^T: 16 value rows, columns of keys in tiles of 16.
 template <int DK>
 struct StateT {
@@ -63,20 +90,13 @@ struct StateT {
 };
 
 // The wave that owns 16 value rows: S through the chunks of a segment.
-template <typename T, int DK>
+template <typename T, int DK, class TT>
 struct Walker {
   static constexpr int NP = planes<T>(), NQ = (DK + 31) / 32, NK = DK / 16;
   StateT<DK> S;
-  bf16x8 T_[kFrags][3];
+  TT t;
   float v[16];
 
-  __device__ __forceinline__ void load_T(const uint4* p) {
-    const int lane = threadIdx.x & 63;
-#pragma unroll
-    for (int f = 0; f < kFrags; ++f)
-#pragma unroll
-      for (int n = 0; n < 3; ++n) T_[f][n] = __builtin_bit_cast(bf16x8, p[(f * 3 + n) * 64 + lane]);
-  }
   // v: the sequence's rows from the chunk's first token on; col: of the 16 rows' first
   __device__ __forceinline__ void load_v(const T* p, long rows, int nv, int col) {
     const int m = threadIdx.x & 15, g = (threadIdx.x & 63) >> 4;
@@ -144,9 +164,11 @@ struct Walker {
 #pragma unroll
       for (int p = 0; p < 3; ++p)
 #pragma unroll
-        for (int r = 0; p + r < 3; ++r)
+        for (int i = 2 * j; i < 4; ++i) {
+          const bf16x8 tf = t.get(frag_of(i, j), p);
 #pragma unroll
-          for (int i = 2 * j; i < 4; ++i) u[i] = mfma16(T_[frag_of(i, j)][p], xf[r], u[i]);
+          for (int r = 0; p + r < 3; ++r) u[i] = mfma16(tf, xf[r], u[i]);
+        }
     }
     load();
     values(u);
@@ -239,17 +261,40 @@ struct Keys {
   }
 };
 
-constexpr int kKeyWaves = 2;             // of a workgroup without outputs
+constexpr int kKeyWaves = 2;             // of a workgroup without outputs: these bring T, too
+// T on its way to LDS.
+template <int NTH>
+struct StageT {
+  static constexpr int N = kT / NTH;
+  static_assert(kT % NTH == 0, "whole units of T a thread");
+  uint4 r[N];
+  __device__ __forceinline__ void load(const uint4* p) {
+#pragma unroll
+    for (int i = 0; i < N; ++i) r[i] = p[i * NTH];
+  }
+  __device__ __forceinline__ void store(uint4* p) const {
+#pragma unroll
+    for (int i = 0; i < N; ++i) p[i * NTH] = r[i];
+  }
+};
+// T_: the walk's first chunk's in memory (REV: the last one walked)
 template <typename T, int DK, bool REV>
-__device__ __forceinline__ void keys_only(StateLds<T, DK>& lds, const T* k, const float* la, const float* be,
-                                          long left, int n, int t) {
+__device__ __forceinline__ void keys_only(KeyLds<T, DK>& lds, const T* k, const float* la, const float* be,
+                                          const uint4* T_, long left, int n, int t) {
+  StageT<64 * kKeyWaves> st;
+  T_ += t;
+  st.load(T_ + (long)(REV ? n - 1 : 0) * kT);
   Keys<T, DK, 64 * kKeyWaves, REV> keys(lds, k, la, be, left, n, t);
+  st.store(lds.t[0] + t);
   for (int c = 0; c < n; ++c) {
     __syncthreads();
+    const int next = c + 1 < n ? c + 1 : c;
+    st.load(T_ + (long)(REV ? n - 1 - next : next) * kT);
     if (c + keys.D < n) {
       keys.load(c + keys.D);
       keys.store(lds, c + keys.D);
     }
+    st.store(lds.t[(c + 1) & 1] + t);
   }
   __syncthreads();
 }
