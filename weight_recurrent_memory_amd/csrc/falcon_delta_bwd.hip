@@ -455,7 +455,22 @@ struct StageState {
   }
 };
 
-// One chunk; wave w owns tokens 16 w.. (as columns m of its results).
+// Four values of NP planes in LDS.
+template <int NP>
+__device__ __forceinline__ floatx4 row_values(const uint16_t* p, int stride) {
+  floatx4 x = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+  for (int i = NP - 1; i >= 0; --i) {
+    Raw4<uint16_t> r;
+    r.u = *reinterpret_cast<const uint2*>(p + i * stride);
+    x += r.values();
+  }
+  return x;
+}
+
+// One chunk; wave w owns tokens 16 w.. (as columns m of its results).  (Eight waves, half of them
+// for the rows behind a token, hold one chunk a compute unit in place of two: 181 us against 143
+// at 8x12x2048x64.)
 template <typename T, int DK>
 __global__ __launch_bounds__(256, (DK <= 64 ? 2 : 1)) void outputs_kernel(BwdArgs a, int chunks) {
   extern __shared__ __align__(16) unsigned char smem[];
@@ -580,6 +595,8 @@ __global__ __launch_bounds__(256, (DK <= 64 ? 2 : 1)) void outputs_kernel(BwdArg
   duv += __shfl_xor(duv, 1, 64);
   duv += __shfl_xor(duv, 2, 64);
   if ((threadIdx.x & 3) == 0) lds.step[threadIdx.x >> 2] = duv;
+  __syncthreads();
+
   const int ti = 16 * wave + m;      // this lane's token
   if (a.dlog_a) {
     // what passes the border behind the chunk: <R, d S + sum_s w_s u_s k_s^T>, of which
@@ -587,9 +604,7 @@ __global__ __launch_bounds__(256, (DK <= 64 ? 2 : 1)) void outputs_kernel(BwdArg
     double sum = 0.0;
 #pragma unroll
     for (int j = 0; j < NK; ++j) {
-      Raw4<T> rk;
-      rk.load(wk, (ti * DK + 16 * j + 4 * g) * (int)sizeof(T));
-      const floatx4 kv = rk.values();
+      const floatx4 kv = row_values<NP>(lds.b.k[0] + at<DK>(ti, 16 * j + 4 * g), C * DK);
 #pragma unroll
       for (int r = 0; r < 4; ++r) sum += (double)kv[r] * dk[j][r];
     }
@@ -598,8 +613,6 @@ __global__ __launch_bounds__(256, (DK <= 64 ? 2 : 1)) void outputs_kernel(BwdArg
     for (int i = 32; i >= 1; i >>= 1) X += __shfl_xor(X, i, 64);
     if (lane == 0) lds.x[wave] = X;
   }
-  __syncthreads();
-
   const float2 Gt = lds.gate.g[ti];
   const float e = lds.gate.e[ti], w = lds.gate.w[ti], b = lds.gate.b[ti];
   duv = lds.step[ti];
@@ -667,10 +680,8 @@ __global__ __launch_bounds__(256, (DK <= 64 ? 2 : 1)) void outputs_kernel(BwdArg
   float qdq = 0.0f, yk = 0.0f;
 #pragma unroll
   for (int j = 0; j < NK; ++j) {
-    Raw4<T> rq, rk;
-    rq.load(wq, (ti * DK + 16 * j + 4 * g) * (int)sizeof(T));
-    rk.load(wk, (ti * DK + 16 * j + 4 * g) * (int)sizeof(T));
-    const floatx4 qv = rq.values(), kv = rk.values();
+    const floatx4 qv = row_values<NP>(lds.b.q[0] + at<DK>(ti, 16 * j + 4 * g), C * DK);
+    const floatx4 kv = row_values<NP>(lds.b.k[0] + at<DK>(ti, 16 * j + 4 * g), C * DK);
 #pragma unroll
     for (int r = 0; r < 4; ++r) {
       qdq += qv[r] * dq[j][r];
