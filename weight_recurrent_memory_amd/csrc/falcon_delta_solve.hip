@@ -120,8 +120,9 @@ __global__ __launch_bounds__(64 * kWaves) void solve_kernel(SolveArgs a, int chu
     }
   }
   wave_order();
-  for (int i = lane; i < C * kPitch / 4; i += 64) reinterpret_cast<floatx4*>(lds.t)[i] = zero;
-  wave_order();
+  // (of the tiles above the diagonal two are read)
+  *reinterpret_cast<floatx4*>(lds.t + m * kPitch + 16 + 4 * g) = zero;
+  *reinterpret_cast<floatx4*>(lds.t + (32 + m) * kPitch + 48 + 4 * g) = zero;
 #pragma unroll
   for (int t = 0; t < 16; ++t) lds.t[(16 * g + t) * kPitch + 16 * g + m] = x[t];
   wave_order();
