@@ -364,7 +364,7 @@ Plan plan_of(const DeltaArgs& a) {
   p.nd = a.dv >= 32 ? 2 : 1;
   if (a.dtype != 0 && a.dk == 128) p.nd = 1;
   // segments: walked twice, and the first time with dk unit rows more
-  cut(chunks, p.chains * ((a.dv + a.dk + 63) / 64), p.segs, p.per);
+  cut(chunks, p.chains * ((a.dv + a.dk + 63) / 64), a.dk, p.segs, p.per);
   p.T_bytes = (size_t)p.chains * chunks * kT * 16;
   p.starts = p.segs > 1 ? (size_t)p.chains * p.segs * a.dv * a.dk * 4 : 0;
   p.moves = p.segs > 1 ? (size_t)p.chains * p.segs * a.dk * a.dk * 4 : 0;

@@ -735,7 +735,7 @@ Plan plan_of(const DeltaBwdArgs& a) {
   p.R = units * state;
   // segments: walked twice, and the first time with dk unit rows more
   const long walks = p.chains * (2 * ((a.ndv + 63) / 64) + (a.ndk + 63) / 64);
-  cut(p.chunks, walks, p.segs, p.per);
+  cut(p.chunks, walks, a.ndk, p.segs, p.per);
   p.starts = p.segs > 1 ? (size_t)p.chains * p.segs * state : 0;
   p.moves = p.segs > 1 ? (size_t)p.chains * p.segs * a.ndk * a.ndk * 4 : 0;
   return p;

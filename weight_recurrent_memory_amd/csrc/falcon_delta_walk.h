@@ -19,9 +19,9 @@ struct StateLds {
   Gates gate[R];
   alignas(16) unsigned char bad[4];
 };
-// The same with T, for workgroups of walkers alone: one read of T from memory serves them all
-// (each wave with T in registers reads its own 18 KB a chunk: us of the gradients' walks at
-// 8x12x2048x64 PLACEHOLDER).
+// The same with T, for workgroups of walkers alone: one read of T from memory serves them all, and
+// the walkers' registers are free of it (each with T in its own: 32 us in place of 26 for the
+// gradients' walks at 1x5x4099, 128x64).
 template <typename T, int DK>
 struct KeyLds : StateLds<T, DK> {
   alignas(16) uint4 t[2][kT];
@@ -305,14 +305,20 @@ __device__ __forceinline__ void keys_only(KeyLds<T, DK>& lds, const T* k, const 
 // walks every segment from zero (N) and from unit rows (M), a second joins them in order, the
 // main walk then starts each segment from its state.  R -> R M^T + N' for the gradient's.
 
-// units: workgroups of the first launch over all chains for one segment each.
-constexpr long kWhole = 16, kSlots = 256;
-inline void cut(long chunks, long units, int& segs, int& per) {
+// units: workgroups of the first launch over all chains for one segment each, of which the GPU
+// holds 256 (one a compute unit, a walker a SIMD); segments have two chunks at least.  Sequences of fewer
+// chunks than kWhole, and those whose chains alone take more than a quarter of the GPU, are walked
+// whole.  Measured, us of a call cut and whole, forward and gradients: 1x16x4096x64 66 and 137, 153 and
+// 235; 1x8x2048x64 45 and 76, 70 and 120; 1x3x3000x32 34 and 88, 52 and 125; 1x2x640x64 31 and 33, 51
+// and 58; 1x16x2048x128 86 and 113, 216 and 218; but 1x1x512x128 42 and 39, 79 and 75 (the joins at 128
+// columns take longest).  With 512 slots 1x16x4096x64 takes 76 and 163.
+constexpr long kWhole = 10, kWholeWide = 16, kSlots = 256;
+inline void cut(long chunks, long units, int dk, int& segs, int& per) {
   segs = 1;
   per = (int)chunks;
-  if (chunks < kWhole || units > kSlots / 4) return;
+  if (chunks < (dk == 128 ? kWholeWide : kWhole) || units > kSlots / 4) return;
   long n = kSlots / units;
-  if (n > chunks / 4) n = chunks / 4;
+  if (n > chunks / 2) n = chunks / 2;
   per = (int)((chunks + n - 1) / n);
   segs = (int)((chunks + per - 1) / per);
 }
