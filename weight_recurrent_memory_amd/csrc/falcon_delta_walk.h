@@ -267,16 +267,19 @@ template <int NTH>
 struct StageT {
   static constexpr int N = kT / NTH;
   static_assert(kT % NTH == 0, "whole units of T a thread");
-  uint4 r[N];
+  uint4_t r[N];            // (a plain vector: an array of HIP's own type stays in memory)
   __device__ __forceinline__ void load(const uint4* p) {
 #pragma unroll
-    for (int i = 0; i < N; ++i) r[i] = p[i * NTH];
+    for (int i = 0; i < N; ++i) r[i] = *reinterpret_cast<const uint4_t*>(p + i * NTH);
   }
   __device__ __forceinline__ void store(uint4* p) const {
 #pragma unroll
-    for (int i = 0; i < N; ++i) p[i * NTH] = r[i];
+    for (int i = 0; i < N; ++i) *reinterpret_cast<uint4_t*>(p + i * NTH) = r[i];
   }
 };
+// What a step stores was loaded in the step before it, so that a load has a chunk's time to come
+// back (loaded and stored in one step the walkers waited for it at every chunk: PLACEHOLDER).  Behind
+// the last chunk it is loaded and stored once more, to places that are not read: no branches.
 // T_: the walk's first chunk's in memory (REV: the last one walked)
 template <typename T, int DK, bool REV>
 __device__ __forceinline__ void keys_only(KeyLds<T, DK>& lds, const T* k, const float* la, const float* be,
@@ -285,16 +288,23 @@ __device__ __forceinline__ void keys_only(KeyLds<T, DK>& lds, const T* k, const 
   T_ += t;
   st.load(T_ + (long)(REV ? n - 1 : 0) * kT);
   Keys<T, DK, 64 * kKeyWaves, REV> keys(lds, k, la, be, left, n, t);
+  constexpr int D = keys.D;
   st.store(lds.t[0] + t);
+  const int last = n - 1;
+  {
+    const int next = n > 1 ? 1 : 0;
+    st.load(T_ + (long)(REV ? last - next : next) * kT);
+  }
+  keys.load(D < n ? D : last);
   for (int c = 0; c < n; ++c) {
     __syncthreads();
-    const int next = c + 1 < n ? c + 1 : c;
-    st.load(T_ + (long)(REV ? n - 1 - next : next) * kT);
-    if (c + keys.D < n) {
-      keys.load(c + keys.D);
-      keys.store(lds, c + keys.D);
-    }
     st.store(lds.t[(c + 1) & 1] + t);
+    keys.store(lds, c + D);
+    __builtin_amdgcn_sched_barrier(0);
+    const int next = c + 2 < n ? c + 2 : last;
+    st.load(T_ + (long)(REV ? last - next : next) * kT);
+    keys.load(c + D + 1 < n ? c + D + 1 : last);
+    __builtin_amdgcn_sched_barrier(0);
   }
   __syncthreads();
 }
