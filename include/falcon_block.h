@@ -36,7 +36,9 @@ extern "C" {
  * (0 <= beta_t |k_t|^2 <= 2 and log_a <= 0: unit keys and a sigmoid's beta are): products
  * run on bf16 matrix cores with float32 operands in three bf16 parts, decays as differences of
  * float64 sums.  Outside of that range S may grow by a factor a token, and so do its
- * roundings.  A NaN or an infinity reaches the outputs that read it, o of its token and of
+ * roundings; a growth that float32 does not hold gives infinities and NaN, also of a state
+ * of zeros (a long sequence of few heads is walked in segments, each of which forms the
+ * matrix that it applies).  A NaN or an infinity reaches the outputs that read it, o of its token and of
  * later ones and S_out, and no others: rows of padding behind a sequence may hold
  * anything.  (A reset does not clear it: 0 * NaN.  Segments that hold one, or start
  * from one, are walked again token by token, which takes many times as long.)

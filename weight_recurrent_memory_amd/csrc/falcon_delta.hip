@@ -1,4 +1,19 @@
 // falcon_delta.hip - forward of the gated delta rule over a sequence (falcon_delta.h).
+//
+// A first launch forms every chunk's T (falcon_delta_solve.hip), a second walks: a workgroup has
+// ND waves of 16 value rows each (falcon_delta_walk.h) and 2 ND waves beside them, which bring keys,
+// q and gates, form the decayed scores and, one chunk behind, o^T = e (S q^T) + U^T P^T from the
+// state's and u's operands that the walkers leave in LDS.  The outputs so come from operands that
+// exist anyway, and u never goes to memory.
+//
+// 8x12x2048x64 bf16: 21 + 75 us of kernels, 90-99 us a call; memory would take 25 us (the walk
+// moves 128 MB over the fabric).  Bound by the walk's latency: 32 chunks in order on 192 workgroups.
+// 1x4x32771x128 in 16 segments: T 23, segments' writes 104, joins 41, walk 117 us (walked whole 1985 us).
+// Not built, for their traffic: u written to memory and the outputs in a launch of their own (2.3
+// times as much); T (b V) and T (b e K) formed beforehand in place of T, which shortens the chain by 12
+// matrix instructions and one split and costs 40 KB a chunk.  Tried: half the output waves (us of
+// the walk: 105 against 77); output waves that branch on their token tiles instead of having them as
+// constants (107 against 105).
 #include "falcon_delta_walk.h"
 
 namespace falcon {

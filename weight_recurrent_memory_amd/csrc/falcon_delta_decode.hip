@@ -5,7 +5,9 @@
 // Every row of S (a value channel) is updated and read by itself, so one pass reads S,
 // forms S k and S q, writes S' and o, and a head's rows may be split over workgroups.
 // Bound by HBM: 8 dk dv bytes of state per head, under one flop per byte.  A row lies on
-// dk / 4 lanes, 16 bytes each.
+// dk / 4 lanes, 16 bytes each.  512 x 12 x 64 x 64: 34.9 us a step = 5.9 TB/s (part of the 100 MB state
+// stays in the Infinity Cache between steps; a copy of 1 GiB moves 5.1 to 5.25 TB/s);
+// 1 x 12 x 128 x 128: 3.0 us, a launch's latency (9.3 us a call with the binding's host time).
 #include "falcon_block_launch.h"
 #include "falcon_device.h"
 

@@ -1,5 +1,13 @@
 // falcon_delta_walk.h - the wave that walks a sequence's chunks in order with 16 value rows of
-// the gated delta rule's state, and the waves that bring keys and gates to LDS for it.
+// the gated delta rule's state, the waves that bring keys and gates to LDS for it, and the
+// segments of a long sequence.
+//
+// The walk S -> X -> U -> S is one chain of dependent products, so its latency counts, not its
+// operations: a chunk takes a wave 2.2 us at 64 columns (84 matrix and about 430 vector
+// instructions, of which 352 split float32 values into bf16 planes; some 75% of the time is
+// issue) and 3.4 us at 128, whatever else the compute unit does.  Value rows do not
+// depend on each other: each wave takes 16, and there is no exchange and no barrier inside a
+// chunk, one barrier a chunk for keys and gates.
 #pragma once
 #include "falcon_delta.h"
 
@@ -278,7 +286,8 @@ struct StageT {
   }
 };
 // What a step stores was loaded in the step before it, so that a load has a chunk's time to come
-// back (loaded and stored in one step the walkers waited for it at every chunk: PLACEHOLDER).  Behind
+// back (loaded and stored in one step the walkers waited for it: 136 us in place of 127 for the
+// gradients' walks at 8x12x2048x64).  Behind
 // the last chunk it is loaded and stored once more, to places that are not read: no branches.
 // T_: the walk's first chunk's in memory (REV: the last one walked)
 template <typename T, int DK, bool REV>
