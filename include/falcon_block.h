@@ -40,7 +40,8 @@ extern "C" {
  * of zeros (a long sequence of few heads is walked in segments, each of which forms the
  * matrix that it applies).  A NaN or an infinity reaches the outputs that read it, o of its token and of
  * later ones and S_out, and no others: rows of padding behind a sequence may hold
- * anything.  (A reset does not clear it: 0 * NaN.  Segments that hold one, or start
+ * anything.  (A reset does not clear it: 0 * NaN.  float32 inputs and states beyond bf16's
+ * 3.39e38 count as infinite.  Segments that hold one, or start
  * from one, are walked again token by token, which takes many times as long.)
  * batch * heads * max(dk, dv) * (L + 63) / 64 < 2^31 (FALCON_ERR_UNSUPPORTED from there on).
  *

@@ -116,6 +116,25 @@ def test_state_in_place_and_given_outputs(L):
     assert o2 is out and torch.equal(o, out) and torch.equal(S, kept)
 
 
+@pytest.mark.parametrize("start,end", [(False, True), (True, False), (False, False)])
+@pytest.mark.parametrize("L", [70, 1500])
+def test_gradients_of_either_end(start, end, L):
+    _check_backward(du.inputs(torch, 21, 1, 2, L, 32, 64, torch.bfloat16, start=start), dS_L=end)
+
+
+def test_gates_of_any_alignment():
+    """beta and log_a as views that start at an odd element."""
+    x = du.inputs(torch, 22, 1, 3, 130, 32, 32, torch.bfloat16)
+    want, wantb = _forward(x), _backward(x)
+    for n in ("beta", "log_a"):
+        room = torch.empty(x[n].numel() + 3, device="cuda")
+        room[3:].copy_(x[n].flatten())
+        x[n] = room[3:].view(1, 3, 130)
+        assert x[n].data_ptr() % 16
+    got = _backward(x)
+    assert torch.equal(_forward(x), want) and all(torch.equal(got[n], wantb[n]) for n in got)
+
+
 def test_rows_behind_the_outputs_stay():
     x = du.inputs(torch, 11, 1, 3, 70, 16, 16, torch.bfloat16)
     room = torch.full((3 * 70 * 16 + 64,), 7.0, device="cuda")
