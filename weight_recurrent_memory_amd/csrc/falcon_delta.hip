@@ -8,7 +8,7 @@
 //
 // 8x12x2048x64 bf16: 21 + 75 us of kernels, 90-99 us a call; memory would take 25 us (the walk
 // moves 128 MB over the fabric).  Bound by the walk's latency: 32 chunks in order on 192 workgroups.
-// 1x4x32771x128 in 16 segments: T 23, segments' writes 104, joins 41, walk 117 us (walked whole 1985 us).
+// 1x4x32771x128 in 16 segments: T 23, segments' writes 104, joins 27, walk 117 us (walked whole 1985 us).
 // Not built, for their traffic: u written to memory and the outputs in a launch of their own (2.3
 // times as much); T (b V) and T (b e K) formed beforehand in place of T, which shortens the chain by 12
 // matrix instructions and one split and costs 40 KB a chunk.  Tried: half the output waves (us of
@@ -32,8 +32,7 @@ struct WalkArgs {
   float* S_out;            // or null; may be S0
   float* starts;           // [chain][segs][dv][dk]: slot j + 1 first segment j's own write,
                            // then slot j the state that segment j starts from
-  float* moves;            // [chain][segs][dk][dk]: what a segment multiplies its start's
-                           // rows with, transposed
+  uint4* moves;            // [chain][segs][StateT::kMove]: what a segment multiplies its start's rows with
   long chains;
   int seqlen, nv;
   int segs, per;           // segments of a chain, chunks of one
@@ -333,7 +332,7 @@ __global__ __launch_bounds__(threads_of(ND, OUT), (waves_of<T, DK, ND, OUT>())) 
       if (!bad && a.S_out && seg == a.segs - 1) w.S.store(a.S_out + chain * state + (long)row * DK);
       __syncthreads();
     } else if (unit_rows) {
-      if (row < DK) w.S.store_transposed(a.moves + (chain * a.segs + seg) * DK * DK, row);
+      if (row < DK) w.S.store_moves(a.moves + (chain * a.segs + seg) * StateT<DK>::kMove, nullptr, row / 16);
     } else {
       w.S.store(a.starts + (chain * a.segs + seg + 1) * state + (long)row * DK);
     }
@@ -379,10 +378,10 @@ Plan plan_of(const DeltaArgs& a) {
   p.nd = a.dv >= 32 ? 2 : 1;
   if (a.dtype != 0 && a.dk == 128) p.nd = 1;
   // segments: walked twice, and the first time with dk unit rows more
-  cut(chunks, p.chains * ((a.dv + a.dk + 63) / 64), a.dk, p.segs, p.per);
+  cut(chunks, p.chains * ((a.dv + a.dk + 63) / 64), p.segs, p.per);
   p.T_bytes = (size_t)p.chains * chunks * kT * 16;
   p.starts = p.segs > 1 ? (size_t)p.chains * p.segs * a.dv * a.dk * 4 : 0;
-  p.moves = p.segs > 1 ? (size_t)p.chains * p.segs * a.dk * a.dk * 4 : 0;
+  p.moves = p.segs > 1 ? (size_t)p.chains * p.segs * move_bytes(a.dk) : 0;
   return p;
 }
 
@@ -404,7 +403,7 @@ template <typename T>
 hipError_t run(const DeltaArgs& a, const Plan& p, hipStream_t stream) {
   char* ws = static_cast<char*>(a.workspace);
   WalkArgs w{a.q, a.k, a.v, a.beta, a.log_a, reinterpret_cast<const uint4*>(ws), a.S0, a.o, a.S_out,
-             reinterpret_cast<float*>(ws + p.T_bytes), reinterpret_cast<float*>(ws + p.T_bytes + p.starts), p.chains, a.seqlen, a.dv, p.segs, p.per};
+             reinterpret_cast<float*>(ws + p.T_bytes), reinterpret_cast<uint4*>(ws + p.T_bytes + p.starts), p.chains, a.seqlen, a.dv, p.segs, p.per};
   const SolveArgs s{a.k, a.beta, a.log_a, static_cast<uint4*>(a.workspace), nullptr, p.chains, a.seqlen};
   const hipError_t e = launch_solve(s, a.dk, a.dtype, stream);
   if (e != hipSuccess) return e;

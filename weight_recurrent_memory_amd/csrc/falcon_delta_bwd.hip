@@ -59,8 +59,8 @@ struct BwdArgs {
   int segs, per;
   float* starts_S;
   float* starts_R;
-  float* moves;            // [chain][segs][dk][dk]: what a segment multiplies its start's rows with, transposed
-  float* moves_t;          // the same as it is, which is what R's rows are multiplied with, transposed
+  uint4* moves;            // [chain][segs][StateT::kMove]: what a segment multiplies its start's rows with
+  uint4* moves_t;          // the same for R
 };
 
 // ----------------------------------------------- P^T dO and dO^T (e Q)
@@ -338,8 +338,7 @@ __global__ __launch_bounds__(64 * (ND + kKeyWaves), 2) void walks_kernel(BwdArgs
     if (!WRITE) return;
     if (unit_rows) {
       if (row >= DK) return;
-      w.S.store_transposed(a.moves + unit * DK * DK, row);
-      w.S.store(a.moves_t + unit * DK * DK + at);
+      w.S.store_moves(a.moves + unit * StateT<DK>::kMove, a.moves_t + unit * StateT<DK>::kMove, row / 16);
     } else if (seg < a.segs - 1) {
       w.S.store(a.starts_S + (unit + 1) * state + at);
     }
@@ -742,9 +741,9 @@ Plan plan_of(const DeltaBwdArgs& a) {
   p.R = units * state;
   // segments: walked twice, and the first time with dk unit rows more
   const long walks = p.chains * (2 * ((a.ndv + 63) / 64) + (a.ndk + 63) / 64);
-  cut(p.chunks, walks, a.ndk, p.segs, p.per);
+  cut(p.chunks, walks, p.segs, p.per);
   p.starts = p.segs > 1 ? (size_t)p.chains * p.segs * state : 0;
-  p.moves = p.segs > 1 ? (size_t)p.chains * p.segs * a.ndk * a.ndk * 4 : 0;
+  p.moves = p.segs > 1 ? (size_t)p.chains * p.segs * move_bytes(a.ndk) : 0;
   return p;
 }
 
@@ -780,8 +779,8 @@ hipError_t run(const DeltaBwdArgs& a, const Plan& p, hipStream_t stream) {
   w.per = p.per;
   w.starts_S = reinterpret_cast<float*>(take(p.starts));
   w.starts_R = reinterpret_cast<float*>(take(p.starts));
-  w.moves = reinterpret_cast<float*>(take(p.moves));
-  w.moves_t = reinterpret_cast<float*>(take(p.moves));
+  w.moves = reinterpret_cast<uint4*>(take(p.moves));
+  w.moves_t = reinterpret_cast<uint4*>(take(p.moves));
   w.U = reinterpret_cast<float*>(take(p.U));
   const SolveArgs s{a.k, a.beta, a.log_a, T_, Tt, p.chains, a.seqlen};
   const hipError_t e = launch_solve(s, a.ndk, a.dtype, stream);

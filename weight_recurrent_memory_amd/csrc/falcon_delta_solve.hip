@@ -8,7 +8,7 @@
 //   [[X, 0], [C, Y]]^-1 = [[X^-1, 0], [-Y^-1 C X^-1, Y^-1]]
 // on matrix cores, float32 operands as three bf16 planes.  T is written as the walk's
 // operands (18 KB a chunk; the transposed ones for the gradients as much again).
-// 8x12x2048x64 bf16: 21 us for 3072 chunks, 81 MB read and written = 3.9 TB/s (32 us with the
+// 8x12x2048x64 bf16: 21 us for the 32 chunks of each chain, 81 MB read and written = 3.9 TB/s (32 us with the
 // transposed ones); one chunk alone takes 6.7 us.
 #include "falcon_delta.h"
 

@@ -77,17 +77,48 @@ struct StateT {
 #pragma unroll
     for (int j = 0; j < NK; ++j) *reinterpret_cast<floatx4*>(S + m * DK + 16 * j + 4 * g) = t[j];
   }
-  __device__ __forceinline__ void store_transposed(float* S, int row0) const {
-    const int m = threadIdx.x & 15, g = (threadIdx.x & 63) >> 4;
-#pragma unroll
-    for (int j = 0; j < NK; ++j)
-#pragma unroll
-      for (int r = 0; r < 4; ++r) S[(16 * j + 4 * g + r) * DK + row0 + m] = t[j][r];
-  }
   __device__ __forceinline__ void frag(int i, bf16x8 (&f)[3]) const {
     const floatx4 zero = {0.f, 0.f, 0.f, 0.f};
     if constexpr (DK == 16) frag_pair(t[0], zero, f);
     else frag_pair(t[2 * i], t[2 * i + 1], f);
+  }
+  // The 16 unit rows of tile w, walked, as a join's operands: `back`'s rows are these rows, `ahead`'s
+  // the columns (either may be null; kMove uint4 each).  A product with the unit matrix exchanges
+  // rows and columns of a tile; its three planes' sum is exact.
+  static constexpr int kMove = NK * NQ * 3 * 64;
+  __device__ __forceinline__ void store_moves(uint4* ahead, uint4* back, int w) const {
+    const int lane = threadIdx.x & 63, m = lane & 15, g = lane >> 4;
+    const floatx4 zero = {0.f, 0.f, 0.f, 0.f};
+    bf16x8 f[3];
+    if (back) {
+#pragma unroll
+      for (int i = 0; i < NQ; ++i) {
+        frag(i, f);
+#pragma unroll
+        for (int p = 0; p < 3; ++p) back[((w * NQ + i) * 3 + p) * 64 + lane] = __builtin_bit_cast(uint4, f[p]);
+      }
+    }
+    if (!ahead) return;
+    uint2 e;                             // bf16 1.0 where slot 4 g + i is column m
+    e.x = (4 * g == m ? 0x3F80u : 0u) | (4 * g + 1 == m ? 0x3F800000u : 0u);
+    e.y = (4 * g + 2 == m ? 0x3F80u : 0u) | (4 * g + 3 == m ? 0x3F800000u : 0u);
+    const bf16x8 unit_matrix = __builtin_bit_cast(bf16x8, uint4{e.x, e.y, 0u, 0u});
+#pragma unroll
+    for (int j = 0; j < NK; ++j) {
+      floatx4 x = zero;
+      frag_pair(t[j], zero, f);
+#pragma unroll
+      for (int p = 0; p < 3; ++p) x = mfma16(f[p], unit_matrix, x);
+      uint2 h[3];
+      split3(x.x, x.y, h[0].x, h[1].x, h[2].x);
+      split3(x.z, x.w, h[0].y, h[1].y, h[2].y);
+#pragma unroll
+      for (int p = 0; p < 3; ++p) {
+        uint4* to = ahead + ((j * NQ + w / 2) * 3 + p) * 64 + lane;
+        if (DK == 16) *to = uint4{h[p].x, h[p].y, 0u, 0u};
+        else reinterpret_cast<uint2*>(to)[w & 1] = h[p];
+      }
+    }
   }
   __device__ __forceinline__ bool finite() const {
     float s = 0.0f;
@@ -325,27 +356,34 @@ __device__ __forceinline__ void keys_only(KeyLds<T, DK>& lds, const T* k, const 
 // main walk then starts each segment from its state.  R -> R M^T + N' for the gradient's.
 
 // units: workgroups of the first launch over all chains for one segment each, of which the GPU
-// holds 256 (one a compute unit, a walker a SIMD); segments have two chunks at least.  Sequences of fewer
-// chunks than kWhole, and those whose chains alone take more than a quarter of the GPU, are walked
-// whole.  Measured, us of a call cut and whole, forward and gradients: 1x16x4096x64 66 and 137, 153 and
-// 235; 1x8x2048x64 45 and 76, 70 and 120; 1x3x3000x32 34 and 88, 52 and 125; 1x2x640x64 31 and 33, 51
-// and 58; 1x16x2048x128 86 and 113, 216 and 218; but 1x1x512x128 42 and 39, 79 and 75 (the joins at 128
-// columns take longest).  With 512 slots 1x16x4096x64 takes 76 and 163.
-constexpr long kWhole = 10, kWholeWide = 16, kSlots = 256;
-inline void cut(long chunks, long units, int dk, int& segs, int& per) {
+// holds 256 (one a compute unit, a walker a SIMD); segments have two chunks at least.  A chain is cut
+// where two walks of a segment are at least kGain chunks shorter than one of the whole, which is what
+// the two launches more cost.  Measured, us of a call cut and whole, forward and gradients:
+// 1x16x4096x64 66 and 137, 153 and 235; 1x8x2048x64 45 and 76, 70 and 120; 1x3x3000x32 34 and 88, 52
+// and 125; 1x20x2048x128 98 and 113; 1x12x4096x128 the gradients 292 and 364; 1x1x768x128 (8 chunks
+// shorter) 42 and 50, 81 and 88; 1x2x640x64 (6) 31 and 33, 51 and 58; but 1x27x704x64 (5) 40 and 38;
+// 1x4x512x128 (4) 40 and 39, 82 and 79; 1x20x1024x128 (4) 66 and 65; 1x20x640x128 (2) 56 and 48.
+// With 512 slots 1x16x4096x64 takes 76 and 163.
+constexpr long kGain = 6, kSlots = 256;
+inline void cut(long chunks, long units, int& segs, int& per) {
   segs = 1;
   per = (int)chunks;
-  if (chunks < (dk == 128 ? kWholeWide : kWhole) || units > kSlots / 4) return;
   long n = kSlots / units;
   if (n > chunks / 2) n = chunks / 2;
-  per = (int)((chunks + n - 1) / n);
-  segs = (int)((chunks + per - 1) / per);
+  if (n < 2) return;
+  const long each = (chunks + n - 1) / n;
+  if (chunks - 2 * each < kGain) return;
+  per = (int)each;
+  segs = (int)((chunks + each - 1) / each);
 }
+
+// Bytes of a segment's matrix as a join's operands (StateT::kMove).
+inline size_t move_bytes(int dk) { return (size_t)(dk / 16) * ((dk + 31) / 32) * 3 * 64 * 16; }
 
 struct Join {
   const float* S0;         // or null
   float* starts;           // [chain][segs][dv][dk]: slot j + 1 step j's own write, then slot j what step j starts from
-  const float* moves;      // [chain][segs][dk][dk], transposed
+  const uint4* moves;      // [chain][segs][StateT::kMove], planes (whose splitting took half of a join)
   bool reverse;            // the first step is the last segment
 };
 struct Joins {
@@ -369,8 +407,9 @@ __global__ __launch_bounds__(4 * DK) void join_kernel(Joins all) {
   const long state = (long)all.nv * DK, row = blk * 16 + m;
   const long at = row * DK + 16 * wave + 4 * g;
   float* starts = a.starts + chain * all.segs * state + at;
-  const float* moves = a.moves + (chain * all.segs + (a.reverse ? steps : 0)) * DK * DK + (16 * wave + m) * DK + 4 * g;
-  const long stride = a.reverse ? -(long)DK * DK : (long)DK * DK;
+  constexpr long kMove = StateT<DK>::kMove;
+  const uint4* moves = a.moves + (chain * all.segs + (a.reverse ? steps : 0)) * kMove + wave * NQ * 3 * 64 + lane;
+  const long stride = a.reverse ? -kMove : kMove;
   const floatx4 zero = {0.f, 0.f, 0.f, 0.f};
   floatx4 x = a.S0 ? *reinterpret_cast<const floatx4*>(a.S0 + chain * state + at) : zero;
   *reinterpret_cast<floatx4*>(starts) = x;
@@ -378,16 +417,16 @@ __global__ __launch_bounds__(4 * DK) void join_kernel(Joins all) {
     for (int i = threadIdx.x; i < 2 * 3 * 64; i += 64) (&s[0][0][0][0][0])[2 * i + 1] = uint2{0u, 0u};
   }
   struct Step {
-    floatx4 lo[NQ], hi[NQ], w;
+    uint4_t f[NQ][3];
+    floatx4 w;
   } ahead[2];
   auto fetch = [&](Step& o, int j) {
     if (j >= steps) j = steps - 1;       // (no branch: one would wait for what is on its way)
     o.w = *reinterpret_cast<const floatx4*>(starts + (j + 1) * state);
 #pragma unroll
-    for (int i = 0; i < NQ; ++i) {
-      o.lo[i] = *reinterpret_cast<const floatx4*>(moves + j * stride + 32 * i);
-      o.hi[i] = DK > 16 ? *reinterpret_cast<const floatx4*>(moves + j * stride + 32 * i + 16) : zero;
-    }
+    for (int i = 0; i < NQ; ++i)
+#pragma unroll
+      for (int p = 0; p < 3; ++p) o.f[i][p] = *reinterpret_cast<const uint4_t*>(moves + j * stride + (i * 3 + p) * 64);
   };
   auto step = [&](Step& o, int j, int buf) {
     uint2 h, mi, l;
@@ -399,7 +438,9 @@ __global__ __launch_bounds__(4 * DK) void join_kernel(Joins all) {
     to[2][lane][wave & 1] = l;
     bf16x8 f[NQ][3];
 #pragma unroll
-    for (int i = 0; i < NQ; ++i) frag_pair(o.lo[i], o.hi[i], f[i]);
+    for (int i = 0; i < NQ; ++i)
+#pragma unroll
+      for (int p = 0; p < 3; ++p) f[i][p] = __builtin_bit_cast(bf16x8, o.f[i][p]);
     x = o.w;
     fetch(o, j + 2);
     __syncthreads();
