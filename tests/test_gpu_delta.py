@@ -107,6 +107,20 @@ def test_long_sequences_of_few_heads(dtype, dk, dv, L):
     assert all(torch.equal(d[n], d2[n]) for n in d)
 
 
+@pytest.mark.parametrize("dtype", TYPES)
+@pytest.mark.parametrize("beta", ["mixed", "zero"])
+@pytest.mark.parametrize("H,dk,dv,L", [(1, 128, 128, 576), (1, 128, 128, 640), (1, 128, 64, 703), (20, 128, 128, 1100),
+                                       (3, 64, 64, 640), (27, 64, 64, 1000), (5, 32, 16, 641), (3, 16, 64, 1999)])
+def test_what_segments_hand_on(dtype, beta, H, dk, dv, L):
+    """No decay, half of the keys without a step: a segment's matrix is far from zero, and the
+    start's share reaches the last segments.  (A join adds one product a segment, up to 8u each of
+    what the decreasing starts hold; the roundings point either way, and the bounds hold twice the
+    rest.)"""
+    x = du.inputs(torch, 23, 1, H, L, dk, dv, dtype, gate="none", beta=beta)
+    _check_forward(x)
+    _check_backward(x)
+
+
 @pytest.mark.parametrize("L", [100, 1500])
 def test_state_in_place_and_given_outputs(L):
     x = du.inputs(torch, 10, 1, 2, L, 32, 32, torch.bfloat16)
