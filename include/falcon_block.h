@@ -43,7 +43,9 @@ extern "C" {
  * anything.  (A reset does not clear it: 0 * NaN.  float32 inputs and states beyond bf16's
  * 3.39e38 count as infinite.  Segments that hold one, or start
  * from one, are walked again token by token, which takes many times as long.)
- * batch * heads * max(dk, dv) * (L + 63) / 64 < 2^31 (FALCON_ERR_UNSUPPORTED from there on).
+ * FALCON_ERR_UNSUPPORTED from batch * heads * max(dk, dv) * (L + 63) / 64 = 2^31 on, and where a
+ * launch would have 2^32 work-items: 12 dv for each (batch, head), whose number counts as the next
+ * multiple of 8, or 64 for each 64-token chunk (four chunks together).
  *
  * falcon_gated_delta_bwd_chunk - gradients of sum <dO, o> + <dS_L, S_L>
  *   q, k, v, beta, log_a, S0, dtype   as the forward's
@@ -60,7 +62,8 @@ extern "C" {
  *   workspace  falcon_gated_delta_bwd_workspace_bytes(...) bytes, 16-byte aligned
  * Here a NaN or an infinity in a token also reaches gradients that do not depend on it, of its
  * 64-token chunk.  Rows of padding have to be finite.  Outputs and workspace overlap no other
- * argument.  Sizes as the forward's.
+ * argument.  Sizes as the forward's, with 512 work-items for each (batch, head) at dv = 32, 384 at
+ * dv = 16, and 256 for each 64-token chunk.
  *
  * falcon_gated_delta_decode_step - one token for serving: S [nseq, heads, dv, dk]
  * float32 updated in place, q, k [nseq, heads, dk], v [nseq, heads, dv], beta and log_a

@@ -107,6 +107,17 @@ int main() {
   expect("forward, size", forward({1 << 14, 1 << 10, 128}, 64, 64, FALCON_BF16, ~0ull >> 8), kNo);
   expect("backward, size", backward({1 << 14, 1 << 10, 128}, 64, 64, FALCON_BF16, ~0ull >> 8), kNo);
   expect("workspace, size", (long long)falcon_gated_delta_fwd_workspace_bytes(1 << 14, 1 << 10, 128, 64, 64, 0), 0);
+  // 2^32 work-items of a launch: one call below, one above
+  for (int dtype : {FALCON_BF16, FALCON_F32}) {
+    expect("forward, value rows", forward({349525, 8, 1}, 16, 128, dtype, ~0ull >> 2), kOk);
+    expect("forward, more value rows", forward({349526, 8, 1}, 16, 128, dtype, ~0ull >> 2), kNo);
+    expect("forward, chunks", forward({1, 4, (1 << 30) - 64}, 16, 16, dtype, ~0ull >> 2), kOk);
+    expect("forward, more chunks", forward({1, 4, (1 << 30) - 63}, 16, 16, dtype, ~0ull >> 2), kNo);
+    expect("backward, value rows", backward({1048575, 8, 1}, 16, 32, dtype, ~0ull >> 2), kOk);
+    expect("backward, more value rows", backward({1048576, 8, 1}, 16, 32, dtype, ~0ull >> 2), kNo);
+    expect("backward, chunks", backward({1, 16, (1 << 26) - 64}, 16, 16, dtype, ~0ull >> 2), kOk);
+    expect("backward, more chunks", backward({1, 16, (1 << 26) - 63}, 16, 16, dtype, ~0ull >> 2), kNo);
+  }
   std::printf("%d checks, %d failures\n", g_checks, g_failures);
   return g_failures ? 1 : 0;
 }

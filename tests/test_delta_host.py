@@ -87,6 +87,31 @@ def test_decode(lib, over, status):
     assert _call(lib.falcon_gated_delta_decode_step, DEC, over) == status
 
 
+# (batch, heads, L, dk, dv) just below 2^32 work-items of a launch, and just above: 12 for a value row of
+# each chain (8 chains side by side) and 64 for a chunk in the forward; in the gradients 16 and 24 for a
+# value row at dv of 32 and 16, and 256 for a chunk.
+FORWARD_LIMITS = [((349525, 8, 1, 16, 128), (349526, 8, 1, 16, 128)), ((699050, 8, 64, 16, 64), (699051, 8, 64, 16, 64)),
+                  ((2796202, 8, 1, 16, 16), (2796203, 8, 1, 16, 16)),
+                  ((1, 4, (1 << 30) - 64, 16, 16), (1, 4, (1 << 30) - 63, 16, 16))]
+BACKWARD_LIMITS = [((349525, 8, 1, 16, 128), (349526, 8, 1, 16, 128)), ((1048575, 8, 1, 16, 32), (1048576, 8, 1, 16, 32)),
+                   ((1398101, 8, 1, 16, 16), (1398102, 8, 1, 16, 16)),
+                   ((1, 15, 64 * 1118481, 16, 16), (1, 16, 64 * 1048576, 16, 16))]
+
+
+@pytest.mark.parametrize("dtype", [0, 1])
+@pytest.mark.parametrize("name,below,above", [("fwd", *x) for x in FORWARD_LIMITS] + [("bwd", *x) for x in BACKWARD_LIMITS])
+def test_work_items_of_a_launch(lib, name, below, above, dtype):
+    """A launch has fewer than 2^32 work-items: sizes beyond are unsupported, and not an error of the
+    launch."""
+    size = getattr(lib, "falcon_gated_delta_%s_workspace_bytes" % name)
+    assert size(*below, dtype) > 0 and size(*above, dtype) == 0
+    defaults = FWD if name == "fwd" else BWD
+    over = dict(zip(("batch", "heads", "seqlen", "dk", "dv"), above), dtype=dtype, wsb=1 << 62)
+    over.update({n: (i + 1) << 44 for i, n in enumerate(list(defaults)[6:-1])})
+    call = getattr(lib, "falcon_gated_delta_%s_chunk" % name)
+    assert _call(call, defaults, over) == UNSUPPORTED
+
+
 def test_workspace_sizes(lib):
     for f in (lib.falcon_gated_delta_fwd_workspace_bytes, lib.falcon_gated_delta_bwd_workspace_bytes):
         assert f(0, 1, 1, 64, 64, 0) == f(1, 1, 1, 48, 64, 0) == f(1, 1, 0, 64, 64, 0) == 0

@@ -8,9 +8,17 @@
 
 namespace {
 
-// Workgroups and records of a launch: counted in 32 bits.
+// Records and workgroups are counted in 31 bits, a launch's work-items in 32.
 bool delta_sizes(int batch, int heads, int seqlen, int dk, int dv) {
   return (double)batch * heads * (dk > dv ? dk : dv) * (((double)seqlen + 63.0) / 64.0) < 2147483648.0;
+}
+bool forward_sizes(int batch, int heads, int seqlen, int dk, int dv, int dtype) {
+  return supported_dim(dk) && supported_dim(dv) && delta_sizes(batch, heads, seqlen, dk, dv) &&
+         falcon::delta_fits(falcon::DeltaArgs{batch, heads, seqlen, dk, dv, dtype});
+}
+bool backward_sizes(int batch, int heads, int seqlen, int dk, int dv, int dtype) {
+  return supported_dim(dk) && supported_dim(dv) && delta_sizes(batch, heads, seqlen, dk, dv) &&
+         falcon::delta_bwd_fits(falcon::DeltaBwdArgs{batch, heads, seqlen, dk, dv, dtype});
 }
 
 }  // namespace
@@ -18,8 +26,8 @@ bool delta_sizes(int batch, int heads, int seqlen, int dk, int dv) {
 FALCON_EXPORT unsigned long long falcon_gated_delta_fwd_workspace_bytes(int batch, int heads, int seqlen,
                                                                         int dk, int dv, int dtype) {
   size_t N, es;
-  if (check_sizes(batch, heads, seqlen, dk, dv, dtype, &N, &es) != FALCON_OK || !supported_dim(dk) ||
-      !supported_dim(dv) || !delta_sizes(batch, heads, seqlen, dk, dv))
+  if (check_sizes(batch, heads, seqlen, dk, dv, dtype, &N, &es) != FALCON_OK ||
+      !forward_sizes(batch, heads, seqlen, dk, dv, dtype))
     return 0;
   falcon::DeltaArgs a{batch, heads, seqlen, dk, dv, dtype};
   return (unsigned long long)falcon::delta_workspace_bytes(a);
@@ -36,8 +44,7 @@ FALCON_EXPORT int falcon_gated_delta_fwd_chunk(int batch, int heads, int seqlen,
   if (!q || !k || !v || !beta || !o || !workspace) return FALCON_ERR_INVALID_ARG;
   const void* ptrs[] = {q, k, v, S0, o, S_out, workspace};
   if (!all_aligned16(ptrs) || !aligned4(beta) || !aligned4(log_a)) return FALCON_ERR_INVALID_ARG;
-  if (!supported_dim(dk) || !supported_dim(dv) || !delta_sizes(batch, heads, seqlen, dk, dv))
-    return FALCON_ERR_UNSUPPORTED;
+  if (!forward_sizes(batch, heads, seqlen, dk, dv, dtype)) return FALCON_ERR_UNSUPPORTED;
   const falcon::DeltaArgs a{batch, heads, seqlen, dk, dv, dtype, q, k, v, beta, log_a, S0, o, S_out, workspace};
   const size_t need = falcon::delta_workspace_bytes(a);
   if (workspace_bytes < need) return FALCON_ERR_INVALID_ARG;
@@ -54,8 +61,8 @@ FALCON_EXPORT int falcon_gated_delta_fwd_chunk(int batch, int heads, int seqlen,
 FALCON_EXPORT unsigned long long falcon_gated_delta_bwd_workspace_bytes(int batch, int heads, int seqlen,
                                                                         int dk, int dv, int dtype) {
   size_t N, es;
-  if (check_sizes(batch, heads, seqlen, dk, dv, dtype, &N, &es) != FALCON_OK || !supported_dim(dk) ||
-      !supported_dim(dv) || !delta_sizes(batch, heads, seqlen, dk, dv))
+  if (check_sizes(batch, heads, seqlen, dk, dv, dtype, &N, &es) != FALCON_OK ||
+      !backward_sizes(batch, heads, seqlen, dk, dv, dtype))
     return 0;
   falcon::DeltaBwdArgs a{batch, heads, seqlen, dk, dv, dtype};
   return (unsigned long long)falcon::delta_bwd_workspace_bytes(a);
@@ -76,8 +83,7 @@ FALCON_EXPORT int falcon_gated_delta_bwd_chunk(int batch, int heads, int seqlen,
   const void* ptrs[] = {q, k, v, S0, dO, dS_L, dq, dk_out, dv_out, dS0, workspace};
   if (!all_aligned16(ptrs) || !aligned4(beta) || !aligned4(log_a) || !aligned4(dbeta) || !aligned4(dlog_a))
     return FALCON_ERR_INVALID_ARG;
-  if (!supported_dim(dk) || !supported_dim(dv) || !delta_sizes(batch, heads, seqlen, dk, dv))
-    return FALCON_ERR_UNSUPPORTED;
+  if (!backward_sizes(batch, heads, seqlen, dk, dv, dtype)) return FALCON_ERR_UNSUPPORTED;
   const falcon::DeltaBwdArgs a{batch, heads, seqlen, dk, dv, dtype, q, k, v, beta, log_a, S0, dO, dS_L,
                                dq, dk_out, dv_out, dbeta, dlog_a, dS0, workspace};
   const size_t need = falcon::delta_bwd_workspace_bytes(a);

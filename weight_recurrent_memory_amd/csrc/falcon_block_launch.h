@@ -21,6 +21,8 @@ struct DeltaArgs {
 };
 // (sizes and type count)
 size_t delta_workspace_bytes(const DeltaArgs& a);
+// Whether every launch has fewer than 2^32 work-items, the most that HIP takes.
+bool delta_fits(const DeltaArgs& a);
 hipError_t launch_delta(const DeltaArgs& a, hipStream_t stream);
 struct DeltaBwdArgs {
   int batch, heads, seqlen, ndk, ndv;
@@ -42,6 +44,7 @@ struct DeltaBwdArgs {
   void* workspace;         // delta_bwd_workspace_bytes(...)
 };
 size_t delta_bwd_workspace_bytes(const DeltaBwdArgs& a);
+bool delta_bwd_fits(const DeltaBwdArgs& a);
 hipError_t launch_delta_bwd(const DeltaBwdArgs& a, hipStream_t stream);
 struct DeltaDecodeArgs {
   int nseq, heads, dk, dv;

@@ -163,6 +163,11 @@ hipError_t with_dim(int d, F&& f) {
   return hipErrorInvalidValue;
 }
 
+// Whether a launch of grid_of(blocks, units) workgroups has fewer than 2^32 work-items.
+inline bool fits(long blocks, long units, long threads) {
+  return (units + 7) / 8 * 8 * blocks * threads < (1l << 32);
+}
+
 struct SolveArgs {
   const void* k;             // [chain][L][dk]
   const float* beta;         // [chain][L]
@@ -172,7 +177,9 @@ struct SolveArgs {
   long chains;
   int seqlen;
 };
-// Every chunk's T (falcon_delta_solve.hip).
+// Every chunk's T (falcon_delta_solve.hip), four chunks a workgroup of 256.
+constexpr int kSolveWaves = 4;
+inline bool solve_fits(long chunks) { return (chunks + kSolveWaves - 1) / kSolveWaves * 64 * kSolveWaves < (1l << 32); }
 hipError_t launch_solve(const SolveArgs& a, int dk, int dtype, hipStream_t stream);
 
 }  // namespace delta

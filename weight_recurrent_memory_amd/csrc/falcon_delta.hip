@@ -370,6 +370,11 @@ struct Plan {
   long chains;
   size_t T_bytes, starts, moves;      // bytes
   size_t bytes() const { return T_bytes + starts + moves; }
+  // (a sequence is cut where the launches it takes more have some 256 workgroups)
+  bool fit(const DeltaArgs& a) const {
+    return solve_fits(chains * (((long)a.seqlen + C - 1) / C)) &&
+           fits(a.dv / (16 * nd), chains * segs, threads_of(nd, true));
+  }
 };
 Plan plan_of(const DeltaArgs& a) {
   Plan p;
@@ -431,6 +436,8 @@ hipError_t run(const DeltaArgs& a, const Plan& p, hipStream_t stream) {
 }  // namespace delta
 
 size_t delta_workspace_bytes(const DeltaArgs& a) { return delta::plan_of(a).bytes(); }
+
+bool delta_fits(const DeltaArgs& a) { return delta::plan_of(a).fit(a); }
 
 hipError_t launch_delta(const DeltaArgs& a, hipStream_t stream) {
   (void)hipGetLastError();

@@ -722,11 +722,20 @@ __global__ __launch_bounds__(256, (DK <= 64 ? 2 : 1)) void outputs_kernel(BwdArg
 
 // ------------------------------------------------------------------- plans
 
+constexpr int kChunkThreads = 256;      // of prep_kernel and outputs_kernel, a chunk a workgroup
+// Walkers of a workgroup.
+constexpr int walkers(int nv) { return nv >= 64 ? 4 : nv / 16; }
+
 struct Plan {
   long chains, chunks;
   int segs, per;
   size_t T, H, G, U, S, R, starts, moves;      // bytes
   size_t bytes() const { return 2 * T + H + G + U + S + R + 2 * starts + 2 * moves; }
+  // (a sequence is cut where the launches it takes more have some 256 workgroups)
+  bool fit(int nv) const {
+    return solve_fits(chains * chunks) && chains * chunks * kChunkThreads < (1l << 32) &&
+           fits(2 * (nv / (16 * walkers(nv))), chains * segs, 64 * (walkers(nv) + kKeyWaves));
+  }
 };
 Plan plan_of(const DeltaBwdArgs& a) {
   Plan p;
@@ -789,7 +798,7 @@ hipError_t run(const DeltaBwdArgs& a, const Plan& p, hipStream_t stream) {
   const unsigned units = (unsigned)(p.chains * p.chunks);
   return with_dim(a.ndk, [&](auto d) {
     constexpr int DK = decltype(d)::value;
-    hipError_t e = go(prep_kernel<T, DK>, units, 256, sizeof(PrepLds<T, DK>), stream, w, n);
+    hipError_t e = go(prep_kernel<T, DK>, units, kChunkThreads, sizeof(PrepLds<T, DK>), stream, w, n);
     if (e != hipSuccess) return e;
     auto walks = [&](auto nd) {
       constexpr int ND = decltype(nd)::value, threads = 64 * (ND + kKeyWaves);
@@ -805,12 +814,13 @@ hipError_t run(const DeltaBwdArgs& a, const Plan& p, hipStream_t stream) {
       return go(walks_kernel<T, DK, ND, false>, grid_of(2 * vblocks, p.chains * p.segs), threads,
                 sizeof(KeyLds<T, DK>), stream, w, n);
     };
-    e = a.ndv >= 64   ? walks(std::integral_constant<int, 4>())
-        : a.ndv == 32 ? walks(std::integral_constant<int, 2>())
-                      : walks(std::integral_constant<int, 1>());
+    const int nd = walkers(a.ndv);
+    e = nd == 4   ? walks(std::integral_constant<int, 4>())
+        : nd == 2 ? walks(std::integral_constant<int, 2>())
+                  : walks(std::integral_constant<int, 1>());
     if (e != hipSuccess) return e;
     static_assert(sizeof(OutLds<T, DK>) <= 163840, "LDS of a workgroup");
-    return go(outputs_kernel<T, DK>, units, 256, sizeof(OutLds<T, DK>), stream, w, n);
+    return go(outputs_kernel<T, DK>, units, kChunkThreads, sizeof(OutLds<T, DK>), stream, w, n);
   });
 }
 
@@ -818,6 +828,8 @@ hipError_t run(const DeltaBwdArgs& a, const Plan& p, hipStream_t stream) {
 }  // namespace delta
 
 size_t delta_bwd_workspace_bytes(const DeltaBwdArgs& a) { return delta::plan_of(a).bytes(); }
+
+bool delta_bwd_fits(const DeltaBwdArgs& a) { return delta::plan_of(a).fit(a.ndv); }
 
 hipError_t launch_delta_bwd(const DeltaBwdArgs& a, hipStream_t stream) {
   (void)hipGetLastError();

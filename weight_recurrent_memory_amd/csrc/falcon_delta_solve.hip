@@ -17,7 +17,6 @@ namespace delta {
 namespace {
 
 constexpr int kPitch = 68;          // floats of a row of T in LDS: 16-byte reads of 16 rows fall apart
-constexpr int kWaves = 4;
 constexpr int kDiag = 272;          // floats of a diagonal block: four blocks fall into different banks
 
 struct SolveLds {
@@ -51,11 +50,11 @@ __device__ __forceinline__ void cols_of_T(const float* t, int row0, int col0, bo
 }
 
 template <typename T, int DK>
-__global__ __launch_bounds__(64 * kWaves) void solve_kernel(SolveArgs a, int chunks) {
+__global__ __launch_bounds__(64 * kSolveWaves) void solve_kernel(SolveArgs a, int chunks) {
   constexpr int NP = planes<T>(), NQ = (DK + 31) / 32;
-  __shared__ SolveLds all[kWaves];
+  __shared__ SolveLds all[kSolveWaves];
   SolveLds& lds = all[wave_id()];
-  const long unit = (long)blockIdx.x * kWaves + wave_id();
+  const long unit = (long)blockIdx.x * kSolveWaves + wave_id();
   if (unit >= a.chains * chunks) return;
   const long chain = unit / chunks, t0 = (unit % chunks) * C, len = a.seqlen;
   const int lane = threadIdx.x & 63, m = lane & 15, g = lane >> 4;
@@ -198,8 +197,8 @@ hipError_t go(const SolveArgs& a, int dk, hipStream_t stream) {
   const int chunks = (int)(((long)a.seqlen + C - 1) / C);
   const long units = a.chains * chunks;
   return with_dim(dk, [&](auto d) {
-    hipLaunchKernelGGL((solve_kernel<T, decltype(d)::value>), dim3((unsigned)((units + kWaves - 1) / kWaves)),
-                       dim3(64 * kWaves), 0, stream, a, chunks);
+    hipLaunchKernelGGL((solve_kernel<T, decltype(d)::value>), dim3((unsigned)((units + kSolveWaves - 1) / kSolveWaves)),
+                       dim3(64 * kSolveWaves), 0, stream, a, chunks);
     return hipGetLastError();
   });
 }
