@@ -80,6 +80,73 @@ def gradients(torch, x, dS_L=True):
     return out
 
 
+C, SLOTS, GAIN, XCDS = 64, 256, 6, 8
+
+
+def write_blocks(rows):
+    """Workgroups of four waves for so many rows of a segment's own write and matrix."""
+    return -(-rows // 64)
+
+
+def _ahead(dk, f32):
+    return 2 if not f32 and dk <= 64 else 1
+
+
+def key_lds(dk, f32):
+    """LDS of a workgroup without outputs: a chunk's keys and gates, one or two ahead, and two T."""
+    return (_ahead(dk, f32) + 1) * ((3 if f32 else 1) * C * dk * 2 + 1552) + 16 + 2 * 18432
+
+
+def walk_lds(dk, f32, waves):
+    """The forward's main walk: S's and u's operands of two chunks in place of T."""
+    s, u = -(-dk // 32) * 3, 6 if dk == 128 else 4
+    return key_lds(dk, f32) - 2 * 18432 + 2 * waves * (s + u) * 1024
+
+
+def rounds(blocks, lds, segments):
+    """Rounds of a launch of so many workgroups a segment, a segment's on one XCD of 32 compute units."""
+    return -(-(-(-segments // XCDS) * blocks) // (SLOTS // XCDS * (2 if 2 * lds <= 163840 else 1)))
+
+
+def cut(chunks, chains, write, unwritten, walk, dk):
+    """Segments of a chain; write and walk: workgroups a segment and their LDS."""
+    n = min(SLOTS // (chains * write[0]), chunks // 2)
+    if n < 2:
+        return 1
+    each = -(-chunks // n)
+    n = -(-chunks // each)
+    first = rounds(*write, chains * (n - unwritten)) if dk < 128 else 1
+    if each * (first + rounds(*walk, chains * n)) + GAIN > chunks * rounds(*walk, chains):
+        return 1
+    return n
+
+
+def _segments(chains, segs, dk, dv):
+    return chains * segs * (dv * dk * 4 + dk // 16 * ((dk + 31) // 32) * 3 * 64 * 16) if segs > 1 else 0
+
+
+def forward_plan(chains, L, dk, dv, f32):
+    """(state waves of a workgroup of the main walk, segments of a chain, bytes of workspace)."""
+    chunks = -(-L // C)
+    waves = 1 if dv == 16 or (f32 and dk == 128) else 2
+    segs = cut(chunks, chains, (write_blocks(dv + dk), key_lds(dk, f32)), 1,
+               (dv // (16 * waves), walk_lds(dk, f32, waves)), dk)
+    return waves, segs, chains * chunks * 18432 + _segments(chains, segs, dk, dv)
+
+
+def backward_plan(chains, L, dk, dv, f32):
+    """(state waves of a workgroup of the main walks, segments of a chain, bytes of workspace)."""
+    chunks = -(-L // C)
+    waves, lds = min(dv // 16, 4), key_lds(dk, f32)
+    segs = cut(chunks, chains, (write_blocks(dv + dk) + write_blocks(dv), lds), 0, (2 * (dv // (16 * waves)), lds), dk)
+    chunk = 2 * 18432 + C * dv * 4 + 3 * dv * dk * 4
+    return waves, segs, chains * (chunks * chunk + L * dv * 4) + 2 * _segments(chains, segs, dk, dv)
+
+
+# (f32, dk, dv, chains, L): every size in both types, walked whole and cut
+PLAN_CASES = [(f32, dk, dv, 2, L) for f32 in (False, True) for dk in DIMS for dv in DIMS for L in (150, 1030)]
+
+
 def norm(x):
     return float(np.linalg.norm(np.asarray(x.detach().cpu(), dtype=np.float64)))
 

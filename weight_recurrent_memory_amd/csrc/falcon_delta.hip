@@ -252,15 +252,15 @@ constexpr int threads_of(int nd, bool out) { return 64 * (nd + (out ? out_waves(
 template <typename T, int DK, int ND, bool OUT>
 constexpr int waves_of() { return OUT && planes<T>() == 3 && DK == 128 ? 1 : 2; }
 
-// OUT: the main walk; else a segment's own write (blocks of value rows) and the matrix it
-// multiplies its start's rows with (blocks of unit rows behind them).
+// OUT: the main walk; else a segment's own write (value rows) and the matrix it multiplies its
+// start's rows with (unit rows behind them), 64 of these rows a workgroup.
 template <typename T, int DK, int ND, bool OUT>
 __global__ __launch_bounds__(threads_of(ND, OUT), (waves_of<T, DK, ND, OUT>())) void walk_kernel(WalkArgs a) {
   extern __shared__ __align__(16) unsigned char smem[];
   using L = typename std::conditional<OUT, WalkLds<T, DK, ND>, KeyLds<T, DK>>::type;
   constexpr int DZ = 16 * ND;
   L& lds = *reinterpret_cast<L*>(smem);
-  const int vblocks = a.nv / DZ, blocks = OUT ? vblocks : vblocks + (DK + DZ - 1) / DZ;
+  const int blocks = OUT ? a.nv / DZ : write_blocks(a.nv + DK);
   const int steps = OUT ? a.segs : a.segs - 1;
   int blk;
   long unit;
@@ -271,11 +271,13 @@ __global__ __launch_bounds__(threads_of(ND, OUT), (waves_of<T, DK, ND, OUT>())) 
   const int n = (int)(chunks - c0 < a.per ? chunks - c0 : a.per);
   const int wave = wave_id(), lane = threadIdx.x & 63;
   const long left = len - c0 * C;            // tokens from the segment's start on
-  const bool unit_rows = !OUT && blk >= vblocks;
-  const int row0 = (unit_rows ? blk - vblocks : blk) * DZ;
+  const int row0 = blk * DZ;
 
   if (wave < ND) {
-    const int row = row0 + 16 * wave;          // (unit rows behind the last one are zeros)
+    const int at = row0 + 16 * wave;
+    const bool unit_rows = !OUT && at >= a.nv;
+    const int row = unit_rows ? at - a.nv : at;
+    if (unit_rows && row >= DK) return idle(n);
     Walker<T, DK, typename std::conditional<OUT, RegT, LdsT>::type> w;
     const T* v = static_cast<const T*>(a.v) + (chain * len + c0 * C) * a.nv;
     const uint4* Tp = a.T + (chain * chunks + c0) * kT;
@@ -332,7 +334,7 @@ __global__ __launch_bounds__(threads_of(ND, OUT), (waves_of<T, DK, ND, OUT>())) 
       if (!bad && a.S_out && seg == a.segs - 1) w.S.store(a.S_out + chain * state + (long)row * DK);
       __syncthreads();
     } else if (unit_rows) {
-      if (row < DK) w.S.store_moves(a.moves + (chain * a.segs + seg) * StateT<DK>::kMove, nullptr, row / 16);
+      w.S.store_moves(a.moves + (chain * a.segs + seg) * StateT<DK>::kMove, nullptr, row / 16);
     } else {
       w.S.store(a.starts + (chain * a.segs + seg + 1) * state + (long)row * DK);
     }
@@ -376,14 +378,29 @@ struct Plan {
            fits(a.dv / (16 * nd), chains * segs, threads_of(nd, true));
   }
 };
+// The segments' first launch and the main walk.
+template <typename T, int DK>
+void launches(int nd, int nv, Launch& write, Launch& walk) {
+  write = {write_blocks(nv + DK), held(sizeof(KeyLds<T, DK>))};
+  walk = {nv / (16 * nd), held(nd == 2 ? sizeof(WalkLds<T, DK, 2>) : sizeof(WalkLds<T, DK, 1>))};
+}
+template <typename T>
+void launches(int dk, int nd, int nv, Launch& write, Launch& walk) {
+  if (dk == 16) launches<T, 16>(nd, nv, write, walk);
+  else if (dk == 32) launches<T, 32>(nd, nv, write, walk);
+  else if (dk == 64) launches<T, 64>(nd, nv, write, walk);
+  else launches<T, 128>(nd, nv, write, walk);
+}
 Plan plan_of(const DeltaArgs& a) {
   Plan p;
   p.chains = (long)a.batch * a.heads;
   const long chunks = ((long)a.seqlen + C - 1) / C;
   p.nd = a.dv >= 32 ? 2 : 1;
   if (a.dtype != 0 && a.dk == 128) p.nd = 1;
-  // segments: walked twice, and the first time with dk unit rows more
-  cut(chunks, p.chains * ((a.dv + a.dk + 63) / 64), p.segs, p.per);
+  Launch write, walk;
+  if (a.dtype == 0) launches<uint16_t>(a.dk, p.nd, a.dv, write, walk);
+  else launches<float>(a.dk, p.nd, a.dv, write, walk);
+  cut(chunks, p.chains, write, 1, walk, a.dk, p.segs, p.per);
   p.T_bytes = (size_t)p.chains * chunks * kT * 16;
   p.starts = p.segs > 1 ? (size_t)p.chains * p.segs * a.dv * a.dk * 4 : 0;
   p.moves = p.segs > 1 ? (size_t)p.chains * p.segs * move_bytes(a.dk) : 0;
@@ -397,8 +414,7 @@ hipError_t go(const WalkArgs& a, hipStream_t stream) {
   auto kernel = walk_kernel<T, DK, ND, OUT>;
   const hipError_t e = lds_limit(kernel, bytes);
   if (e != hipSuccess) return e;
-  constexpr int DZ = 16 * ND;
-  const int blocks = OUT ? a.nv / DZ : a.nv / DZ + (DK + DZ - 1) / DZ;
+  const int blocks = OUT ? a.nv / (16 * ND) : write_blocks(a.nv + DK);
   hipLaunchKernelGGL(kernel, dim3(grid_of(blocks, a.chains * (OUT ? a.segs : a.segs - 1))), dim3(threads_of(ND, OUT)), bytes,
                      stream, a);
   return hipGetLastError();
@@ -417,8 +433,7 @@ hipError_t run(const DeltaArgs& a, const Plan& p, hipStream_t stream) {
     auto walk = [&](auto nd) {
       constexpr int ND = decltype(nd)::value;
       if (p.segs > 1) {
-        // (a state wave for each SIMD of a compute unit)
-        hipError_t e = a.dv >= 64 ? go<T, DK, 4, false>(w, stream) : go<T, DK, ND, false>(w, stream);
+        hipError_t e = go<T, DK, kWriters, false>(w, stream);
         if (e != hipSuccess) return e;
         const Joins j{{{a.S0, w.starts, w.moves, false}, {}}, p.chains, a.dv, p.segs};
         if ((e = launch_join<DK>(j, 1, stream)) != hipSuccess) return e;

@@ -279,22 +279,21 @@ __device__ __forceinline__ void store_values(const float* p, int nv, int col, lo
 }
 
 // ND walkers of one segment; the first blocks walk forward, as many more backward.  WRITE: each
-// segment's own write from zero, and behind them unit rows, which give the matrix that a segment
-// multiplies its start's rows with.
+// segment's own write from zero, and forward, behind the value rows, unit rows, which give the matrix
+// that a segment multiplies its start's rows with.
 template <typename T, int DK, int ND, bool WRITE>
 __global__ __launch_bounds__(64 * (ND + kKeyWaves), 2) void walks_kernel(BwdArgs a, int chunks) {
   extern __shared__ __align__(16) unsigned char smem[];
   using L = KeyLds<T, DK>;
   constexpr int DZ = 16 * ND, NK = DK / 16;
   L& lds = *reinterpret_cast<L*>(smem);
-  const int vblocks = a.nv / DZ;
+  const int ahead = WRITE ? write_blocks(a.nv + DK) : a.nv / DZ;
   int blk;
   long unit;
-  if (!place(2 * vblocks + (WRITE ? (DK + DZ - 1) / DZ : 0), a.chains * a.segs, blk, unit)) return;
+  if (!place(ahead + (WRITE ? write_blocks(a.nv) : a.nv / DZ), a.chains * a.segs, blk, unit)) return;
   const long chain = unit / a.segs;
   const int seg = (int)(unit % a.segs);
-  const bool unit_rows = WRITE && blk >= 2 * vblocks, back = !unit_rows && blk >= vblocks;
-  const int row0 = (blk - (unit_rows ? 2 * vblocks : back ? vblocks : 0)) * DZ;
+  const bool back = blk >= ahead;
   const int wave = wave_id();
   const long c0 = (long)seg * a.per, first = chain * a.seqlen + c0 * C, left = a.seqlen - c0 * C;
   const int n = chunks - c0 < a.per ? (int)(chunks - c0) : a.per;
@@ -305,7 +304,10 @@ __global__ __launch_bounds__(64 * (ND + kKeyWaves), 2) void walks_kernel(BwdArgs
     else keys_only<T, DK, false>(lds, k, la, a.beta + first, a.T + (chain * chunks + c0) * kT, left, n, threadIdx.x - 64 * ND);
     return;
   }
-  const int row = row0 + 16 * wave;            // (unit rows behind the last one are zeros)
+  const int from = (back ? blk - ahead : blk) * DZ + 16 * wave;
+  const bool unit_rows = WRITE && !back && from >= a.nv;
+  const int row = unit_rows ? from - a.nv : from;
+  if (WRITE && row >= (unit_rows ? DK : a.nv)) return idle(n);
   const long state = (long)a.nv * DK, at = (long)row * DK;
   if (!back) {
     Walker<T, DK, LdsT> w;
@@ -337,7 +339,6 @@ __global__ __launch_bounds__(64 * (ND + kKeyWaves), 2) void walks_kernel(BwdArgs
     __syncthreads();
     if (!WRITE) return;
     if (unit_rows) {
-      if (row >= DK) return;
       w.S.store_moves(a.moves + unit * StateT<DK>::kMove, a.moves_t + unit * StateT<DK>::kMove, row / 16);
     } else if (seg < a.segs - 1) {
       w.S.store(a.starts_S + (unit + 1) * state + at);
@@ -737,6 +738,12 @@ struct Plan {
            fits(2 * (nv / (16 * walkers(nv))), chains * segs, 64 * (walkers(nv) + kKeyWaves));
   }
 };
+// Walkers' workgroups that a compute unit holds.
+template <typename T>
+int held_of(int dk) {
+  return held(dk == 16 ? sizeof(KeyLds<T, 16>) : dk == 32 ? sizeof(KeyLds<T, 32>)
+              : dk == 64 ? sizeof(KeyLds<T, 64>) : sizeof(KeyLds<T, 128>));
+}
 Plan plan_of(const DeltaBwdArgs& a) {
   Plan p;
   p.chains = (long)a.batch * a.heads;
@@ -748,9 +755,10 @@ Plan plan_of(const DeltaBwdArgs& a) {
   p.U = (size_t)p.chains * a.seqlen * a.ndv * 4;
   p.S = units * state;
   p.R = units * state;
-  // segments: walked twice, and the first time with dk unit rows more
-  const long walks = p.chains * (2 * ((a.ndv + 63) / 64) + (a.ndk + 63) / 64);
-  cut(p.chunks, walks, p.segs, p.per);
+  const int room = a.dtype == 0 ? held_of<uint16_t>(a.ndk) : held_of<float>(a.ndk);
+  const Launch write{write_blocks(a.ndv + a.ndk) + write_blocks(a.ndv), room};
+  const Launch walk{2 * (a.ndv / (16 * walkers(a.ndv))), room};
+  cut(p.chunks, p.chains, write, 0, walk, a.ndk, p.segs, p.per);
   p.starts = p.segs > 1 ? (size_t)p.chains * p.segs * state : 0;
   p.moves = p.segs > 1 ? (size_t)p.chains * p.segs * move_bytes(a.ndk) : 0;
   return p;
@@ -801,18 +809,18 @@ hipError_t run(const DeltaBwdArgs& a, const Plan& p, hipStream_t stream) {
     hipError_t e = go(prep_kernel<T, DK>, units, kChunkThreads, sizeof(PrepLds<T, DK>), stream, w, n);
     if (e != hipSuccess) return e;
     auto walks = [&](auto nd) {
-      constexpr int ND = decltype(nd)::value, threads = 64 * (ND + kKeyWaves);
-      const int vblocks = a.ndv / (16 * ND), ublocks = (DK + 16 * ND - 1) / (16 * ND);
+      constexpr int ND = decltype(nd)::value;
       if (p.segs > 1) {
-        hipError_t e = go(walks_kernel<T, DK, ND, true>, grid_of(2 * vblocks + ublocks, p.chains * p.segs), threads,
-                          sizeof(KeyLds<T, DK>), stream, w, n);
+        const int blocks = write_blocks(a.ndv + DK) + write_blocks(a.ndv);
+        hipError_t e = go(walks_kernel<T, DK, kWriters, true>, grid_of(blocks, p.chains * p.segs),
+                          64 * (kWriters + kKeyWaves), sizeof(KeyLds<T, DK>), stream, w, n);
         if (e != hipSuccess) return e;
         const Joins j{{{a.S0, w.starts_S, w.moves, false}, {a.dS_L, w.starts_R, w.moves_t, true}},
                       p.chains, a.ndv, p.segs};
         if ((e = launch_join<DK>(j, 2, stream)) != hipSuccess) return e;
       }
-      return go(walks_kernel<T, DK, ND, false>, grid_of(2 * vblocks, p.chains * p.segs), threads,
-                sizeof(KeyLds<T, DK>), stream, w, n);
+      return go(walks_kernel<T, DK, ND, false>, grid_of(2 * (a.ndv / (16 * ND)), p.chains * p.segs),
+                64 * (ND + kKeyWaves), sizeof(KeyLds<T, DK>), stream, w, n);
     };
     const int nd = walkers(a.ndv);
     e = nd == 4   ? walks(std::integral_constant<int, 4>())

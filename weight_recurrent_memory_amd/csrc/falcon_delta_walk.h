@@ -355,26 +355,54 @@ __device__ __forceinline__ void keys_only(KeyLds<T, DK>& lds, const T* k, const 
 // walks every segment from zero (N) and from unit rows (M), a second joins them in order, the
 // main walk then starts each segment from its state.  R -> R M^T + N' for the gradient's.
 
-// units: workgroups of the first launch over all chains for one segment each, of which the GPU
-// holds 256 (one a compute unit, a walker a SIMD); segments have two chunks at least.  A chain is cut
-// where two walks of a segment are at least kGain chunks shorter than one of the whole, which is what
+// State waves of the first launch's workgroups, one for each SIMD of a compute unit whatever dv
+// is, and its workgroups for so many value and unit rows of a segment.
+constexpr int kWriters = 4;
+__host__ __device__ constexpr int write_blocks(int rows) { return (rows + 16 * kWriters - 1) / (16 * kWriters); }
+
+// A launch's workgroups for one segment, which lie on one of the GPU's 8 XCDs (place), of 32 compute
+// units, and how many of them a compute unit holds (by LDS).
+struct Launch {
+  int blocks, held;
+};
+constexpr int held(size_t lds) { return lds <= 163840 / 2 ? 2 : 1; }
+inline long rounds(const Launch& l, long segments) {
+  const long all = (segments + 7) / 8 * l.blocks, room = 32 * l.held;
+  return (all + room - 1) / room;
+}
+
+// Segments of two chunks at least, 256 workgroups of the first launch aimed at (one a compute unit, a
+// walker a SIMD; `unwritten` segments of a chain are not in it).  A chain is cut where two walks of a
+// segment, each in its rounds, are at least kGain chunks shorter than one of the whole, which is what
 // the two launches more cost.  Measured, us of a call cut and whole, forward and gradients:
 // 1x16x4096x64 66 and 137, 153 and 235; 1x8x2048x64 45 and 76, 70 and 120; 1x3x3000x32 34 and 88, 52
 // and 125; 1x20x2048x128 98 and 113; 1x12x4096x128 the gradients 292 and 364; 1x1x768x128 (8 chunks
 // shorter) 42 and 50, 81 and 88; 1x2x640x64 (6) 31 and 33, 51 and 58; but 1x27x704x64 (5) 40 and 38;
 // 1x4x512x128 (4) 40 and 39, 82 and 79; 1x20x1024x128 (4) 66 and 65; 1x20x640x128 (2) 56 and 48.
-// With 512 slots 1x16x4096x64 takes 76 and 163.
+// With 512 slots 1x16x4096x64 takes 76 and 163.  Narrow values: 1x9x4096, 128x16 81 and 186, 141 and
+// 218; 1x28x4096, 128x32 fp32 237 and 308.  Two rounds, fp32: of the main walk 1x20x2048x128 184 and
+// 160; of the first launch 1x28x4096, 64x16 the gradients 259 and 245, 64x32 286 and 269.  At 128 columns
+// a second round of the first launch, which stores no states, takes 4.0 us a chunk against 6.0 of the
+// main walk's, and is not counted: 1x14x4096x128 the gradients 522 and 551.
 constexpr long kGain = 6, kSlots = 256;
-inline void cut(long chunks, long units, int& segs, int& per) {
+inline void cut(long chunks, long chains, const Launch& write, int unwritten, const Launch& walk, int dk, int& segs,
+                int& per) {
   segs = 1;
   per = (int)chunks;
-  long n = kSlots / units;
+  long n = kSlots / (chains * write.blocks);
   if (n > chunks / 2) n = chunks / 2;
   if (n < 2) return;
   const long each = (chunks + n - 1) / n;
-  if (chunks - 2 * each < kGain) return;
+  n = (chunks + each - 1) / each;
+  const long first = dk < 128 ? rounds(write, chains * (n - unwritten)) : 1;
+  if (each * (first + rounds(walk, chains * n)) + kGain > chunks * rounds(walk, chains)) return;
   per = (int)each;
-  segs = (int)((chunks + each - 1) / each);
+  segs = (int)n;
+}
+
+// A wave behind the last of these rows: the walkers' barriers.
+__device__ __forceinline__ void idle(int chunks) {
+  for (int c = 0; c <= chunks; ++c) __syncthreads();
 }
 
 // Bytes of a segment's matrix as a join's operands (StateT::kMove).
