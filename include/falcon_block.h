@@ -22,9 +22,11 @@ extern "C" {
  * squared-error step with a decay of its own in place of 1 - eta lambda, the same step's
  * key, and a step size that is not divided by the key's energy.
  *   beta     [batch, heads, L] float32, finite
- *   log_a    [batch, heads, L] float32, or NULL (a = 1).  A log decay below -1000 counts
- *            as -1000.  A token whose decay is 0 in float32 (-inf, and any log decay below
- *            about -104) is a reset: a new sequence starts at it.
+ *   log_a    [batch, heads, L] float32, or NULL (a = 1).  A token whose decay is below 2^-126, the
+ *            smallest normal float32 (-inf, and any log decay below about -87.34), is a reset: its
+ *            decay counts as 0, and a new sequence starts at it.  (In _fwd_chunk and _bwd_chunk a
+ *            product of several tokens' decays counts as 0 below 2^-126, too, and is off by up to
+ *            2^-134: below 2^-110 it keeps fewer bits than a float32.)
  * (beta, log_a, dbeta, dlog_a 4-byte aligned, every other pointer 16)
  *
  * falcon_gated_delta_fwd_chunk - a sequence, in chunks of 64 tokens

@@ -9,7 +9,7 @@
 // stays in the Infinity Cache between steps; a copy of 1 GiB moves 5.1 to 5.25 TB/s);
 // 1 x 12 x 128 x 128: 3.0 us, a launch's latency (9.3 us a call with the binding's host time).
 #include "falcon_block_launch.h"
-#include "falcon_device.h"
+#include "falcon_gated.h"
 
 namespace falcon {
 namespace {
@@ -38,7 +38,8 @@ __global__ __launch_bounds__(kRows * DK / 4) void delta_decode_kernel(DeltaDecod
     qq[e] = ld_in(q, head * DK + c0 + e);
   }
   const float vv = ld_in(v, head * a.dv + row), b = a.beta[head];
-  const float dec = a.log_a ? expf(a.log_a[head]) : 1.0f;
+  // (what counts as a reset is the sequence form's rule)
+  const float la = a.log_a ? a.log_a[head] : 0.0f, dec = gated::is_reset(la) ? 0.0f : expf(la);
   const float sk = group_sum<TPR>(s.x * kk[0] + s.y * kk[1] + s.z * kk[2] + s.w * kk[3]);
   const float u = b * (vv - dec * sk);
   floatx4 n;
