@@ -101,7 +101,8 @@ int falcon_gated_delta_decode_step(int nseq, int heads, int dk, int dv, int dtyp
  * the columns from rot on pass, v = v_in.
  *   q_in, k_in, v_in   token-major with strides, as falcon_norm_in
  *   positions          [batch, L] 64-bit integers, |position| < 2^53
- *   freqs              [rot / 2] float64, radians a token; angles are reduced in float64
+ *   freqs              [rot / 2] float64, radians a token; angles are reduced to float32
+ *                      rounding at every position
  *   rot                even, 2 <= rot <= dk
  *   pairs              FALCON_PAIRS_HALF (columns i and i + rot / 2) or
  *                      FALCON_PAIRS_NEIGHBOURS (2 i and 2 i + 1)

@@ -7,8 +7,9 @@
 //                  dx = r (dy - y (y . dy)),  y = r x,  r = 1 / sqrt(|x|^2 + eps)
 //
 // Bound by HBM like the norms.  A position times a frequency passes 2^24 radians in a long
-// document and keeps no fraction in float32: angles are formed in float64, as turns, and
-// reduced there; the fraction of a turn then goes to sincospi in float32.  A workgroup
+// document and keeps no fraction in float32: angles are formed in two float64, as turns, and
+// reduced there (in one, an angle at 2^53 is off by a radian); the fraction of a turn then goes to
+// sincospi in float32.  A workgroup
 // forms them once per token of its tile, in LDS, for all heads; its first rows are on their way
 // meanwhile.  Measured: 8x2048x12x64 bf16 33 us = 4.6 TB/s (norm_in, without the rotation, 26 us),
 // 1x8191x8x128 float32 36 us of kernel = 5.6 TB/s (rows not read ahead: 40), the gradient at
@@ -45,6 +46,17 @@ struct Angles {
   alignas(16) float sin[TT][D / 2];
 };
 
+// position * freq as a fraction of a turn, at most 1/2: products as a value and what rounding took
+// from it, 1 / (2 pi) to 106 bits, so good to 2^-52 of a turn up to 2^53 turns.
+__device__ __forceinline__ double turns_of(double position, double freq) {
+#pragma clang fp contract(off)
+  const double c = 0.15915494309189535, c_rest = -9.839338337591243e-18;
+  const double a = position * freq, a_rest = __builtin_fma(position, freq, -a);
+  const double t = a * c, t_rest = __builtin_fma(a, c, -t) + __builtin_fma(a, c_rest, a_rest * c);
+  const double x = (t - rint(t)) + t_rest;
+  return x - rint(x);
+}
+
 // cos and sin, scaled, of the tile's tokens and the rotation's pairs.
 template <int D, int TT>
 __device__ __forceinline__ void angles_of(Angles<D, TT>& a, const Rotation& r, long tile, long N) {
@@ -54,9 +66,7 @@ __device__ __forceinline__ void angles_of(Angles<D, TT>& a, const Rotation& r, l
     const long n = tile * TT + t;
     float s = 0.0f, c = 1.0f;
     if (n < N) {
-      double x = (double)r.positions[n] * r.freqs[p] * 0.15915494309189535;
-      x -= rint(x);
-      sincospif((float)(2.0 * x), &s, &c);
+      sincospif((float)(2.0 * turns_of((double)r.positions[n], r.freqs[p])), &s, &c);
     }
     a.cos[t][p] = r.scale * c;
     a.sin[t][p] = r.scale * s;
