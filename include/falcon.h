@@ -448,8 +448,9 @@ int falcon_norm_out_bwd(int batch, int heads, int seqlen, int dv, int dtype, con
  *   S_t = a_t S_{t-1} + v_t k_t^T,   a_t = exp(log_a_t),   o_t = S_t q_t
  *   log_a    [batch, heads, L] float32 (4-byte aligned, the other pointers 16), or
  *            NULL (a = 1).  A log decay below -1000 counts as -1000.  A token whose
- *            decay is 0 in float32 (-inf, and any log decay below about -104) is a
- *            reset: a new sequence starts at it.
+ *            decay is 0 is a reset: a new sequence starts at it.  (-inf, and in the chunk
+ *            calls any log decay below about -87.34, a decay below 2^-126; the decode step
+ *            keeps decays down to 2^-149, log decays of about -104.)
  *
  * falcon_gated_fwd_chunk - a sequence, in chunks of 64 tokens
  *   q, k, v, S0, o, S_out   as falcon_fwd_chunk (S0, S_out may be NULL; S_out may

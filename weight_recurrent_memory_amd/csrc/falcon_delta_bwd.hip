@@ -18,12 +18,12 @@
 // the walks, S and u from the first chunk on and R and du from the last one, side by side,
 // both by falcon_delta_walk.h's wave of 16 value rows; every chunk's outputs from S, R, u, du.
 //
-// 8x12x2048x64 bf16: 32 + 39 + 127 + 133 us of kernels, 314 us a call from GPU to GPU.  The walks
+// 8x12x2048x64 bf16: 32 + 40 + 127 to 132 + 133 to 140 us of kernels, 305 us a call.  The walks
 // write S, R, u and du (197 MB) and wait for each other's chunks; without these writes they would take
 // 84 us, and the outputs would have no states to start from.  The outputs read and write 460 MB
-// (3.5 TB/s) and issue 1500 vector and 336 matrix instructions a chunk and wave, two
+// (3.5 TB/s) and issue 2030 vector instructions a chunk and wave, 336 of them matrix ones, two
 // workgroups a compute unit.  Sequences of few chains in segments, as the forward's: 1x5x4099, 128x64
-// 12 + 11 + 23 + 29 + 26 + 40 us (walked whole 360 us).  Tried: stores past the caches (128 -> 136 us).
+// 12 + 11 + 24 + 19 + 26 + 40 us, 127 us a call (walked whole 266).  Tried: stores past the caches (128 -> 136 us).
 #include "falcon_delta_walk.h"
 
 namespace falcon {
@@ -684,6 +684,9 @@ __global__ __launch_bounds__(256, (DK <= 64 ? 2 : 1)) void outputs_kernel(BwdArg
     }
   }
   // dk = R^T u - b y, and the gates' gradients
+  // (a token's own sums in float32: q . dq is as wrong as dq, rounded in float32 accumulators; summed in
+  // float64, duv too, dlog_a's error goes from 5.7e-7 to 5.4e-7 at 8x12x2048x64 and the call takes up to
+  // 1.7% longer.  Sums over tokens are float64.)
   float qdq = 0.0f, yk = 0.0f;
 #pragma unroll
   for (int j = 0; j < NK; ++j) {

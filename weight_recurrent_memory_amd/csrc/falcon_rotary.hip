@@ -12,7 +12,8 @@
 // sincospi in float32.  A workgroup
 // forms them once per token of its tile, in LDS, for all heads; its first rows are on their way
 // meanwhile.  Measured: 8x2048x12x64 bf16 33 us = 4.6 TB/s (norm_in, without the rotation, 26 us),
-// 1x8191x8x128 float32 36 us of kernel = 5.6 TB/s (rows not read ahead: 40), the gradient at
+// 1x8191x8x128 float32 37 us = 5.4 TB/s over the outputs of the call before, which the Infinity Cache
+// still holds (rows not read ahead: 40), and 46 us into other memory; the gradient at
 // 4x1999x16x128 bf16 64 us = 5.7 TB/s (norm_in_bwd 60), 512 single tokens x 12 x 64 5.2 us.
 #include "falcon_block_launch.h"
 #include "falcon_rows.h"
